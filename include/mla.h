@@ -300,6 +300,102 @@ mla_status_t mla_attn_prefill(mla_handle_t *h, const void *q_c, const void *q_ro
                               int64_t max_seqlen, const void *cache, int64_t capacity, void *o,
                               mla_stream_t stream);
 
+/* ---- The paged latent cache -------------------------------------------------------------------
+ * The same cache rows in pages that need not lie next to each other: a pool [num_pages, page_size,
+ * d_c + d_r], a block table that names the page of every page_size positions of a sequence, and a
+ * batch of new tokens, the last ones of each sequence (one per sequence in a decode step, several
+ * in a chunk or a draft-and-verify step, none for a sequence that sits a step out).
+ *
+ * For new token t (packed by cu_q) of sequence b, with n_b = cu_q[b+1] - cu_q[b] new tokens:
+ *   position  pos = kv_lens[b] - n_b + (t - cu_q[b])
+ *   its row   page block_table[b][pos / page_size], row pos % page_size of it
+ * Pages may be shared by sequences for reading (a common prefix); an append into a page that another
+ * sequence's new tokens also write to the same rows of is a race. Table entries behind a sequence's
+ * last page are not read.
+ *
+ * cu_q[B] <= total_q: a padded batch is allowed, and rows of the outputs from cu_q[B] on are left as
+ * they were. B, total_q and the pointers are all that a launch depends on, so a captured call can be
+ * replayed after the contents of cu_q, kv_lens and block_table have changed.
+ *
+ * Device checks (MLA_ERR_DEVICE_CHECK through mla_sync_status): cu_q[0] = 0, cu_q non-decreasing,
+ * cu_q[B] <= total_q, n_b <= kv_lens[b] <= max_pages * page_size, pages in [0, num_pages). A token of
+ * an offending sequence is not appended, and its outputs are zero, with lse = -inf and no blocks; a
+ * page outside the pool is read as zero rows.
+ * The handle's cache format must be MLA_CACHE_BF16 (MLA_ERR_UNSUPPORTED otherwise); page_size is a
+ * multiple of 16, and num_pages * page_size < 2^31. A handle without weights serves these calls; its
+ * first call allocates the error word, so it must not be part of a stream capture. */
+typedef struct {
+  void *cache;                /* [num_pages, page_size, d_c + d_r] handle dtype, rows as elsewhere     */
+  int64_t num_pages;
+  int32_t page_size;
+  const int32_t *block_table; /* [B, max_pages] device int32, row b at block_table + b * table_stride  */
+  int64_t max_pages;
+  int64_t table_stride;       /* elements, >= max_pages                                                */
+  const int64_t *cu_q;        /* [B + 1] device int64: new tokens, packed                              */
+  const int64_t *kv_lens;     /* [B] device int64: cached rows INCLUDING the new tokens                */
+  int64_t B;
+  int64_t total_q;            /* rows of the per-token arrays, >= cu_q[B]                              */
+} mla_paged_t;
+
+/* Bytes of one summary row (mla_paged_append, mla_paged_select): d_c + d_r codes (int8), the fp32 scale
+ * right behind them, zeros up to a multiple of 16 (592 bytes at the DeepSeek-V3 sizes). Needs d_c + d_r
+ * to be a multiple of 4. Host-only arithmetic. */
+mla_status_t mla_paged_summary_bytes(const mla_handle_t *h, size_t *bytes);
+
+/* Appends the new tokens' rows to their pages, with the position rotation (section 一(一)3 step (7)) and the
+ * handle's opt-in RMSNorm (on c^KV) on the way: row = [c | R_pos k] of kv = [c | k]. With q_rope the
+ * tokens' decoupled queries are rotated in the same launch (step (3)).
+ *   kv         [total_q, d_c + d_r]  handle dtype, row t at kv + t * kv_stride (elements; a multiple
+ *                                    of 8 for bf16): the projections W^DKV h, W^KR h of the new
+ *                                    tokens, not rotated, not normalised
+ *   q_rope     [total_q, n_h, d_r]   handle dtype, not rotated; NULL: no queries
+ *   q_out      [total_q, n_h, d_r]   handle dtype, R_pos q; may be q_rope itself; NULL with q_rope
+ *   summaries  [num_pages] rows of mla_paged_summary_bytes(); NULL: none. For every page that the
+ *              new tokens complete (its last row is one of them), its summary: the mean of its rows
+ *              (sums in fp64, one rounding to fp32), x / scale rounded to the nearest whole number (ties
+ *              to even) in -127 .. 127, scale = max|x| / 127 (a row of scale 0, inf or NaN: all zero). */
+mla_status_t mla_paged_append(mla_handle_t *h, const mla_paged_t *batch, const void *kv, int64_t kv_stride,
+                              const void *q_rope, void *q_out, void *summaries, mla_stream_t stream);
+
+/* Attention of the new tokens over their sequences' pages, the absorbed form of step (10) as in
+ * mla_attn_decode_latent, for any number of new tokens per sequence: token t attends to rows 0 .. pos
+ * of its sequence (its own row included, so append first).
+ *   q_abs   [total_q, n_h, d_c]  handle dtype (q~ = W_i^UK^T q^C_i)
+ *   q_rope  [total_q, n_h, d_r]  handle dtype (rotated q^R)
+ *   o_lat   [total_q, n_h, d_c]  handle dtype, sum_j p_j c_j (what W^UV is multiplied with)
+ *   lse     [total_q, n_h]       fp32, natural log of sum_j exp(s_j)
+ * Rows past pos may hold anything (NaN included). ws: mla_attn_paged_workspace() bytes; calls that
+ * may overlap need workspaces of their own. */
+mla_status_t mla_attn_paged(mla_handle_t *h, const mla_paged_t *batch, const void *q_abs, const void *q_rope,
+                            void *o_lat, float *lse, void *ws, size_t ws_bytes, mla_stream_t stream);
+
+/* Workspace bytes of mla_attn_paged and mla_attn_paged_sparse. Host-only arithmetic. */
+mla_status_t mla_attn_paged_workspace(const mla_handle_t *h, int64_t B, int64_t total_q, size_t *bytes);
+
+/* Chooses the blocks (a block = the rows of one page) that each new token attends to, by a cheap score over
+ * the pages' summaries. A token at position pos sees n = pos / page_size + 1 blocks, its own the last. With
+ * n <= top_k it takes all of them; else the first n_first, the last n_last (its own among them, so blocks
+ * that are not whole yet need no summary) and, of the others, those of the largest score
+ *   score(t, g) = s_g * max_i s_i (x_i . y_g),  ties to the lowest block,
+ * where y_g, s_g are block g's summary and x_i, s_i the codes of [q~_i | q^R_i], taken as the summaries' are
+ * (the products are whole numbers below 2^24, then two fp32 multiplications: the choice does not depend on
+ * the order of any sum).
+ *   blocks  [total_q, top_k] int32: the blocks' numbers within the sequence, ascending, -1 behind the last
+ * n_first >= 0, n_last >= 1, n_first + n_last <= top_k <= 2^20, total_q <= 65535, d_c + d_r a multiple of 4.
+ * ws: mla_paged_select_workspace() bytes. */
+mla_status_t mla_paged_select(mla_handle_t *h, const mla_paged_t *batch, const void *q_abs, const void *q_rope,
+                              const void *summaries, int32_t top_k, int32_t n_first, int32_t n_last,
+                              int32_t *blocks, void *ws, size_t ws_bytes, mla_stream_t stream);
+mla_status_t mla_paged_select_workspace(const mla_handle_t *h, int64_t total_q, int64_t max_pages, size_t *bytes);
+
+/* mla_attn_paged over chosen blocks only: token t attends to the rows of blocks[t][0 .. top_k) that are at or
+ * before its position. A list ends at its first -1; a list that does not strictly ascend or passes the
+ * token's own block is flagged (MLA_ERR_DEVICE_CHECK) and its token's outputs are those of an empty list:
+ * o_lat = 0, lse = -inf. */
+mla_status_t mla_attn_paged_sparse(mla_handle_t *h, const mla_paged_t *batch, const void *q_abs,
+                                   const void *q_rope, const int32_t *blocks, int32_t top_k, void *o_lat,
+                                   float *lse, void *ws, size_t ws_bytes, mla_stream_t stream);
+
 /* Synchronizes the stream, then reports (and clears) the handle's device error word:
  * MLA_ERR_TIMEOUT, MLA_ERR_DEVICE_CHECK or MLA_OK. */
 mla_status_t mla_sync_status(mla_handle_t *h, mla_stream_t stream);

@@ -11,20 +11,9 @@
 
 #include "mla.h"
 #include "common.cuh"
+#include "handle.cuh"
 #include "simt.cuh"
 #include "tc.cuh"
-
-struct mla_handle {
-  mla_dims_t dims;
-  mla_dtype_t dtype;
-  int device;
-  mla_weights_t w;
-  bool has_weights;
-  uint32_t* d_err;         // device error word (sticky until mla_sync_status)
-  uint32_t last_err_bits;  // last word read by mla_sync_status
-  int num_sms;
-  mla::LayerOpts opts;     // RMSNorm gains and the RoPE (plain or YaRN)
-};
 
 namespace mla {
 static std::atomic<unsigned long long> g_launches{0};
@@ -57,38 +46,23 @@ void timer_end(TimedKernel k, cudaStream_t st) {
 
 namespace {
 
+using mla::DeviceGuard;
 using mla::SimtAttnArgs;
 using mla::SimtGemmArgs;
+using mla::aligned16;
+using mla::cuda_status;
+using mla::elem_size;
+using mla::ensure_device;
+using mla::tc_dims;
 
 constexpr size_t kAlign = 1024;
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-size_t elem_size(const mla_handle* h) { return h->dtype == MLA_BF16 ? 2 : 4; }
-
 // The sizes the tcgen05/TMA kernels are built for: the DeepSeek-V3 head layout, d and d_c'
 // multiples of 64. BF16 handles exist only at these sizes (mla_create).
 bool v3_dims(const mla_dims_t& d) {
   return d.n_h == 128 && d.d_h == 128 && d.d_c == 512 && d.d_r == 64 && d.d_cq % 64 == 0 && d.d % 64 == 0;
 }
-
-// BF16 handles run on the tcgen05/TMA kernels; FP32 handles on the generic CUDA-core kernels.
-bool tc_dims(const mla_handle* h) { return h->dtype == MLA_BF16; }
-
-// Makes the handle's device current for the life of the guard and restores the caller's device
-// afterwards, so that no entry point changes the calling thread's current device.
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = false;
-  explicit DeviceGuard(int device) {
-    if (cudaGetDevice(&prev) != cudaSuccess) return;
-    ok = prev == device || cudaSetDevice(device) == cudaSuccess;
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-  }
-};
 
 struct Layout {
   size_t off[9];
@@ -153,26 +127,6 @@ Layout layout(const mla_handle* h, mla_op_t op, int64_t B, int32_t tq, int64_t t
   }
   L.total = cur;
   return L;
-}
-
-mla_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA; }
-
-#define MLA_TRY(expr)                              \
-  do {                                             \
-    cudaError_t _e = (expr);                       \
-    if (_e != cudaSuccess) return MLA_ERR_CUDA;    \
-  } while (0)
-
-// Allocates the handle's error word on first use. The caller holds a DeviceGuard for h->device.
-mla_status_t ensure_device(mla_handle* h) {
-  if (!h->d_err) {
-    MLA_TRY(cudaMalloc(&h->d_err, sizeof(uint32_t)));
-    MLA_TRY(cudaMemset(h->d_err, 0, sizeof(uint32_t)));
-    int sms = 0;
-    MLA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, h->device));
-    h->num_sms = sms;
-  }
-  return MLA_OK;
 }
 
 // --- generic (CUDA-core) building blocks ----------------------------------------------------
@@ -305,6 +259,7 @@ mla_status_t mla_create(const mla_dims_t* dims, mla_dtype_t dtype, int device, m
   h->device = device;
   h->opts.eps = 1e-6f;
   h->opts.rope = mla::RopeSpec{d.rope_base, 1.0, 1.0, 32.0, 4096.0};
+  mla::fill_theta(h);
   *out = h;
   return MLA_OK;
 }
@@ -339,6 +294,7 @@ mla_status_t mla_cache_quantize_fp8(mla_handle_t* h, const void* rows, int64_t n
 mla_status_t mla_set_yarn(mla_handle_t* h, double s, double alpha, double beta, double original_len) {
   if (!h || !(s >= 1.0) || !(beta > alpha) || !(original_len > 0.0)) return MLA_ERR_INVALID_ARG;
   h->opts.rope = mla::RopeSpec{h->dims.rope_base, s, alpha, beta, original_len};
+  mla::fill_theta(h);
   return MLA_OK;
 }
 

@@ -16,6 +16,8 @@ enum : uint32_t {
   DEVERR_SEQ_TOO_LONG = 1u << 4,  // a prefill sequence (or chunk) longer than max_seqlen (max_q)
   DEVERR_TOTAL = 1u << 5,         // cu_seqlens[B] differs from the token count given on the host
   DEVERR_TIMEOUT = 1u << 6,       // a bounded mbarrier wait gave up
+  DEVERR_PAGE = 1u << 7,          // a page outside the cache, or a sequence longer than its block table
+  DEVERR_BLOCKS = 1u << 8,        // a list of blocks that does not ascend or passes its token's block
 };
 
 // Host-side count of kernels this library has launched (mla_kernel_launches()).
@@ -45,6 +47,13 @@ __host__ __device__ inline double rope_theta(const RopeSpec& r, int m, int d_r) 
 __host__ __device__ inline float rope_mul(const RopeSpec& r) {
   return r.yarn_s > 1.0 ? (float)(0.1 * log(r.yarn_s) + 1.0) : 1.0f;
 }
+
+// Frequencies theta_m and the factor on each rotated vector, by value in kernel arguments.
+constexpr int kRopeTablePairs = 64;
+struct RopeTable {
+  double theta[kRopeTablePairs];
+  float mul;
+};
 
 // Opt-in parts of a layer: the RMSNorm after the latent compression (section 三(二)1 of the notes:
 // c^Q = RMSNorm(W^DQ h), c^KV = RMSNorm(W^DKV h), y = x / sqrt(mean(x^2) + eps) * g) and the RoPE.

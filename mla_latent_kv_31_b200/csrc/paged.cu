@@ -1,0 +1,397 @@
+// Kernels of the paged latent cache that need no matrix unit: the append with the position rotation on the
+// way, the pages' summaries, the choice of blocks, and the attention of the fp32 configuration.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "paged.cuh"
+
+namespace mla {
+namespace {
+
+__device__ __forceinline__ void rope_angle(const RopeTable& rt, const LayerOpts& o, int64_t pos, int m, int d_r,
+                                           float* c, float* s) {
+  // the angle in double: a position of 2^17 turns the first pair by 2^17 radians
+  const double theta = m < kRopeTablePairs ? rt.theta[m] : rope_theta(o.rope, m, d_r);
+  double sd, cd;
+  sincos((double)pos * theta, &sd, &cd);
+  *c = (float)cd;
+  *s = (float)sd;
+}
+
+// ---- append -----------------------------------------------------------------------------------------------
+// One block per new token: its row [c | R_pos k] into its page and, with q, its n_h rotated queries.
+template <typename T>
+__global__ void __launch_bounds__(128)
+    append_kernel(PagedView v, const T* kv, int64_t kv_stride, const T* q, T* q_out, LayerOpts o, RopeTable rt,
+                  uint32_t* err) {
+  extern __shared__ float2 cs[];      // [d_r / 2] cos, sin
+  __shared__ float red[32];
+  const int tid = threadIdx.x;
+  const int64_t t = blockIdx.x;
+  if (t == 0) paged_check(v, err);
+  const PagedToken tok = paged_token(v, t);
+  if (tok.pos < 0) return;
+  const int64_t page = paged_page(v, tok.seq, tok.pos / v.page, err);
+  for (int m = tid; m < v.d_r / 2; m += blockDim.x) rope_angle(rt, o, tok.pos, m, v.d_r, &cs[m].x, &cs[m].y);
+  __syncthreads();
+  const T* src = kv + t * kv_stride;
+  if (page >= 0) {
+    T* row = reinterpret_cast<T*>(v.cache) + (page * v.page + tok.pos % v.page) * (v.d_c + v.d_r);
+    float inv = 1.f;
+    if (o.g_kv) {
+      float ss = 0.f;
+      for (int c = tid; c < v.d_c; c += blockDim.x) ss = fmaf(to_f(src[c]), to_f(src[c]), ss);
+      inv = 1.f / sqrtf(block_sum(ss, red) / (float)v.d_c + o.eps);
+    }
+    for (int c = tid; c < v.d_c; c += blockDim.x)
+      row[c] = o.g_kv ? from_f<T>(to_f(src[c]) * inv * to_f(reinterpret_cast<const T*>(o.g_kv)[c])) : src[c];
+    for (int m = tid; m < v.d_r / 2; m += blockDim.x) {
+      const float x0 = to_f(src[v.d_c + 2 * m]), x1 = to_f(src[v.d_c + 2 * m + 1]);
+      row[v.d_c + 2 * m] = from_f<T>((x0 * cs[m].x - x1 * cs[m].y) * rt.mul);
+      row[v.d_c + 2 * m + 1] = from_f<T>((x0 * cs[m].y + x1 * cs[m].x) * rt.mul);
+    }
+  }
+  if (!q) return;
+  const int64_t base = t * v.n_h * v.d_r;
+  for (int i = tid; i < v.n_h * (v.d_r / 2); i += blockDim.x) {
+    const float2 w = cs[i % (v.d_r / 2)];
+    const float x0 = to_f(q[base + 2 * i]), x1 = to_f(q[base + 2 * i + 1]);
+    q_out[base + 2 * i] = from_f<T>((x0 * w.x - x1 * w.y) * rt.mul);
+    q_out[base + 2 * i + 1] = from_f<T>((x0 * w.y + x1 * w.x) * rt.mul);
+  }
+}
+
+// The scale and one code of a row whose largest magnitude is amax: x / scale to the nearest whole number.
+// A row whose scale is 0, infinite or NaN has scale 0 and codes 0; a NaN element has code 0.
+__device__ __forceinline__ float code_scale(float amax) {
+  const float s = __fdiv_rn(amax, 127.f);
+  return s > 0.f && s < INFINITY ? s : 0.f;
+}
+__device__ __forceinline__ int code_of(float x, float s) {
+  if (!(s > 0.f)) return 0;
+  const float r = rintf(__fdiv_rn(x, s));
+  return r >= 127.f ? 127 : r <= -127.f ? -127 : (int)r;
+}
+
+// Summaries of the pages that the new tokens complete. Block i looks at `group` tokens; a token that is its
+// page's last row stands for the page.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    summarise_kernel(PagedView v, int group, uint8_t* summaries, int64_t pitch) {
+  extern __shared__ float mean[];     // [W]
+  __shared__ float red[32];
+  const int tid = threadIdx.x, W = v.d_c + v.d_r;
+  for (int k = 0; k < group; ++k) {
+    const int64_t t = (int64_t)blockIdx.x * group + k;
+    if (t >= v.total_q) return;
+    const PagedToken tok = paged_token(v, t);
+    if (tok.seq < 0) return;
+    if (tok.pos < 0 || tok.pos % v.page != v.page - 1) continue;
+    const int32_t p = v.table[(int64_t)tok.seq * v.stride + tok.pos / v.page];
+    if (p < 0 || p >= v.num_pages) continue;      // flagged by the append
+    const T* rows = reinterpret_cast<const T*>(v.cache) + (int64_t)p * v.page * W;
+    float amax = 0.f;
+    for (int c = tid; c < W; c += blockDim.x) {
+      double sum = 0.0;               // of 8-bit mantissas: exact in double, whatever the order
+      for (int r = 0; r < v.page; ++r) sum += (double)to_f(rows[(int64_t)r * W + c]);
+      mean[c] = (float)(sum / v.page);
+      amax = fmaxf(amax, fabsf(mean[c]));
+    }
+    const float s = code_scale(block_max(amax, red));
+    uint8_t* out = summaries + (int64_t)p * pitch;
+    for (int c = tid; c < pitch; c += blockDim.x)
+      if (c < W) out[c] = (uint8_t)(int8_t)code_of(mean[c], s);
+      else if (c >= W + 4) out[c] = 0;
+    if (tid == 0) *reinterpret_cast<float*>(out + W) = s;
+    __syncthreads();
+  }
+}
+
+// ---- attention by CUDA cores --------------------------------------------------------------------------------
+constexpr int ATT = 128;
+constexpr int ATT_MAX_DV = 512;
+
+template <typename T>
+__global__ void __launch_bounds__(ATT)
+    paged_attention_kernel(PagedView v, const T* q_abs, const T* q_rope, const int32_t* blocks, int32_t top_k,
+                           float scale, T* o_lat, float* lse, uint32_t* err) {
+  __shared__ float qs[1024];
+  __shared__ float ps[ATT];
+  __shared__ int64_t row_of[ATT];
+  __shared__ float red[32];
+  __shared__ int list_scratch[2];
+  const int64_t t = blockIdx.x;
+  const int head = blockIdx.y, tid = threadIdx.x, W = v.d_c + v.d_r;
+  if (t == 0 && head == 0) paged_check(v, err);
+  const PagedToken tok = paged_token(v, t);
+  if (tok.seq < 0) return;
+  const int32_t* list = blocks ? blocks + t * top_k : nullptr;
+  int64_t n = tok.pos + 1;
+  if (list) n = tok.pos < 0 ? 0 : paged_list_rows(list, top_k, tok.pos, v.page, list_scratch, err);
+  const int64_t oq = t * v.n_h + head;
+  for (int c = tid; c < W; c += ATT)
+    qs[c] = c < v.d_c ? to_f(q_abs[oq * v.d_c + c]) : to_f(q_rope[oq * v.d_r + c - v.d_c]);
+  __syncthreads();
+  const T* rows = reinterpret_cast<const T*>(v.cache);
+  float m = -INFINITY, l = 0.f;
+  float acc[ATT_MAX_DV / ATT] = {};
+  for (int64_t c0 = 0; c0 < n; c0 += ATT) {
+    const int64_t j = c0 + tid;
+    float s = -INFINITY;
+    row_of[tid] = -1;
+    if (j < n) {
+      const int64_t g = list ? list[j / v.page] : j / v.page;
+      const int64_t page = paged_page(v, tok.seq, g, err);
+      float d = 0.f;                  // a page outside the pool counts as rows of zeros
+      if (page >= 0) {
+        row_of[tid] = page * v.page + j % v.page;
+        const T* k = rows + row_of[tid] * W;
+        for (int c = 0; c < W; ++c) d = fmaf(qs[c], to_f(k[c]), d);
+      }
+      s = d * scale;
+    }
+    const float m_new = fmaxf(m, block_max(s, red));
+    const float alpha = m == -INFINITY ? 0.f : __expf(m - m_new);
+    const float p = j < n ? __expf(s - m_new) : 0.f;
+    ps[tid] = p;
+    l = l * alpha + block_sum(p, red);
+#pragma unroll
+    for (int i = 0; i < ATT_MAX_DV / ATT; ++i) acc[i] *= alpha;
+    __syncthreads();
+    const int cnt = (int)min((int64_t)ATT, n - c0);
+    for (int jj = 0; jj < cnt; ++jj) {
+      if (row_of[jj] < 0) continue;
+      const float pj = ps[jj];
+      const T* vr = rows + row_of[jj] * W;
+#pragma unroll
+      for (int i = 0; i < ATT_MAX_DV / ATT; ++i) {
+        const int c = tid + i * ATT;
+        if (c < v.d_c) acc[i] = fmaf(pj, to_f(vr[c]), acc[i]);
+      }
+    }
+    m = m_new;
+    __syncthreads();
+  }
+  const float inv = n > 0 ? 1.f / l : 0.f;
+#pragma unroll
+  for (int i = 0; i < ATT_MAX_DV / ATT; ++i) {
+    const int c = tid + i * ATT;
+    if (c < v.d_c) o_lat[oq * v.d_c + c] = from_f<T>(acc[i] * inv);
+  }
+  if (tid == 0) lse[oq] = n > 0 ? m + logf(l) : -INFINITY;
+}
+
+// ---- selection ----------------------------------------------------------------------------------------------
+// Codes and scale of each query row [q~_i | q^R_i] (one warp per row).
+template <typename T>
+__global__ void __launch_bounds__(256)
+    query_codes_kernel(PagedView v, const T* q_abs, const T* q_rope, int8_t* codes, float* scales, uint32_t* err) {
+  if (blockIdx.x == 0) paged_check(v, err);
+  const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, W = v.d_c + v.d_r;
+  if (r >= v.total_q * v.n_h || r / v.n_h >= v.cu_q[v.B]) return;
+  auto at = [&](int c) { return c < v.d_c ? to_f(q_abs[r * v.d_c + c]) : to_f(q_rope[r * v.d_r + c - v.d_c]); };
+  float amax = 0.f;
+  for (int c = lane; c < W; c += 32) amax = fmaxf(amax, fabsf(at(c)));
+  const float s = code_scale(warp_max(amax));
+  for (int c = lane; c < W; c += 32) codes[r * W + c] = (int8_t)code_of(at(c), s);
+  if (lane == 0) scales[r] = s;
+}
+
+// Scores of 32 blocks for one token: lane = block, the warps share the heads.
+constexpr int SCORE_WARPS = 8;
+__global__ void __launch_bounds__(32 * SCORE_WARPS)
+    score_kernel(PagedView v, const int8_t* codes, const float* scales, const uint8_t* summaries, int64_t pitch,
+                 int32_t top_k, float* scores, uint32_t* err) {
+  extern __shared__ int32_t ksh[];    // [32][W / 4 | 1]
+  __shared__ float best[SCORE_WARPS][32];
+  const int64_t t = blockIdx.y;
+  const PagedToken tok = paged_token(v, t);
+  if (tok.pos < 0) return;
+  const int64_t nb = tok.pos / v.page + 1, g0 = (int64_t)blockIdx.x * 32;
+  if (nb <= top_k || g0 >= nb) return;
+  const int W4 = (v.d_c + v.d_r) / 4, ld = W4 | 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = warp; i < 32; i += SCORE_WARPS) {
+    const int64_t g = g0 + i;
+    const int64_t p = g < nb ? paged_page(v, tok.seq, g, err) : -1;
+    const int32_t* src = reinterpret_cast<const int32_t*>(summaries + (p < 0 ? 0 : p) * pitch);
+    for (int c = lane; c < W4; c += 32) ksh[i * ld + c] = p < 0 ? 0 : src[c];
+  }
+  __syncthreads();
+  float mx = -INFINITY;
+  for (int h = warp; h < v.n_h; h += SCORE_WARPS) {
+    const int32_t* q = reinterpret_cast<const int32_t*>(codes + (t * v.n_h + h) * 4 * W4);
+    int d = 0;
+    for (int c = 0; c < W4; ++c) d = __dp4a(q[c], ksh[lane * ld + c], d);
+    mx = fmaxf(mx, (float)d * scales[t * v.n_h + h]);
+  }
+  best[warp][lane] = mx;
+  __syncthreads();
+  if (warp == 0 && g0 + lane < nb) {
+#pragma unroll
+    for (int w = 1; w < SCORE_WARPS; ++w) mx = fmaxf(mx, best[w][lane]);
+    const int64_t g = g0 + lane;
+    const int32_t p = v.table[(int64_t)tok.seq * v.stride + g];
+    const float s = p < 0 || p >= v.num_pages ? 0.f : *reinterpret_cast<const float*>(summaries + p * pitch + 4 * W4);
+    scores[t * v.max_pages + g] = mx * s + 0.f;       // + 0: a -0 ties with a 0
+  }
+}
+
+// Order-preserving key of a float.
+__device__ __forceinline__ uint32_t key_of(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// The chosen blocks of one token, by a radix select (8 bits a pass) and an ordered write.
+__global__ void __launch_bounds__(256)
+    select_kernel(PagedView v, const float* scores, int32_t top_k, int32_t n_first, int32_t n_last, int32_t* blocks) {
+  __shared__ int hist[256];
+  __shared__ uint32_t s_prefix;
+  __shared__ int s_left;
+  __shared__ int wsum[8][2];
+  const int64_t t = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const PagedToken tok = paged_token(v, t);
+  if (tok.seq < 0) return;
+  int32_t* out = blocks + t * top_k;
+  const int64_t nb = tok.pos < 0 ? 0 : tok.pos / v.page + 1;
+  if (nb <= top_k) {
+    for (int i = tid; i < top_k; i += blockDim.x) out[i] = i < nb ? i : -1;
+    return;
+  }
+  const float* sc = scores + t * v.max_pages;
+  const int64_t lo = n_first, hi = nb - n_last;       // candidates
+  const int want = top_k - n_first - n_last;
+  for (int i = tid; i < n_first; i += blockDim.x) out[i] = i;
+  for (int i = tid; i < n_last; i += blockDim.x) out[top_k - n_last + i] = (int32_t)(hi + i);
+  if (want == 0) return;
+  uint32_t prefix = 0, mask = 0;
+  int left = want;
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    hist[tid] = 0;
+    __syncthreads();
+    for (int64_t g = lo + tid; g < hi; g += blockDim.x) {
+      const uint32_t k = key_of(sc[g]);
+      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
+    }
+    __syncthreads();
+    if (tid == 0) {
+      int d = 255, n = left;
+      while (hist[d] < n) n -= hist[d--];
+      s_prefix = prefix | ((uint32_t)d << shift);
+      s_left = n;
+    }
+    __syncthreads();
+    prefix = s_prefix;
+    left = s_left;
+    mask |= 255u << shift;
+    __syncthreads();
+  }
+  // all keys above `prefix`, and the first `left` of those equal to it, in the order of the blocks
+  int done = n_first, eq_done = 0;
+  for (int64_t g0 = lo; g0 < hi; g0 += blockDim.x) {
+    const int64_t g = g0 + tid;
+    const uint32_t k = g < hi ? key_of(sc[g]) : 0;
+    const bool gt = g < hi && k > prefix, eq = g < hi && k == prefix;
+    const uint32_t below = (1u << lane) - 1u;
+    const uint32_t mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
+    if (lane == 0) {
+      wsum[warp][0] = __popc(mg);
+      wsum[warp][1] = __popc(me);
+    }
+    __syncthreads();
+    int g_before = __popc(mg & below), e_before = __popc(me & below), g_all = 0, e_all = 0;
+    for (int w = 0; w < 8; ++w) {
+      if (w < warp) {
+        g_before += wsum[w][0];
+        e_before += wsum[w][1];
+      }
+      g_all += wsum[w][0];
+      e_all += wsum[w][1];
+    }
+    const int rank = eq_done + e_before;              // of this key among the equal ones
+    if (gt || (eq && rank < left)) out[done + g_before + min(rank, left) - min(eq_done, left)] = (int32_t)g;
+    done += g_all + min(eq_done + e_all, left) - min(eq_done, left);
+    eq_done += e_all;
+    __syncthreads();
+  }
+}
+
+size_t align16(size_t x) { return (x + 15) / 16 * 16; }
+size_t align1k(size_t x) { return (x + 1023) / 1024 * 1024; }
+
+template <typename T>
+cudaError_t append_launch(const PagedView& v, const void* kv, int64_t kv_stride, const void* q, void* q_out,
+                          void* summaries, const LayerOpts& o, const RopeTable& rt, uint32_t* err, cudaStream_t st) {
+  append_kernel<T><<<(unsigned)v.total_q, 128, (size_t)v.d_r * 4, st>>>(
+      v, (const T*)kv, kv_stride, (const T*)q, (T*)q_out, o, rt, err);
+  note_launch();
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !summaries) return e;
+  const int group = (int)((v.total_q + 2047) / 2048);
+  summarise_kernel<T><<<(unsigned)((v.total_q + group - 1) / group), 256, (size_t)(v.d_c + v.d_r) * 4, st>>>(
+      v, group, (uint8_t*)summaries, (int64_t)summary_pitch(v.d_c, v.d_r));
+  note_launch();
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t attention_launch(const PagedView& v, const void* q_abs, const void* q_rope, const int32_t* blocks,
+                             int32_t top_k, float scale, void* o_lat, float* lse, uint32_t* err, cudaStream_t st) {
+  paged_attention_kernel<T><<<dim3((unsigned)v.total_q, (unsigned)v.n_h), ATT, 0, st>>>(
+      v, (const T*)q_abs, (const T*)q_rope, blocks, top_k, scale, (T*)o_lat, lse, err);
+  note_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t summary_pitch(int32_t d_c, int32_t d_r) { return align16((size_t)d_c + d_r + 4); }
+
+cudaError_t paged_append(const PagedView& v, bool bf16, const void* kv, int64_t kv_stride, const void* q_rope,
+                         void* q_out, void* summaries, const LayerOpts& o, const RopeTable& rope, uint32_t* err,
+                         cudaStream_t st) {
+  return bf16 ? append_launch<__nv_bfloat16>(v, kv, kv_stride, q_rope, q_out, summaries, o, rope, err, st)
+              : append_launch<float>(v, kv, kv_stride, q_rope, q_out, summaries, o, rope, err, st);
+}
+
+cudaError_t paged_attention_simt(const PagedView& v, bool bf16, const void* q_abs, const void* q_rope,
+                                 const int32_t* blocks, int32_t top_k, float scale, void* o_lat, float* lse,
+                                 uint32_t* err, cudaStream_t st) {
+  return bf16 ? attention_launch<__nv_bfloat16>(v, q_abs, q_rope, blocks, top_k, scale, o_lat, lse, err, st)
+              : attention_launch<float>(v, q_abs, q_rope, blocks, top_k, scale, o_lat, lse, err, st);
+}
+
+size_t paged_select_bytes(int32_t n_h, int32_t d_c, int32_t d_r, int64_t total_q, int64_t max_pages) {
+  const size_t rows = (size_t)total_q * n_h;
+  return align1k(rows * (d_c + d_r)) + align1k(rows * 4) + align1k((size_t)total_q * max_pages * 4);
+}
+
+cudaError_t paged_select(const PagedView& v, bool bf16, const void* q_abs, const void* q_rope, const void* summaries,
+                         int32_t top_k, int32_t n_first, int32_t n_last, int32_t* blocks, void* ws, uint32_t* err,
+                         cudaStream_t st) {
+  const size_t rows = (size_t)v.total_q * v.n_h, W = (size_t)v.d_c + v.d_r;
+  int8_t* codes = (int8_t*)ws;
+  float* scales = (float*)((char*)ws + align1k(rows * W));
+  float* scores = (float*)((char*)scales + align1k(rows * 4));
+  const unsigned qgrid = (unsigned)((rows + 7) / 8);
+  if (bf16)
+    query_codes_kernel<__nv_bfloat16><<<qgrid, 256, 0, st>>>(v, (const __nv_bfloat16*)q_abs,
+                                                             (const __nv_bfloat16*)q_rope, codes, scales, err);
+  else
+    query_codes_kernel<float><<<qgrid, 256, 0, st>>>(v, (const float*)q_abs, (const float*)q_rope, codes, scales, err);
+  note_launch();
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  score_kernel<<<dim3((unsigned)((v.max_pages + 31) / 32), (unsigned)v.total_q), 32 * SCORE_WARPS,
+                 32 * ((W / 4) | 1) * 4, st>>>(v, codes, scales, (const uint8_t*)summaries,
+                                               (int64_t)summary_pitch(v.d_c, v.d_r), top_k, scores, err);
+  note_launch();
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  select_kernel<<<(unsigned)v.total_q, 256, 0, st>>>(v, scores, top_k, n_first, n_last, blocks);
+  note_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace mla

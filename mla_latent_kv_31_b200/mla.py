@@ -31,6 +31,12 @@ class MlaWeights(ctypes.Structure):
     _fields_ = [(n, c_void_p) for n in WEIGHT_NAMES]
 
 
+class MlaPaged(ctypes.Structure):
+    _fields_ = [("cache", c_void_p), ("num_pages", c_int64), ("page_size", c_int32), ("block_table", c_void_p),
+                ("max_pages", c_int64), ("table_stride", c_int64), ("cu_q", c_void_p), ("kv_lens", c_void_p),
+                ("B", c_int64), ("total_q", c_int64)]
+
+
 class MLAError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -71,6 +77,17 @@ def lib() -> ctypes.CDLL:
                                                c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
             "mla_attn_prefill": (c_int, [H, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_int64,
                                          c_int64, c_void_p, c_int64, c_void_p, c_void_p]),
+            "mla_paged_summary_bytes": (c_int, [H, POINTER(c_size_t)]),
+            "mla_paged_append": (c_int, [H, POINTER(MlaPaged), c_void_p, c_int64, c_void_p, c_void_p, c_void_p,
+                                         c_void_p]),
+            "mla_attn_paged": (c_int, [H, POINTER(MlaPaged), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                       c_size_t, c_void_p]),
+            "mla_attn_paged_workspace": (c_int, [H, c_int64, c_int64, POINTER(c_size_t)]),
+            "mla_paged_select": (c_int, [H, POINTER(MlaPaged), c_void_p, c_void_p, c_void_p, c_int32, c_int32,
+                                         c_int32, c_void_p, c_void_p, c_size_t, c_void_p]),
+            "mla_paged_select_workspace": (c_int, [H, c_int64, c_int64, POINTER(c_size_t)]),
+            "mla_attn_paged_sparse": (c_int, [H, POINTER(MlaPaged), c_void_p, c_void_p, c_void_p, c_int32, c_void_p,
+                                              c_void_p, c_void_p, c_size_t, c_void_p]),
             "mla_set_rmsnorm": (c_int, [H, c_void_p, c_void_p, c_double]),
             "mla_set_yarn": (c_int, [H, c_double, c_double, c_double, c_double]),
             "mla_set_cache_format": (c_int, [H, c_int]),
@@ -199,6 +216,80 @@ def mla_attn_prefill(handle, q_c, q_rope, k_c, v_c, B, cu_seqlens, total_tokens,
            "mla_attn_prefill")
 
 
+class PagedBatch:
+    """A paged latent cache and the new tokens of a step (mla_paged_t): cache [num_pages, page_size, d_c + d_r],
+    block_table [B, max_pages] int32, cu_q [B + 1] int64, kv_lens [B] int64 (the new tokens included) and the
+    rows total_q of the per-token arrays. All on the handle's device; the table's rows may be strided."""
+
+    def __init__(self, cache, block_table, cu_q, kv_lens, total_q: int):
+        import torch
+        B = kv_lens.shape[0]
+        for name, x, dtype, shape in (("block_table", block_table, torch.int32, (B, None)),
+                                      ("cu_q", cu_q, torch.int64, (B + 1,)), ("kv_lens", kv_lens, torch.int64, (B,)),
+                                      ("cache", cache, cache.dtype, (None, None, None))):
+            _expect(name, x, dtype, shape, cache.device, contiguous=name != "block_table")
+        if block_table.shape[1] > 1 and block_table.stride(1) != 1:
+            raise ValueError("block_table: the entries of a row must be adjacent")
+        self.tensors = (cache, block_table, cu_q, kv_lens)    # borrowed by the calls
+        self.cache, self.total_q, self.B, self.max_pages = cache, total_q, B, block_table.shape[1]
+        stride = block_table.stride(0) if B > 1 else block_table.shape[1]
+        self.c = MlaPaged(cache.data_ptr(), cache.shape[0], cache.shape[1], block_table.data_ptr(),
+                          block_table.shape[1], stride, cu_q.data_ptr(), kv_lens.data_ptr(), B, total_q)
+
+
+def _expect(name, x, dtype, shape, device, contiguous=True):
+    """Raises ValueError unless x has this dtype, shape (None: any size), device and, if asked, no gaps."""
+    if x.dtype != dtype or len(x.shape) != len(shape) or any(n is not None and n != m for n, m in zip(shape, x.shape)):
+        want = ", ".join("*" if n is None else str(n) for n in shape)
+        raise ValueError(f"{name}: expected {dtype} [{want}], got {x.dtype} {list(x.shape)}")
+    if x.device != device:
+        raise ValueError(f"{name}: on {x.device}, expected {device}")
+    if contiguous and not x.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+
+
+def mla_paged_summary_bytes(handle) -> int:
+    n = c_size_t()
+    _check(lib().mla_paged_summary_bytes(handle, ctypes.byref(n)), "mla_paged_summary_bytes")
+    return n.value
+
+
+def mla_paged_append(handle, batch, kv, kv_stride, q_rope=None, q_out=None, summaries=None, stream=None, device=0):
+    _check(lib().mla_paged_append(handle, ctypes.byref(batch.c), _ptr(kv), kv_stride, _ptr(q_rope), _ptr(q_out),
+                                  _ptr(summaries), _stream(stream, device)), "mla_paged_append")
+
+
+def mla_attn_paged_workspace(handle, B: int, total_q: int) -> int:
+    n = c_size_t()
+    _check(lib().mla_attn_paged_workspace(handle, B, total_q, ctypes.byref(n)), "mla_attn_paged_workspace")
+    return n.value
+
+
+def mla_attn_paged(handle, batch, q_abs, q_rope, o_lat, lse, ws, ws_bytes, stream=None, device=0):
+    _check(lib().mla_attn_paged(handle, ctypes.byref(batch.c), _ptr(q_abs), _ptr(q_rope), _ptr(o_lat), _ptr(lse),
+                                _ptr(ws), ws_bytes, _stream(stream, device)), "mla_attn_paged")
+
+
+def mla_paged_select_workspace(handle, total_q: int, max_pages: int) -> int:
+    n = c_size_t()
+    _check(lib().mla_paged_select_workspace(handle, total_q, max_pages, ctypes.byref(n)), "mla_paged_select_workspace")
+    return n.value
+
+
+def mla_paged_select(handle, batch, q_abs, q_rope, summaries, top_k, n_first, n_last, blocks, ws, ws_bytes,
+                     stream=None, device=0):
+    _check(lib().mla_paged_select(handle, ctypes.byref(batch.c), _ptr(q_abs), _ptr(q_rope), _ptr(summaries), top_k,
+                                  n_first, n_last, _ptr(blocks), _ptr(ws), ws_bytes, _stream(stream, device)),
+           "mla_paged_select")
+
+
+def mla_attn_paged_sparse(handle, batch, q_abs, q_rope, blocks, top_k, o_lat, lse, ws, ws_bytes, stream=None,
+                          device=0):
+    _check(lib().mla_attn_paged_sparse(handle, ctypes.byref(batch.c), _ptr(q_abs), _ptr(q_rope), _ptr(blocks), top_k,
+                                       _ptr(o_lat), _ptr(lse), _ptr(ws), ws_bytes, _stream(stream, device)),
+           "mla_attn_paged_sparse")
+
+
 def mla_set_rmsnorm(handle, g_q, g_kv, eps: float = 1e-6):
     """RMSNorm gains of c^Q and c^KV (device tensors in the handle dtype), or None, None to turn it off."""
     _check(lib().mla_set_rmsnorm(handle, _ptr(g_q), _ptr(g_kv), eps), "mla_set_rmsnorm")
@@ -265,16 +356,19 @@ def mla_destroy(handle):
 
 # --- convenience owner of a handle, its weights and workspaces -----------------------------
 class MLA:
-    """Owns one handle plus torch allocations (weights kept alive, workspaces reused)."""
+    """Owns one handle plus torch allocations (weights kept alive, workspaces reused). weights = None: a handle
+    for the calls that need none (the attention cores and the paged cache)."""
 
-    def __init__(self, dims, weights: dict, dtype: int = MLA_BF16, device: int = 0):
+    def __init__(self, dims, weights: dict | None, dtype: int = MLA_BF16, device: int = 0):
         import torch
         self.torch = torch
         self.dims, self.dtype, self.device = dims, dtype, device
         self.tdtype = torch.bfloat16 if dtype == MLA_BF16 else torch.float32
         self.handle = mla_create(dims, dtype, device)
-        self.weights = {n: weights[n] for n in WEIGHT_NAMES}
-        mla_set_weights(self.handle, self.weights)
+        weights = weights or {}
+        self.weights = {n: weights[n] for n in WEIGHT_NAMES} if weights else {}
+        if weights:
+            mla_set_weights(self.handle, self.weights)
         # opt-in parts of the layer: RMSNorm gains among the weights, YaRN settings in the dims
         if "g_q" in weights or "g_kv" in weights:
             self.gains = (weights["g_q"], weights["g_kv"])
@@ -282,6 +376,7 @@ class MLA:
         if getattr(dims, "yarn_s", 1.0) > 1.0:
             mla_set_yarn(self.handle, dims.yarn_s, dims.yarn_alpha, dims.yarn_beta, dims.yarn_l0)
         self._ws = None
+        self._ws_captured, self._kept = False, []
 
     def close(self):
         if self.handle:
@@ -297,7 +392,11 @@ class MLA:
     def workspace(self, nbytes: int):
         torch = self.torch
         if self._ws is None or self._ws.numel() < nbytes:
+            if self._ws_captured:
+                self._kept.append(self._ws)     # a captured graph still writes to it when it is replayed
+                self._ws_captured = False
             self._ws = torch.empty(max(nbytes, 1024), dtype=torch.uint8, device=f"cuda:{self.device}")
+        self._ws_captured = self._ws_captured or torch.cuda.is_current_stream_capturing()
         return self._ws
 
     def region(self, op, which, shape, dtype, num_seqs=0, tq=1, total_tokens=0):
@@ -382,6 +481,85 @@ class MLA:
         mla_attn_decode_latent(self.handle, q_abs, q_rope, B, Tq, cu_seqlens, cache, cache.shape[0], o_lat, lse, ws,
                                ws.numel(), device=self.device)
         return o_lat, lse
+
+    # --- the paged latent cache (PagedBatch)
+    def _expect_rows(self, batch, **tensors):
+        """Checks tensors [total_q, ...] given as name=(tensor, trailing shape, dtype or None for the handle's)."""
+        if batch.cache.dtype != self.tdtype or batch.cache.shape[2] != self.dims.d_c + self.dims.d_r:
+            raise ValueError(f"cache: expected {self.tdtype} rows of {self.dims.d_c + self.dims.d_r}, "
+                             f"got {batch.cache.dtype} {list(batch.cache.shape)}")
+        dev = self.torch.device("cuda", self.device)
+        if batch.cache.device != dev:
+            raise ValueError(f"cache: on {batch.cache.device}, the handle is on {dev}")
+        for name, (x, shape, dtype) in tensors.items():
+            if x is not None:
+                _expect(name, x, dtype or self.tdtype, (batch.total_q, *shape), batch.cache.device)
+
+    def new_summaries(self, num_pages: int):
+        """Zeroed summary rows of num_pages pages."""
+        return self.torch.zeros(num_pages, mla_paged_summary_bytes(self.handle), dtype=self.torch.uint8,
+                                device=f"cuda:{self.device}")
+
+    def _expect_summaries(self, batch, summaries):
+        _expect("summaries", summaries, self.torch.uint8, (batch.cache.shape[0], mla_paged_summary_bytes(self.handle)),
+                batch.cache.device)
+
+    def paged_append(self, batch, kv, q_rope=None, q_out=None, summaries=None):
+        """Writes the new tokens' rows (kv [total_q, d_c + d_r], rows may be strided) to their pages; with q_rope
+        returns the rotated queries (q_out, which may be q_rope itself)."""
+        d = self.dims
+        qs = ((d.n_h, d.d_r), None)
+        if q_rope is not None and q_out is None:
+            q_out = self.torch.empty_like(q_rope)
+        self._expect_rows(batch, q_rope=(q_rope, *qs), q_out=(q_out, *qs))
+        _expect("kv", kv, self.tdtype, (batch.total_q, d.d_c + d.d_r), batch.cache.device, contiguous=False)
+        if kv.stride(1) != 1:
+            raise ValueError("kv: the elements of a row must be adjacent")
+        if summaries is not None:
+            self._expect_summaries(batch, summaries)
+        stride = kv.stride(0) if kv.shape[0] > 1 else kv.shape[1]
+        mla_paged_append(self.handle, batch, kv, stride, q_rope, q_out, summaries, device=self.device)
+        return q_out
+
+    def attn_paged(self, batch, q_abs, q_rope, o_lat=None, lse=None):
+        """(o_lat [total_q, n_h, d_c] in the handle's dtype, lse [total_q, n_h] fp32)."""
+        return self._attn_paged(batch, q_abs, q_rope, None, o_lat, lse)
+
+    def attn_paged_sparse(self, batch, q_abs, q_rope, blocks, o_lat=None, lse=None):
+        """attn_paged over the blocks [total_q, top_k] of each token (int32, ascending, -1 behind the last)."""
+        return self._attn_paged(batch, q_abs, q_rope, blocks, o_lat, lse)
+
+    def _attn_paged(self, batch, q_abs, q_rope, blocks, o_lat, lse):
+        torch, d, T = self.torch, self.dims, batch.total_q
+        if o_lat is None:
+            o_lat = torch.empty(T, d.n_h, d.d_c, dtype=self.tdtype, device=q_abs.device)
+        if lse is None:
+            lse = torch.empty(T, d.n_h, dtype=torch.float32, device=q_abs.device)
+        top_k = 0 if blocks is None else blocks.shape[-1]
+        self._expect_rows(batch, q_abs=(q_abs, (d.n_h, d.d_c), None), q_rope=(q_rope, (d.n_h, d.d_r), None),
+                          o_lat=(o_lat, (d.n_h, d.d_c), None), lse=(lse, (d.n_h,), torch.float32),
+                          blocks=(blocks, (top_k,), torch.int32))
+        ws = self.workspace(mla_attn_paged_workspace(self.handle, batch.B, T))
+        if blocks is None:
+            mla_attn_paged(self.handle, batch, q_abs, q_rope, o_lat, lse, ws, ws.numel(), device=self.device)
+        else:
+            mla_attn_paged_sparse(self.handle, batch, q_abs, q_rope, blocks, top_k, o_lat, lse, ws, ws.numel(),
+                                  device=self.device)
+        return o_lat, lse
+
+    def paged_select(self, batch, q_abs, q_rope, summaries, top_k: int, n_first: int = 1, n_last: int = 1,
+                     blocks=None):
+        """The blocks each new token attends to, [total_q, top_k] int32."""
+        d = self.dims
+        if blocks is None:
+            blocks = self.torch.empty(batch.total_q, top_k, dtype=self.torch.int32, device=q_abs.device)
+        self._expect_rows(batch, q_abs=(q_abs, (d.n_h, d.d_c), None), q_rope=(q_rope, (d.n_h, d.d_r), None),
+                          blocks=(blocks, (top_k,), self.torch.int32))
+        self._expect_summaries(batch, summaries)
+        ws = self.workspace(mla_paged_select_workspace(self.handle, batch.total_q, batch.max_pages))
+        mla_paged_select(self.handle, batch, q_abs, q_rope, summaries, top_k, n_first, n_last, blocks, ws, ws.numel(),
+                         device=self.device)
+        return blocks
 
     def sync_status(self) -> int:
         return mla_sync_status(self.handle, device=self.device)

@@ -1,0 +1,424 @@
+"""The paged latent cache on the GPU against its float64 form: ragged batches, pages that end inside a tile, NaN in
+every row that must not matter, padded batches, lists of blocks, captured and replayed steps."""
+import pytest
+import torch
+
+from mla_latent_kv_31_b200 import mla, synth
+from paged_testlib import DT, HALF, NAN, Case, handle, rope
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mods():
+    m = {dt: handle(dt) for dt in ("bf16", "fp32")}
+    yield m
+    for x in m.values():
+        x.close()
+
+
+def ok(m):
+    s = m.sync_status()
+    assert s == 0, (mla.mla_status_string(s), hex(mla.mla_device_error_bits(m.handle)))
+
+
+def flagged(m, bit):
+    assert m.sync_status() == 7
+    assert mla.mla_device_error_bits(m.handle) == bit
+
+
+def prefix(c):
+    return lambda t, b, pos: c.rows[b][:pos + 1]
+
+
+LENS = [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 255, 257, 1000]
+
+
+@pytest.mark.parametrize("dtype,page,lens,tq", [
+    ("fp32", 16, LENS, [1] * 14), ("fp32", 32, [40, 700, 3, 129], [5, 1, 3, 0]), ("fp32", 48, [1000], [130]),
+    ("bf16", 16, LENS, [1] * 14), ("bf16", 64, LENS, [1] * 14), ("bf16", 32, [40, 700, 3, 129], [5, 1, 3, 0]),
+    ("bf16", 48, [200, 1000, 47], [3, 2, 1]), ("bf16", 80, [321, 79, 81, 400], [2, 2, 2, 2]),
+    ("bf16", 128, [1025, 128, 5], [1, 8, 5]), ("bf16", 192, [700, 191], [1, 4]),
+    ("bf16", 64, [4097], [1]), ("bf16", 64, [9000, 77], [1, 1]), ("bf16", 64, [300], [300]),
+    ("bf16", 1024, [1500, 2049], [2, 1])])
+def test_attention(mods, dtype, page, lens, tq):
+    c = Case(dtype, page, lens, tq, seed=len(lens) + page)
+    o, lse = mods[dtype].attn_paged(c.batch(), c.q_abs, c.q_rope)
+    ok(mods[dtype])
+    c.check_attention(o, lse, prefix(c))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_attention_many_short_sequences(mods, dtype):
+    c = Case(dtype, 16, [1 + 7 * i % 90 for i in range(200)], [1] * 200, seed=3)
+    o, lse = mods[dtype].attn_paged(c.batch(), c.q_abs, c.q_rope)
+    ok(mods[dtype])
+    c.check_attention(o, lse, prefix(c))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_attention_padded_batch_and_strided_table(mods, dtype):
+    c = Case(dtype, 64, [130, 64, 700], [2, 0, 3], pad=6, seed=4)
+    wide = torch.full((3, c.table.shape[1] + 5), -3, dtype=torch.int32, device="cuda")
+    wide[:, :c.table.shape[1]] = c.d_table
+    b = mla.PagedBatch(c.cache, wide[:, :c.table.shape[1]], c.d_cu, c.d_lens, c.T + 6)
+    o = torch.full((c.T + 6, c.dims.n_h, c.dims.d_c), 7.0, dtype=DT[dtype], device="cuda")
+    lse = torch.full((c.T + 6, c.dims.n_h), 7.0, device="cuda")
+    mods[dtype].attn_paged(b, c.q_abs, c.q_rope, o, lse)
+    ok(mods[dtype])
+    c.check_attention(o, lse, prefix(c))
+    assert (o[c.T:] == 7).all() and (lse[c.T:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_attention_later_rows_may_be_nan(mods, dtype):
+    """The last two rows of the sequence are NaN: the tokens before them do not see it."""
+    c = Case(dtype, 16, [70], [5], seed=5)
+    for p in (68, 69):
+        c.cache[c.table[0, p // 16].long(), p % 16] = NAN
+    o, lse = mods[dtype].attn_paged(c.batch(), c.q_abs, c.q_rope)
+    ok(mods[dtype])
+    assert torch.isnan(o[3:]).any()
+    c.tq, c.lens = [3], [68]                              # the first three tokens alone
+    c.check_attention(o, lse, prefix(c))
+
+
+def test_attention_shared_prefix_pages(mods):
+    c = Case("bf16", 32, [200, 170, 96 + 5], [1, 2, 4], seed=6, share=3)
+    o, lse = mods["bf16"].attn_paged(c.batch(), c.q_abs, c.q_rope)
+    ok(mods["bf16"])
+    c.check_attention(o, lse, prefix(c))
+
+
+def test_attention_large_scores(mods):
+    """Rows whose scores rise by hundreds along the sequence: the running maximum moves at every tile."""
+    c = Case("bf16", 64, [1000], [1], seed=7)
+    r = c.rows[0]
+    d = c.dims.d_c
+    r[:, :d] = c.q[0, 0, :d] * torch.linspace(0.0, 40.0, 1000, dtype=torch.float64)[:, None]
+    r[:] = r.to(torch.bfloat16).double()
+    pos = torch.arange(1000)
+    c.cache[c.table[0, pos // 64].long().cuda(), (pos % 64).cuda()] = r.to(torch.bfloat16).cuda()
+    o, lse = mods["bf16"].attn_paged(c.batch(), c.q_abs, c.q_rope)
+    ok(mods["bf16"])
+    c.check_attention(o, lse, prefix(c))
+
+
+def test_attention_equals_the_contiguous_core(mods):
+    c = Case("bf16", 64, [500, 1, 129], [1, 1, 1], seed=8)
+    o, lse = mods["bf16"].attn_paged(c.batch(), c.q_abs, c.q_rope)
+    rows = torch.cat(c.rows).to(torch.bfloat16).cuda()
+    cu = torch.tensor([0, 500, 501, 630], dtype=torch.int64, device="cuda")
+    o2, lse2 = mods["bf16"].attn_decode_latent(c.q_abs, c.q_rope, 3, 1, cu, rows)
+    ok(mods["bf16"])
+    # each side is within 2 * 2^-8 of sum p |c| (weights and output or partial rounded to bf16)
+    lim = 4 * HALF["bf16"] * max(float(r[:, :512].abs().max()) for r in c.rows)
+    assert (o.float() - o2).abs().max() <= lim
+    assert (lse - lse2).abs().max() <= 1e-4
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_attention_is_deterministic_and_runs_on_any_stream(mods, dtype):
+    m = mods[dtype]
+    c = Case(dtype, 64, [700, 64, 3000], [2, 1, 1], seed=9)
+    b, qa, qr = c.batch(), c.q_abs, c.q_rope
+    o, lse = m.attn_paged(b, qa, qr)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        o2, lse2 = m.attn_paged(b, qa, qr)
+    torch.cuda.synchronize()
+    ok(m)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_flagged_batches_give_empty_rows(mods, dtype):
+    m = mods[dtype]
+
+    def run(c, batch):
+        o, lse = m.attn_paged(batch, c.q_abs, c.q_rope)
+        return o, lse
+
+    c = Case(dtype, 32, [40, 70], [1, 2], seed=10)
+    c.d_lens[1] = 1                                        # fewer rows than new tokens
+    o, lse = run(c, c.batch())
+    flagged(m, 1 << 1)
+    assert (o[1:] == 0).all() and torch.isneginf(lse[1:]).all()
+    c.tq, c.lens = [1], [40]
+    c.check_attention(o, lse, prefix(c))
+    c = Case(dtype, 32, [40, 70], [1, 2], seed=10)
+    c.d_lens[1] = 32 * c.table.shape[1] + 1                # longer than its table
+    o, lse = run(c, c.batch())
+    flagged(m, 1 << 7)
+    assert (o[1:] == 0).all() and torch.isneginf(lse[1:]).all()
+    c = Case(dtype, 32, [40, 70], [1, 2], seed=10)
+    c.d_cu[2] = 9                                          # past the rows given
+    o, lse = run(c, c.batch())
+    assert m.sync_status() == 7 and mla.mla_device_error_bits(m.handle) & (1 << 5)
+    for bad in (c.num_pages, -1, 2 ** 31 - 1, -2 ** 31):
+        c = Case(dtype, 32, [70, 40], [1, 1], seed=10)
+        c.d_table[0, 1] = bad                              # rows 32 .. 63 are read as zeros
+        o, lse = run(c, c.batch())
+        flagged(m, 1 << 7)
+        c.rows[0][32:64] = 0
+        c.check_attention(o, lse, prefix(c))
+
+
+# ---- chosen blocks ----------------------------------------------------------------------------------------
+def listed_rows(c, blocks):
+    def rows(t, b, pos):
+        g = [x for x in blocks[t].tolist() if x >= 0]
+        j = [x * c.page + k for x in g for k in range(c.page) if x * c.page + k <= pos]
+        return c.rows[b][j]
+    return rows
+
+
+def random_blocks(c, top_k, seed, own=True):
+    g = torch.Generator().manual_seed(seed)
+    out = torch.full((c.T + c.pad, top_k), -1, dtype=torch.int32)
+    for t, b, pos in c.tokens():
+        nb = pos // c.page + 1
+        n = min(nb, int(torch.randint(1, top_k + 1, (1,), generator=g)))
+        pick = torch.randperm(nb, generator=g)[:n].tolist()
+        if own and nb - 1 not in pick:
+            pick[-1] = nb - 1
+        out[t, :n] = torch.tensor(sorted(pick), dtype=torch.int32)
+    return out
+
+
+@pytest.mark.parametrize("dtype,page,lens,tq,top_k", [
+    ("fp32", 16, [300, 40, 1, 17], [5, 2, 1, 1], 6), ("bf16", 16, [300, 40, 1, 17], [5, 2, 1, 1], 20),
+    ("bf16", 64, [3000, 100, 64], [9, 1, 3], 12), ("bf16", 128, [2000], [40], 5), ("bf16", 48, [500, 95], [2, 2], 7)])
+@pytest.mark.parametrize("own", [True, False])
+def test_sparse_attention(mods, dtype, page, lens, tq, top_k, own):
+    c = Case(dtype, page, lens, tq, seed=page + top_k)
+    blocks = random_blocks(c, top_k, 1, own)
+    blocks[0] = -1                                         # a token that attends to nothing
+    o, lse = mods[dtype].attn_paged_sparse(c.batch(), c.q_abs, c.q_rope, blocks.cuda())
+    ok(mods[dtype])
+    c.check_attention(o, lse, listed_rows(c, blocks))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_sparse_over_all_blocks_is_the_whole_attention(mods, dtype):
+    c = Case(dtype, 64, [777, 130], [3, 2], seed=11)
+    blocks = torch.full((c.T, 13), -1, dtype=torch.int32)
+    for t, b, pos in c.tokens():
+        blocks[t, :pos // 64 + 1] = torch.arange(pos // 64 + 1, dtype=torch.int32)
+    o, lse = mods[dtype].attn_paged_sparse(c.batch(), c.q_abs, c.q_rope, blocks.cuda())
+    o2, lse2 = mods[dtype].attn_paged(c.batch(), c.q_abs, c.q_rope)
+    ok(mods[dtype])
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("bad", [[3, 3, 4], [2, 1, 4], [0, 1, 5], [0, 1, 2 ** 31 - 1]])
+def test_sparse_flags_lists_that_do_not_ascend(mods, dtype, bad):
+    c = Case(dtype, 16, [70, 70], [1, 1], seed=12)         # own block: 4
+    blocks = torch.tensor([bad, [0, 2, 4]], dtype=torch.int32)
+    o, lse = mods[dtype].attn_paged_sparse(c.batch(), c.q_abs, c.q_rope, blocks.cuda())
+    flagged(mods[dtype], 1 << 8)
+    blocks[0] = -1
+    c.check_attention(o, lse, listed_rows(c, blocks))
+
+
+# ---- append -------------------------------------------------------------------------------------------------
+def check_append(c, m, dims, kv, q, gains=None, in_place=False):
+    before = c.cache.clone()
+    sums = m.new_summaries(c.num_pages)
+    sums += 5
+    qd = c.on(q)
+    got = m.paged_append(c.batch(), kv, q_rope=qd, q_out=qd if in_place else None, summaries=sums)
+    ok(m)
+    assert (got is qd) == in_place
+    half, W, d_c = HALF[c.dtype], c.W, dims.d_c
+    x = kv.double().cpu()
+    written = torch.zeros(before.shape[:2], dtype=torch.bool)
+    after = c.cache.double().cpu()
+    for t, b, pos in c.tokens():
+        page, r = int(c.table[b, pos // c.page]), pos % c.page
+        written[page, r] = True
+        want = x[t].clone()
+        if gains is not None:
+            want[:d_c] = want[:d_c] / (want[:d_c].square().mean() + 1e-6).sqrt() * gains.double()
+        want[d_c:] = rope(want[d_c:], pos, dims)
+        tol = torch.zeros(W, dtype=torch.float64)
+        # norm: 512 squares, a root and two products in fp32; rotation: two products and a sum of them; one rounding
+        tol[:d_c] = (half + (600 * 2.0 ** -24 if gains is not None else 0)) * want[:d_c].abs() if gains is not None else 0
+        pair = x[t][d_c:].view(-1, 2).norm(dim=1).repeat_interleave(2) * 1.5
+        tol[d_c:] = half * want[d_c:].abs() + 8 * 2.0 ** -24 * pair
+        assert ((after[page, r] - want).abs() <= tol).all(), (t, b, pos)
+        tol = half * 2.0 * q[t].abs().max() + 8 * 2.0 ** -24
+        wq = rope(q[t], pos, dims)
+        pair = q[t].view(c.dims.n_h, -1, 2).norm(dim=-1).repeat_interleave(2, dim=-1) * 1.5
+        tol = half * wq.abs() + 8 * 2.0 ** -24 * pair
+        assert ((got[t].double().cpu() - wq).abs() <= tol).all(), (t, b, pos)
+    same = ~written.to(c.cache.device)
+    i = DT[c.dtype] == torch.bfloat16 and torch.int16 or torch.int32
+    assert torch.equal(c.cache.view(i)[same], before.view(i)[same])
+    if c.pad:
+        assert torch.equal(got[c.T:], qd[c.T:]) if in_place else True
+    # the pages that the new tokens completed, from the rows that the cache holds now; no other page
+    done = sorted({int(c.table[b, pos // c.page]) for _, b, pos in c.tokens() if pos % c.page == c.page - 1})
+    rest = torch.tensor([p for p in range(c.num_pages) if p not in done])
+    assert (sums.cpu()[rest] == 5).all()
+    if done:
+        means = (after[done].sum(1) / c.page).float()
+        assert torch.equal(sums.cpu()[done], c.summaries(means.double()))
+
+
+@pytest.mark.parametrize("dtype,page,lens,tq,pad", [
+    ("fp32", 16, [1, 16, 33, 40], [1, 16, 2, 0], 0), ("bf16", 16, [1, 16, 33, 40], [1, 16, 2, 0], 3),
+    ("bf16", 64, [64, 4096, 65, 128, 100], [1, 1, 1, 1, 1], 0), ("bf16", 64, [1000, 200], [700, 137], 5),
+    ("bf16", 48, [500], [333], 0), ("fp32", 32, [131072 + 32], [40], 0)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_append(mods, dtype, page, lens, tq, pad, in_place):
+    c = Case(dtype, page, lens, tq, seed=20, pad=pad)
+    wide = torch.full((c.T + pad, c.W + 16), 3.0, dtype=DT[dtype], device="cuda")   # rows of a wider projection
+    kv = wide[:, :c.W]
+    kv.copy_(c.normal(c.T + pad, c.W))
+    check_append(c, mods[dtype], c.dims, kv, c.normal(c.T + pad, c.dims.n_h, c.dims.d_r), in_place=in_place)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_append_with_norm_and_yarn(dtype):
+    c = Case(dtype, 32, [131072, 70, 5], [3, 40, 5], seed=21)
+    m = handle(dtype)
+    dims = synth.Dims(**{**c.dims.__dict__, "yarn_s": 40.0, "yarn_l0": 4096.0})
+    mla.mla_set_yarn(m.handle, 40.0, dims.yarn_alpha, dims.yarn_beta, 4096.0)
+    gq, gkv = c.on(c.normal(c.dims.d_cq)), c.normal(c.dims.d_c)
+    gd = c.on(gkv)
+    mla.mla_set_rmsnorm(m.handle, gq, gd, 1e-6)
+    check_append(c, m, dims, c.on(c.normal(c.T, c.W)), c.normal(c.T, c.dims.n_h, c.dims.d_r), gains=gkv)
+    m.close()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_append_flags_bad_pages_and_writes_nothing_for_them(mods, dtype):
+    m = mods[dtype]
+    c = Case(dtype, 16, [40, 20], [20, 1], seed=22)
+    c.d_table[0, 1] = c.num_pages
+    page2 = int(c.table[0, 2])
+    before = c.cache.clone()
+    kv = c.on(c.normal(c.T, c.W))
+    m.paged_append(c.batch(), kv)
+    flagged(m, 1 << 7)
+    i = torch.int16 if dtype == "bf16" else torch.int32
+    changed = (c.cache.view(i) != before.view(i)).flatten(1).any(1).nonzero().flatten().tolist()
+    assert changed == sorted([page2, int(c.table[1, 1])])
+
+
+# ---- selection ----------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype,page,lens,tq,top_k,first,last", [
+    ("fp32", 16, [700, 90, 16], [3, 2, 1], 8, 1, 2), ("bf16", 16, [700, 90, 16], [3, 2, 1], 8, 1, 2),
+    ("bf16", 16, [9000, 3000], [1, 1], 64, 0, 1), ("bf16", 64, [9000], [70], 16, 2, 3),
+    ("bf16", 16, [2100, 2000], [130, 5], 1, 0, 1), ("bf16", 32, [5000], [2], 7, 3, 4),
+    ("bf16", 16, [16 * 300], [1], 200, 1, 1)])
+def test_select(mods, dtype, page, lens, tq, top_k, first, last):
+    m = mods[dtype]
+    c = Case(dtype, page, lens, tq, seed=top_k + page, pad=2)
+    means = c.normal(c.num_pages, c.W) * 0.3
+    blocks = torch.full((c.T + 2, top_k), -9, dtype=torch.int32, device="cuda")
+    m.paged_select(c.batch(), c.q_abs, c.q_rope, c.summaries(means).cuda(), top_k, first, last, blocks)
+    ok(m)
+    assert torch.equal(blocks[:c.T].cpu(), c.select(means, top_k, first, last))
+    assert (blocks[c.T:] == -9).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_select_ties_and_empty_summaries(mods, dtype):
+    m = mods[dtype]
+    c = Case(dtype, 16, [16 * 150, 16 * 40], [2, 1], seed=30)
+    means = c.normal(3, c.W)[torch.arange(c.num_pages) % 3]             # three kinds of pages: ties everywhere
+    means[c.table[0, 7].long()] = 0
+    means[c.table[0, 9].long(), 3] = float("inf")                       # scale 0, codes 0
+    for top_k, first, last in ((20, 1, 1), (100, 0, 2), (3, 0, 1)):
+        got = m.paged_select(c.batch(), c.q_abs, c.q_rope, c.summaries(means).cuda(), top_k, first, last)
+        ok(m)
+        assert torch.equal(got.cpu(), c.select(means, top_k, first, last))
+    c.q[:] = 0                                                          # nothing to tell them apart
+    got = m.paged_select(c.batch(), c.q_abs, c.q_rope, c.summaries(means).cuda(), 20, 1, 2)
+    ok(m)
+    assert torch.equal(got.cpu(), c.select(means, 20, 1, 2))
+
+
+# ---- together -----------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_a_prompt_in_chunks_then_decode_steps(mods, dtype):
+    """Chunks of a prompt, then single tokens: append, choose blocks, attend, with the cache and the summaries
+    carried along; every step against the float64 form over the rows that the cache holds."""
+    m = mods[dtype]
+    page, top_k = 16, 6
+    c = Case(dtype, page, [150, 90], [150, 90], seed=40)
+    d = c.dims
+    c.cache.fill_(NAN)
+    sums = m.new_summaries(c.num_pages)
+    full = [c.normal(n, c.W) for n in c.lens]
+    at = [0, 0]
+    for new in ([100, 17], [30, 60], [1, 1], [1, 0], [1, 1], [17, 11]):
+        new = [min(n, len(full[b]) - at[b]) for b, n in enumerate(new)]
+        at = [a + n for a, n in zip(at, new)]
+        c.lens, c.tq, c.T = list(at), list(new), sum(new)
+        c.cu = torch.tensor([0] + new, dtype=torch.int64).cumsum(0)
+        c.d_cu, c.d_lens = c.cu.cuda(), torch.tensor(at, dtype=torch.int64, device="cuda")
+        c.q = c.normal(c.T, d.n_h, c.W)
+        kv = c.on(torch.cat([full[b][at[b] - n:at[b]] for b, n in enumerate(new)]))
+        q_rope = m.paged_append(c.batch(), kv, q_rope=c.q_rope, summaries=sums)
+        c.q[..., d.d_c:] = q_rope.double().cpu()
+        qa = c.q_abs
+        blocks = m.paged_select(c.batch(), qa, q_rope, sums, top_k, 1, 2)
+        o, lse = m.attn_paged_sparse(c.batch(), qa, q_rope, blocks)
+        o2, lse2 = m.attn_paged(c.batch(), qa, q_rope)
+        ok(m)
+        pool = c.cache.double().cpu()
+        c.rows = []
+        for b, n in enumerate(at):
+            pos = torch.arange(n)
+            c.rows.append(pool[c.table[b, pos // page].long(), pos % page])
+        means = (pool.sum(1) / page).float().double()                    # of whole pages; the others are forced
+        assert torch.equal(blocks.cpu(), c.select(torch.nan_to_num(means), top_k, 1, 2))
+        c.check_attention(o, lse, listed_rows(c, blocks.cpu()))
+        c.check_attention(o2, lse2, prefix(c))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_captured_steps_replay_on_new_lengths(mods, dtype):
+    """Two graphs of the same handle, captured one after the other and replayed in turn with other lengths,
+    tables and a batch that shrank (its last rows padded)."""
+    m = mods[dtype]
+    a, b = (Case(dtype, 32, [300, 64], [2, 2], seed=50 + k) for k in range(2))
+    state = []
+    for c in (a, b):
+        kv, qa, qr = c.on(c.normal(c.T, c.W)), c.q_abs, c.q_rope
+        sums, blocks = c.summaries(c.normal(c.num_pages, c.W)).cuda(), torch.empty(c.T, 4, dtype=torch.int32, device="cuda")
+        o, lse = torch.empty_like(qa), torch.empty(c.T, c.dims.n_h, device="cuda")
+        batch = c.batch()
+
+        def step(c=c, kv=kv, qa=qa, qr=qr, sums=sums, blocks=blocks, o=o, lse=lse, batch=batch):
+            m.paged_append(batch, kv, summaries=sums)
+            m.paged_select(batch, qa, qr, sums, 4, 1, 1, blocks)
+            m.attn_paged_sparse(batch, qa, qr, blocks, o, lse)
+        step()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        state.append((c, g, kv, qa, qr, sums, blocks, o, lse))
+    m.workspace(1 << 26)                                    # a larger call in between
+    for lens, tq in (([299, 64], [2, 2]), ([200, 33], [1, 2]), ([97, 50], [3, 0])):
+        for c, g, kv, qa, qr, sums, blocks, o, lse in state:
+            c.lens, c.tq, c.T = list(lens), list(tq), sum(tq)
+            c.cu = torch.tensor([0] + tq, dtype=torch.int64).cumsum(0)
+            c.d_cu.copy_(c.cu)
+            c.d_lens.copy_(torch.tensor(lens))
+            o.fill_(7.0)
+        for _, g, *_ in state:
+            g.replay()
+        torch.cuda.synchronize()
+        ok(m)
+        for c, g, kv, qa, qr, sums, blocks, o, lse in state:
+            pool = c.cache.double().cpu()
+            c.rows = [pool[c.table[s, torch.arange(n) // 32].long(), torch.arange(n) % 32] for s, n in enumerate(lens)]
+            c.check_attention(o, lse, listed_rows(c, blocks.cpu()))
+            assert (o[c.T:] == 7).all()
