@@ -6,6 +6,7 @@
 #include "handle.cuh"
 #include "mla.h"
 #include "paged.cuh"
+#include "tc_paged.cuh"
 
 namespace {
 
@@ -65,8 +66,11 @@ mla_status_t attention(mla_handle_t* h, const mla_paged_t* batch, const void* q_
   if (!g.ok) return MLA_ERR_CUDA;
   if ((s = ensure_device(h)) != MLA_OK) return s;
   const float scale = (float)(1.0 / sqrt((double)(h->dims.d_h + h->dims.d_r)));
-  return cuda_status(mla::paged_attention_simt(v, tc_dims(h), q_abs, q_rope, blocks, top_k, scale, o_lat, lse, h->d_err,
-                                               (cudaStream_t)stream));
+  if (tc_dims(h))
+    return cuda_status(mla::tc_paged_attention(v, q_abs, q_rope, blocks, top_k, scale, o_lat, lse, ws, h->num_sms,
+                                               h->d_err, (cudaStream_t)stream));
+  return cuda_status(
+      mla::paged_attention_simt(v, q_abs, q_rope, blocks, top_k, scale, o_lat, lse, h->d_err, (cudaStream_t)stream));
 }
 
 }  // namespace
@@ -100,7 +104,7 @@ mla_status_t mla_paged_append(mla_handle_t* h, const mla_paged_t* batch, const v
 
 mla_status_t mla_attn_paged_workspace(const mla_handle_t* h, int64_t B, int64_t total_q, size_t* bytes) {
   if (!h || !bytes || B <= 0 || total_q <= 0) return MLA_ERR_INVALID_ARG;
-  *bytes = 0;
+  *bytes = tc_dims(h) ? mla::tc_paged_attention_bytes(total_q) : 0;
   return MLA_OK;
 }
 

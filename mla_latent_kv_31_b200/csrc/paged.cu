@@ -111,10 +111,9 @@ __global__ void __launch_bounds__(256)
 constexpr int ATT = 128;
 constexpr int ATT_MAX_DV = 512;
 
-template <typename T>
 __global__ void __launch_bounds__(ATT)
-    paged_attention_kernel(PagedView v, const T* q_abs, const T* q_rope, const int32_t* blocks, int32_t top_k,
-                           float scale, T* o_lat, float* lse, uint32_t* err) {
+    paged_attention_kernel(PagedView v, const float* q_abs, const float* q_rope, const int32_t* blocks, int32_t top_k,
+                           float scale, float* o_lat, float* lse, uint32_t* err) {
   __shared__ float qs[1024];
   __shared__ float ps[ATT];
   __shared__ int64_t row_of[ATT];
@@ -130,9 +129,9 @@ __global__ void __launch_bounds__(ATT)
   if (list) n = tok.pos < 0 ? 0 : paged_list_rows(list, top_k, tok.pos, v.page, list_scratch, err);
   const int64_t oq = t * v.n_h + head;
   for (int c = tid; c < W; c += ATT)
-    qs[c] = c < v.d_c ? to_f(q_abs[oq * v.d_c + c]) : to_f(q_rope[oq * v.d_r + c - v.d_c]);
+    qs[c] = c < v.d_c ? q_abs[oq * v.d_c + c] : q_rope[oq * v.d_r + c - v.d_c];
   __syncthreads();
-  const T* rows = reinterpret_cast<const T*>(v.cache);
+  const float* rows = reinterpret_cast<const float*>(v.cache);
   float m = -INFINITY, l = 0.f;
   float acc[ATT_MAX_DV / ATT] = {};
   for (int64_t c0 = 0; c0 < n; c0 += ATT) {
@@ -145,8 +144,8 @@ __global__ void __launch_bounds__(ATT)
       float d = 0.f;                  // a page outside the pool counts as rows of zeros
       if (page >= 0) {
         row_of[tid] = page * v.page + j % v.page;
-        const T* k = rows + row_of[tid] * W;
-        for (int c = 0; c < W; ++c) d = fmaf(qs[c], to_f(k[c]), d);
+        const float* k = rows + row_of[tid] * W;
+        for (int c = 0; c < W; ++c) d = fmaf(qs[c], k[c], d);
       }
       s = d * scale;
     }
@@ -162,11 +161,11 @@ __global__ void __launch_bounds__(ATT)
     for (int jj = 0; jj < cnt; ++jj) {
       if (row_of[jj] < 0) continue;
       const float pj = ps[jj];
-      const T* vr = rows + row_of[jj] * W;
+      const float* vr = rows + row_of[jj] * W;
 #pragma unroll
       for (int i = 0; i < ATT_MAX_DV / ATT; ++i) {
         const int c = tid + i * ATT;
-        if (c < v.d_c) acc[i] = fmaf(pj, to_f(vr[c]), acc[i]);
+        if (c < v.d_c) acc[i] = fmaf(pj, vr[c], acc[i]);
       }
     }
     m = m_new;
@@ -176,7 +175,7 @@ __global__ void __launch_bounds__(ATT)
 #pragma unroll
   for (int i = 0; i < ATT_MAX_DV / ATT; ++i) {
     const int c = tid + i * ATT;
-    if (c < v.d_c) o_lat[oq * v.d_c + c] = from_f<T>(acc[i] * inv);
+    if (c < v.d_c) o_lat[oq * v.d_c + c] = acc[i] * inv;
   }
   if (tid == 0) lse[oq] = n > 0 ? m + logf(l) : -INFINITY;
 }
@@ -336,15 +335,6 @@ cudaError_t append_launch(const PagedView& v, const void* kv, int64_t kv_stride,
   return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t attention_launch(const PagedView& v, const void* q_abs, const void* q_rope, const int32_t* blocks,
-                             int32_t top_k, float scale, void* o_lat, float* lse, uint32_t* err, cudaStream_t st) {
-  paged_attention_kernel<T><<<dim3((unsigned)v.total_q, (unsigned)v.n_h), ATT, 0, st>>>(
-      v, (const T*)q_abs, (const T*)q_rope, blocks, top_k, scale, (T*)o_lat, lse, err);
-  note_launch();
-  return cudaGetLastError();
-}
-
 }  // namespace
 
 size_t summary_pitch(int32_t d_c, int32_t d_r) { return align16((size_t)d_c + d_r + 4); }
@@ -356,11 +346,12 @@ cudaError_t paged_append(const PagedView& v, bool bf16, const void* kv, int64_t 
               : append_launch<float>(v, kv, kv_stride, q_rope, q_out, summaries, o, rope, err, st);
 }
 
-cudaError_t paged_attention_simt(const PagedView& v, bool bf16, const void* q_abs, const void* q_rope,
-                                 const int32_t* blocks, int32_t top_k, float scale, void* o_lat, float* lse,
-                                 uint32_t* err, cudaStream_t st) {
-  return bf16 ? attention_launch<__nv_bfloat16>(v, q_abs, q_rope, blocks, top_k, scale, o_lat, lse, err, st)
-              : attention_launch<float>(v, q_abs, q_rope, blocks, top_k, scale, o_lat, lse, err, st);
+cudaError_t paged_attention_simt(const PagedView& v, const void* q_abs, const void* q_rope, const int32_t* blocks,
+                                 int32_t top_k, float scale, void* o_lat, float* lse, uint32_t* err, cudaStream_t st) {
+  paged_attention_kernel<<<dim3((unsigned)v.total_q, (unsigned)v.n_h), ATT, 0, st>>>(
+      v, (const float*)q_abs, (const float*)q_rope, blocks, top_k, scale, (float*)o_lat, lse, err);
+  note_launch();
+  return cudaGetLastError();
 }
 
 size_t paged_select_bytes(int32_t n_h, int32_t d_c, int32_t d_r, int64_t total_q, int64_t max_pages) {

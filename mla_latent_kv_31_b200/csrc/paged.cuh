@@ -95,8 +95,8 @@ cudaError_t paged_append(const PagedView& v, bool bf16, const void* kv, int64_t 
                          void* q_out, void* summaries, const LayerOpts& o, const RopeTable& rope, uint32_t* err,
                          cudaStream_t st);
 
-// o_lat and lse of the new tokens by CUDA cores, over all rows (blocks == nullptr) or the listed blocks.
-cudaError_t paged_attention_simt(const PagedView& v, bool bf16, const void* q_abs, const void* q_rope,
+// o_lat and lse of the new tokens in fp32 by CUDA cores, over all rows (blocks == nullptr) or the listed blocks.
+cudaError_t paged_attention_simt(const PagedView& v, const void* q_abs, const void* q_rope,
                                  const int32_t* blocks, int32_t top_k, float scale, void* o_lat, float* lse,
                                  uint32_t* err, cudaStream_t st);
 

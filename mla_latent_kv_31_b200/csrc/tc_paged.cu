@@ -1,0 +1,824 @@
+// Attention over the paged latent cache at the DeepSeek-V3 sizes (n_h = 128, d_c = 512, d_h^R = 64): bf16,
+// fp32 accumulation, tcgen05 + TMA. For new token t of sequence b and head i, over the rows j that t sees
+// (0 .. pos, or those of its chosen blocks):
+//   s_j = (q~_t,i . c_j + q^R_t,i . k^R_j) / sqrt(d_h + d_r),  o_t,i = sum_j softmax(s)_j c_j,  lse = log sum_j e^{s_j}.
+//
+// Shape of the work. One token's 128 heads against 256 keys at a time, by a pair of CTAs (cta_group::2, M = 128:
+// 64 heads in each SM). O = P.C for 64 heads x 512 latent columns is 256 TMEM columns of each SM (an
+// M = 128 pair accumulator keeps columns [0, N/2) in lanes 0-63 and [N/2, N) in lanes 64-127), which leaves
+// 256 columns for two score buffers of 64 heads x 256 keys. So softmax, P and O of a head stay in one SM
+// and nothing but the shared B operands crosses between the two: each CTA loads half of the keys for QK^T
+// (128 keys x 576) and half of the latent columns for P.V (256 keys x 256): 272 KB per 256 keys, against
+// 16 x 36 and 2 x 16 x 4 MMAs of N = 256. (An M = 128 pair MMA takes 78 cycles at N = 256 and 68 at N = 128,
+// measured: the 256-key step is what keeps the tensor cores near their rate.)
+//
+// Work split. Tokens are cut into units of 64 keys; all units of all tokens, plus a fixed cost per token,
+// are dealt to the pairs in equal contiguous ranges. A token that lies in one range is written by its pair; one
+// that crosses ranges leaves an unnormalised fp32 partial per range, merged exactly by combine_kernel.
+//
+// Pages. A step's 256 keys are 16 groups of 16 keys; each group's row in the pool comes from the block table (and
+// the token's block list). TMA boxes are 64, 32 or 16 rows high, the largest that divides the page size, so a
+// box never crosses a page; boxes past the last visible key read out of range, which fills zeros. Rows between the
+// last visible key and its box's end may hold anything, even NaN: their scores are masked, and their value
+// rows (at most two ring entries of a token's last step) are zeroed in shared memory before P.V.
+//
+// Roles (512 threads): warp 0 fills the ring of 16 KB entries in the order the MMAs take them (K of step j + 1
+// before V of step j); warp 1 of the leader CTA issues the MMAs; warp 2 loads a token's queries; warps 4-11 are
+// the softmax (thread = TMEM lane, two warps per lane quarter, 64 keys each) and rescale O when the running
+// maximum has grown by 2^8; warps 12-15 write O out while the next token's first step runs.
+// Every wait is bounded (a timeout sets the error word and the role returns).
+#include <cuda_bf16.h>
+#include <string.h>
+
+#include "paged.cuh"
+#include "sm100.cuh"
+#include "tc_gemm.cuh"
+#include "tc_paged.cuh"
+
+namespace mla {
+namespace {
+
+using namespace sm100;
+
+constexpr int H = 128, DC = 512, DR = 64;
+constexpr int HC = H / 2;                      // heads per CTA
+constexpr int NK = 256;                        // keys per step
+constexpr int UNIT = 64;                       // keys per unit of the work split
+constexpr int GROUPS = NK / 16;
+constexpr int kThreads = 512;
+constexpr int kMaxPairs = 74;
+constexpr int kStartUnits = 4;                 // a token's fixed cost (query load, epilogue), in units
+constexpr float kRescaleLog2 = 8.f;            // keep the running maximum until it grows by 2^8
+constexpr int kIssuers = 4;                    // TMA issuing lanes
+constexpr int kEntriesK = 9, kEntriesV = 8;    // ring entries of a step: [128 keys x 64], 2 x [64 keys x 64]
+constexpr int RING = 7;
+constexpr uint32_t ENTRY = 16384, BOX = 8192;
+constexpr uint32_t Q_BYTES = HC * (DC + DR) * 2;
+constexpr uint32_t P_BYTES = HC * NK * 2;
+
+constexpr uint32_t OFF_RED = 512;                                  // [2][4][64] floats: maxima of the four key blocks
+constexpr uint32_t OFF_STAT = OFF_RED + 2 * 4 * HC * 4;            // [5][64] floats: sums of the four key blocks, maximum
+constexpr uint32_t OFF_COORD = OFF_STAT + 5 * HC * 4;              // [4][16] row coordinates of the steps ahead
+constexpr uint32_t OFF_Q = 4096;
+constexpr uint32_t OFF_P = OFF_Q + Q_BYTES;
+constexpr uint32_t OFF_RING = OFF_P + P_BYTES;
+constexpr uint32_t SMEM_BYTES = OFF_RING + RING * ENTRY + 1024;
+static_assert(OFF_COORD + 4 * GROUPS * 4 <= OFF_Q, "statistics block");
+static_assert(OFF_Q % 1024 == 0 && OFF_P % 1024 == 0 && OFF_RING % 1024 == 0, "swizzle atom alignment");
+static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+
+enum : int {
+  B_FULL = 0,                 // [RING] entry landed in both CTAs (leader; 1 + bytes)
+  B_EMPTY = B_FULL + RING,    // [RING] entry's MMAs done (both CTAs)
+  B_SFULL = B_EMPTY + RING,   // [2] scores ready (both CTAs)
+  B_SFREE = B_SFULL + 2,      // [2] scores read (leader; 16 warps)
+  B_PRDY = B_SFREE + 2,       // P written, O rescaled (leader; 16 warps)
+  B_PVD = B_PRDY + 1,         // P.V of a step done (both CTAs)
+  B_QFULL = B_PVD + 1,        // a token's queries landed in both CTAs (leader; 1 + bytes)
+  B_QEMPTY = B_QFULL + 1,     // a token's last QK^T done (both CTAs)
+  B_TMAX = B_QEMPTY + 1,      // [2] the four softmax warps of a block of 32 heads
+  B_TAIL = B_TMAX + 2,        // the two entries with the last visible key landed in this CTA (2 + bytes)
+  B_TRDY = B_TAIL + 1,        // ... and their rows behind it zeroed (leader; 16 warps)
+  B_ODONE = B_TRDY + 1,       // a token's last P.V done (both CTAs)
+  B_OFREE = B_ODONE + 1,      // O read out (leader; 8 warps)
+  B_LRDY = B_OFREE + 1,       // a token's sums and maxima written (8 warps)
+  B_LFREE = B_LRDY + 1,       // ... and read (4 warps)
+  NBAR = B_LFREE + 1
+};
+static_assert(NBAR * 8 + 16 <= OFF_RED, "barrier block");
+
+struct CoreParams {
+  CUtensorMap kvmap;          // the pool as [rows, 576], box {64, gran}
+  CUtensorMap qmap, qrmap;    // q~ [T * 128, 512], q^R [T * 128, 64], box {64, 64}
+  PagedView v;
+  const int32_t* blocks;      // [T, top_k] chosen blocks; nullptr: all rows
+  int32_t top_k, gran, pairs;
+  const int2* tinfo;          // [T]: sequence, visible rows
+  const int4* pinfo;          // [pairs]: first token, its first unit, last token, its end unit
+  __nv_bfloat16* o_lat;
+  float* lse;
+  float4* part_o;             // [2 * pairs][DC / 4][H]
+  float2* part_ml;            // [2 * pairs][H]: maximum (natural units), sum
+  float scale_log2;
+  uint32_t* err;
+};
+
+// ---- pairs of CTAs ------------------------------------------------------------------------------------------
+__device__ __forceinline__ void pair_alloc(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void pair_relinquish() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// D (+)= A . B^T over both CTAs; the descriptors hold the same offsets in both.
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// One arrival on the barrier at this offset in both CTAs once the MMAs issued so far are done.
+__device__ __forceinline__ void pair_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// A TMA load into this CTA that counts its bytes on `bar`, a barrier of either CTA (cluster address).
+__device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
+      "[%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait_cluster(bar, parity)) return true;
+    if (globaltimer() - t0 > kWaitTimeoutNs) return false;
+  }
+}
+
+// The tokens of a pair's range, and of each the keys [k0, k1) that fall into it.
+struct Walk {
+  const int2* tinfo;
+  int tok, tok1, e1;
+  int seq, vis, k0, k1;
+  __device__ void load(int u) {
+    const int2 ti = tinfo[tok];
+    seq = ti.x;
+    vis = ti.y;
+    k0 = u * UNIT;
+    k1 = tok == tok1 ? min(vis, e1 * UNIT) : vis;
+  }
+  __device__ void init(const CoreParams& p, int4 pi) {
+    tinfo = p.tinfo;
+    tok = pi.x; tok1 = pi.z; e1 = pi.w;
+    if (valid()) load(pi.y);
+  }
+  __device__ bool valid() const { return tok >= 0 && tok <= tok1; }
+  __device__ void next() {
+    do {
+      ++tok;
+      if (tok > tok1) return;
+      load(0);
+    } while (vis <= 0);
+  }
+  __device__ int steps() const { return (k1 - k0 + NK - 1) / NK; }
+  __device__ bool whole() const { return k0 == 0 && k1 == vis; }
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    paged_core_kernel(const __grid_constant__ CoreParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_addr(smem);
+  auto bar = [&](int i) { return sbase + 8u * (uint32_t)i; };
+  const uint32_t tmem_slot = sbase + 8 * NBAR;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t r = cluster_rank();
+  const int pair = blockIdx.x >> 1;
+  auto lead = [&](int i) { return map_peer(bar(i), 0); };
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NBAR; ++i) {
+      uint32_t cnt = 1;
+      if (i == B_SFREE || i == B_SFREE + 1 || i == B_PRDY || i == B_TRDY) cnt = 16;
+      else if (i == B_TMAX || i == B_TMAX + 1 || i == B_LFREE) cnt = 4;
+      else if (i == B_TAIL) cnt = 2;
+      else if (i == B_OFREE || i == B_LRDY) cnt = 8;
+      mbar_init(bar(i), cnt);
+    }
+    fence_mbar_init();
+    prefetch_tmap(&p.kvmap);
+    prefetch_tmap(&p.qmap);
+    prefetch_tmap(&p.qrmap);
+  }
+  if (warp == 1) {
+    pair_alloc(tmem_slot, 512);
+    pair_relinquish();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<const uint32_t*>(smem + 8 * NBAR);
+  Walk w;
+  w.init(p, p.pinfo[pair]);
+  bool ok = true;
+
+  if (warp == 0) {
+    // -------------------------------------------------------------- ring producer
+    int32_t* coord = reinterpret_cast<int32_t*>(smem + OFF_COORD);
+    const int g = lane & (GROUPS - 1);
+    // pool row of the group's first key of the step at k, or a row out of range (read as zeros)
+    auto row_of = [&](const Walk& a, int k) -> int32_t {
+      const int j = k + 16 * g;
+      if (j >= a.k1) return -4096;
+      const int i = j / p.v.page;
+      const int64_t blk = p.blocks ? p.blocks[(int64_t)a.tok * p.top_k + i] : i;
+      const int64_t pg = paged_page(p.v, a.seq, blk, p.err);
+      return pg < 0 ? -4096 : (int32_t)(pg * p.v.page + j % p.v.page);
+    };
+    int n = 0, last = -1, js = 0;
+    // entry n: this lane's if its turn; waits for the slot and announces its bytes
+    auto take = [&](bool tail, uint32_t* dst, uint32_t* b) -> bool {
+      const int cur = n++;
+      if (!ok || (cur & (kIssuers - 1)) != lane) return false;
+      const int slot = cur % RING;
+      if (!mbar_wait(bar(B_EMPTY + slot), ((cur / RING) & 1) ^ 1)) { ok = false; return false; }
+      *dst = sbase + OFF_RING + slot * ENTRY;
+      if (tail) {
+        // counted in this CTA, whose softmax warps zero rows of it before P.V takes it
+        mbar_expect_tx(bar(B_TAIL), ENTRY);
+        *b = bar(B_TAIL);
+        if (r == 0) mbar_arrive(bar(B_FULL + slot));
+      } else {
+        if (r == 0) mbar_expect_tx(bar(B_FULL + slot), 2 * ENTRY);
+        *b = lead(B_FULL + slot);
+        last = cur;
+      }
+      return true;
+    };
+    auto load_v = [&](const int32_t* c, int tail_kq) {
+      for (int e = 0; e < kEntriesV; ++e) {
+        uint32_t dst, b;
+        const int kq = e >> 1, x = 256 * (e & 1) + 128 * (int)r;
+        if (!take(kq == tail_kq, &dst, &b)) continue;
+        for (int s = 0; s < 64; s += p.gran) {
+          const int32_t y = c[(64 * kq + s) >> 4];
+          pair_load(dst + s * 128, &p.kvmap, x, y, b);
+          pair_load(dst + BOX + s * 128, &p.kvmap, x + 64, y, b);
+        }
+      }
+    };
+    if (w.valid()) {
+      const int32_t c0 = row_of(w, w.k0);
+      if (lane < GROUPS) coord[g] = c0;
+    }
+    __syncwarp();
+    for (; w.valid(); ) {
+      Walk nx = w;
+      nx.next();
+      const int ns = w.steps();
+      for (int j = 0; j < ns; ++j, ++js) {
+        const int32_t* c = coord + (js & 3) * GROUPS;
+        // the next step's rows come in while this step's entries are issued
+        int32_t ahead = -4096;
+        if (j + 1 < ns) ahead = row_of(w, w.k0 + (j + 1) * NK);
+        else if (nx.valid()) ahead = row_of(nx, nx.k0);
+        for (int e = 0; e < kEntriesK; ++e) {
+          uint32_t dst, b;
+          if (!take(false, &dst, &b)) continue;
+          for (int s = 0; s < 128; s += p.gran)
+            pair_load(dst + s * 128, &p.kvmap, 64 * e, c[(128 * (int)r + s) >> 4], b);
+        }
+        if (j > 0) load_v(coord + ((js - 1) & 3) * GROUPS, -1);
+        if (j == ns - 1) {
+          const int rem = w.k1 - (w.k0 + j * NK);
+          load_v(c, rem % 64 ? rem / 64 : -1);
+        }
+        __syncwarp();
+        if (lane < GROUPS) coord[((js + 1) & 3) * GROUPS + g] = ahead;
+        ok = __all_sync(0xffffffffu, ok) != 0;
+        if (!ok) break;
+      }
+      if (!ok) break;
+      w = nx;
+    }
+    if (!ok) {
+      if (lane == 0) flag_error(p.err, DEVERR_TIMEOUT);
+      // this lane's entries still in flight (of both CTAs, seen at the leader's barriers)
+      if (r == 0 && lane < kIssuers)
+        for (int i = max(lane, last - RING + 1); i <= last; ++i)
+          if ((i & (kIssuers - 1)) == lane) mbar_wait(bar(B_FULL + i % RING), (i / RING) & 1);
+    }
+  } else if (warp == 1) {
+    // -------------------------------------------------------------- MMA issuer (leader CTA)
+    if (r == 0 && lane == 0) {
+      constexpr uint32_t id_qk = idesc_bf16(128, NK, 0, 0), id_pv = idesc_bf16(128, 256, 0, 1);
+      int n = 0, js = 0, gpc = 0, tails = 0;  // ring index, step, token, tokens that end inside 64 keys
+      auto qk = [&](int j) -> bool {
+        const int sb = j & 1;
+        if (!wait_cluster(bar(B_SFREE + sb), ((j >> 1) & 1) ^ 1)) return false;
+        tc_fence_after();
+        const uint32_t d = tmem + 256 + 128 * sb;
+        for (int e = 0; e < kEntriesK; ++e, ++n) {
+          const int slot = n % RING;
+          if (!wait_cluster(bar(B_FULL + slot), (n / RING) & 1)) return false;
+          tc_fence_after();
+          const uint64_t a = sw128_desc(sbase + OFF_Q + e * BOX, 0, 1024);
+          const uint64_t b = sw128_desc(sbase + OFF_RING + slot * ENTRY, 0, 1024);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) pair_mma(d, a + 2 * kk, b + 2 * kk, id_qk, (e | kk) ? 1u : 0u);
+          pair_commit(bar(B_EMPTY + slot));
+        }
+        pair_commit(bar(B_SFULL + sb));
+        return true;
+      };
+      auto pv = [&](int j, bool first, int tail_kq) -> bool {
+        if (!wait_cluster(bar(B_PRDY), j & 1)) return false;
+        if (first && !wait_cluster(bar(B_OFREE), (gpc & 1) ^ 1)) return false;
+        tc_fence_after();
+        for (int e = 0; e < kEntriesV; ++e, ++n) {
+          const int slot = n % RING, kq = e >> 1;
+          if (!wait_cluster(bar(B_FULL + slot), (n / RING) & 1)) return false;
+          if (kq == tail_kq && (e & 1) == 0 && !wait_cluster(bar(B_TRDY), tails++ & 1)) return false;
+          tc_fence_after();
+          const uint64_t a = sw128_desc(sbase + OFF_P + kq * BOX, 0, 1024);
+          const uint64_t b = sw128_desc(sbase + OFF_RING + slot * ENTRY, BOX, 1024);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            pair_mma(tmem + 128 * (e & 1), a + 2 * kk, b + 128 * kk, id_pv, (first && kq == 0 && kk == 0) ? 0u : 1u);
+          pair_commit(bar(B_EMPTY + slot));
+        }
+        pair_commit(bar(B_PVD));
+        return true;
+      };
+      for (; ok && w.valid(); w.next(), ++gpc) {
+        const int ns = w.steps();
+        ok = wait_cluster(bar(B_QFULL), gpc & 1);
+        tc_fence_after();
+        for (int j = 0; ok && j < ns; ++j) {
+          ok = qk(js + j);
+          if (ok && j == ns - 1) pair_commit(bar(B_QEMPTY));
+          if (ok && j > 0) ok = pv(js + j - 1, j == 1, -1);
+        }
+        const int rem = w.k1 - (w.k0 + (ns - 1) * NK);
+        if (ok) ok = pv(js + ns - 1, ns == 1, rem % 64 ? rem / 64 : -1);
+        if (ok) pair_commit(bar(B_ODONE));
+        js += ns;
+      }
+      if (!ok) flag_error(p.err, DEVERR_TIMEOUT);
+    }
+  } else if (warp == 2) {
+    // -------------------------------------------------------------- queries
+    if (lane == 0) {
+      int gpc = 0;
+      for (; w.valid(); w.next(), ++gpc) {
+        if (!mbar_wait(bar(B_QEMPTY), (gpc & 1) ^ 1)) { ok = false; break; }
+        if (r == 0) mbar_expect_tx(bar(B_QFULL), 2 * Q_BYTES);
+        const int32_t y = w.tok * H + HC * (int)r;
+        for (int c = 0; c < 8; ++c) pair_load(sbase + OFF_Q + c * BOX, &p.qmap, 64 * c, y, lead(B_QFULL));
+        pair_load(sbase + OFF_Q + 8 * BOX, &p.qrmap, 0, y, lead(B_QFULL));
+      }
+      if (!ok) flag_error(p.err, DEVERR_TIMEOUT);
+      if (!ok && r == 0 && gpc > 0) mbar_wait(bar(B_QFULL), (gpc - 1) & 1);
+    }
+  } else if (warp >= 4 && warp < 12) {
+    // -------------------------------------------------------------- softmax
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    const int i = (32 * quarter + lane) & (HC - 1);          // head of this CTA
+    const int kq = 2 * (quarter >> 1) + half;                // this warp's block of 64 keys
+    const int rb = quarter & 1;                              // block of 32 heads
+    const uint32_t trow = tmem + ((uint32_t)(32 * quarter) << 16);
+    float* red = reinterpret_cast<float*>(smem + OFF_RED);
+    float* stat = reinterpret_cast<float*>(smem + OFF_STAT);
+    const float c2 = p.scale_log2, thr = kRescaleLog2 / c2;
+    const uint32_t sfree = lead(B_SFREE), prdy = lead(B_PRDY), trdy = lead(B_TRDY);
+    auto wait_u = [&](uint32_t b, uint32_t par) { return __all_sync(0xffffffffu, mbar_wait(b, par)) != 0; };
+    int js = 0, gpc = 0, tails = 0, nbase = 0;
+    for (; ok && w.valid(); w.next(), ++gpc) {
+      const int ns = w.steps();
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < ns; ++j, ++js) {
+        const int sb = js & 1;
+        const int rem = w.k1 - (w.k0 + j * NK);              // visible keys from the step's first on
+        if (!wait_u(bar(B_SFULL + sb), (js >> 1) & 1)) { ok = false; break; }
+        tc_fence_after();
+        float s[64];
+        tmem_ld32(trow + 256 + 128 * sb + 64 * half, reinterpret_cast<uint32_t*>(s));
+        tmem_ld32(trow + 256 + 128 * sb + 64 * half + 32, reinterpret_cast<uint32_t*>(s) + 32);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(sfree + 8 * sb);
+        const int nvis = rem - 64 * kq;
+        if (nvis < 64) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) s[c] = c < nvis ? s[c] : -INFINITY;
+        }
+        float mx[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) mx[c] = fmaxf(fmaxf(s[4 * c], s[4 * c + 1]), fmaxf(s[4 * c + 2], s[4 * c + 3]));
+#pragma unroll
+        for (int k = 8; k > 0; k >>= 1)
+#pragma unroll
+          for (int c = 0; c < k; ++c) mx[c] = fmaxf(mx[c], mx[c + k]);
+        float* rbuf = red + sb * 4 * HC;
+        rbuf[kq * HC + i] = mx[0];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_TMAX + rb));
+        if (!wait_u(bar(B_TMAX + rb), js & 1)) { ok = false; break; }
+        const float top = fmaxf(fmaxf(rbuf[i], rbuf[HC + i]), fmaxf(rbuf[2 * HC + i], rbuf[3 * HC + i]));
+        // the four threads of a head see the same maxima, so they take the same decision
+        float alpha = 1.f;
+        if (top > -INFINITY && (m == -INFINITY || top > m + thr)) {
+          alpha = m == -INFINITY ? 0.f : ex2_approx((m - top) * c2);
+          l *= alpha;
+          m = top;
+        }
+        uint32_t pk[32];
+        if (m > -INFINITY) {
+          const uint64_t cc = f2_pack(c2, c2), off = f2_pack(-m * c2, -m * c2);
+          uint64_t acc[8];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            float a0, a1;
+            f2_unpack(f2_fma(f2_pack(s[2 * c], s[2 * c + 1]), cc, off), a0, a1);
+            const float e0 = ex2_approx(a0), e1 = ex2_approx(a1);
+            // P in bf16 for the MMA (2^-8 of each weight); the sum takes the unrounded weights
+            pk[c] = pack_bf16(e0, e1);
+            const uint64_t le = f2_pack(e0, e1);
+            if (c < 8) acc[c] = le;
+            else acc[c & 7] = f2_add(acc[c & 7], le);
+          }
+#pragma unroll
+          for (int k = 4; k > 0; k >>= 1)
+#pragma unroll
+            for (int c = 0; c < k; ++c) acc[c] = f2_add(acc[c], acc[c + k]);
+          float l0, l1;
+          f2_unpack(acc[0], l0, l1);
+          l += l0 + l1;
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) pk[c] = 0u;
+        }
+        // P.V of the step before is done: P may be overwritten and O rescaled
+        if (js > 0 && !wait_u(bar(B_PVD), (js - 1) & 1)) { ok = false; break; }
+        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 128 * half; c < 128 * half + 128; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(trow + c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+            tmem_st32(trow + c, v);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        uint8_t* prow = smem + OFF_P + kq * BOX + i * 128;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(prow + ((c ^ (i & 7)) << 4)) =
+              make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(prdy);
+        if (j == ns - 1 && rem % 64) {
+          // value rows behind the last visible key: zeros, since 0 * NaN is not 0
+          if (!wait_u(bar(B_TAIL), tails & 1)) { ok = false; break; }
+          ++tails;
+          const int tail_kq = rem / 64, row0 = rem % 64;
+          const int e0 = nbase + kEntriesK * ns + kEntriesV * (ns - 1) + 2 * tail_kq;
+          for (int q = threadIdx.x - 128; q < 2 * 64 * 16; q += 256) {
+            const int e = q >> 10, row = (q >> 4) & 63, c16 = q & 15;
+            if (row < row0) continue;
+            uint8_t* ent = smem + OFF_RING + ((e0 + e) % RING) * ENTRY + (c16 >> 3) * BOX;
+            *reinterpret_cast<uint4*>(ent + row * 128 + (c16 & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) arrive_cluster(trdy);
+        }
+      }
+      if (!ok) break;
+      nbase += (kEntriesK + kEntriesV) * ns;
+      if (!wait_u(bar(B_LFREE), (gpc & 1) ^ 1)) { ok = false; break; }
+      stat[kq * HC + i] = l;
+      if (kq == 0) stat[4 * HC + i] = m;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_LRDY));
+    }
+    if (!ok && lane == 0) flag_error(p.err, DEVERR_TIMEOUT);
+  } else if (warp >= 12) {
+    // -------------------------------------------------------------- outputs
+    const int quarter = warp & 3;
+    const int i = (32 * quarter + lane) & (HC - 1), head = HC * (int)r + i;
+    const int col0 = 128 * (quarter >> 1);
+    const uint32_t trow = tmem + ((uint32_t)(32 * quarter) << 16);
+    const float* stat = reinterpret_cast<const float*>(smem + OFF_STAT);
+    const uint32_t ofree = lead(B_OFREE);
+    auto wait_u = [&](uint32_t b, uint32_t par) { return __all_sync(0xffffffffu, mbar_wait(b, par)) != 0; };
+    int gpc = 0;
+    for (; ok && w.valid(); w.next(), ++gpc) {
+      if (!wait_u(bar(B_LRDY), gpc & 1)) { ok = false; break; }
+      const float l = (stat[i] + stat[HC + i]) + (stat[2 * HC + i] + stat[3 * HC + i]);
+      const float m = stat[4 * HC + i] * p.scale_log2 * 0.69314718055994531f;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_LFREE));
+      if (!wait_u(bar(B_ODONE), gpc & 1)) { ok = false; break; }
+      tc_fence_after();
+      const bool whole = w.whole();
+      const int64_t row = (int64_t)w.tok * H + head;
+      const int slot = 2 * pair + (gpc > 0 ? 1 : 0);
+      if (quarter < 2) {
+        if (whole) p.lse[row] = l == 0.f ? -INFINITY : m + logf(l);
+        else p.part_ml[(int64_t)slot * H + head] = make_float2(l == 0.f ? -INFINITY : m, l);
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      uint4* dst = reinterpret_cast<uint4*>(p.o_lat + row * DC + col0);
+      float4* part = p.part_o + ((int64_t)slot * (DC / 4) + col0 / 4) * H + head;
+#pragma unroll 1
+      for (int c = 0; c < 256; c += 32) {
+        uint32_t v[32];
+        tmem_ld32(trow + c, v);
+        tmem_wait_ld();
+        const int lat = (c & 127) + 256 * (c >> 7);          // latent column - col0
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t u[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              u[k] = pack_bf16(__uint_as_float(v[8 * e + 2 * k]) * inv, __uint_as_float(v[8 * e + 2 * k + 1]) * inv);
+            dst[lat / 8 + e] = make_uint4(u[0], u[1], u[2], u[3]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            part[(int64_t)(lat / 4 + e) * H] =
+                make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]), __uint_as_float(v[4 * e + 2]),
+                            __uint_as_float(v[4 * e + 3]));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(ofree);
+    }
+    if (!ok && lane == 0) flag_error(p.err, DEVERR_TIMEOUT);
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    pair_dealloc(tmem, 512);
+  }
+}
+
+// ---- plan ---------------------------------------------------------------------------------------------------
+// Sequence and visible rows of every new token, one warp each; the checks of the batch; the empty rows.
+__global__ void __launch_bounds__(256)
+    paged_tokens_kernel(PagedView v, const int32_t* blocks, int32_t top_k, int2* tinfo, __nv_bfloat16* o_lat, float* lse,
+                        uint32_t* err) {
+  if (blockIdx.x == 0) paged_check(v, err);
+  const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (t >= v.total_q) return;
+  const PagedToken tok = paged_token(v, t);
+  int64_t vis = tok.pos + 1;
+  if (blocks && vis > 0) {
+    const int32_t* list = blocks + t * top_k;
+    const int64_t own = tok.pos / v.page;
+    int n = top_k, bad = 0, at = -1;          // first -1, a fault, the last block
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int g = i0 + lane < top_k ? list[i0 + lane] : -1;
+      int before = __shfl_up_sync(0xffffffffu, g, 1);
+      if (lane == 0) before = at;
+      const uint32_t end = __ballot_sync(0xffffffffu, g < 0);
+      const int cnt = end ? __ffs(end) - 1 : 32;
+      if (lane < cnt && (g > own || g <= before)) bad = 1;
+      if (cnt > 0) at = __shfl_sync(0xffffffffu, g, cnt - 1);
+      if (cnt < 32) n = i0 + cnt;
+    }
+    if (__any_sync(0xffffffffu, bad)) {
+      if (lane == 0) flag_error(err, DEVERR_BLOCKS);
+      n = 0;
+    }
+    vis = n == 0 ? 0 : (int64_t)(n - 1) * v.page + (at == own ? tok.pos % v.page + 1 : v.page);
+  }
+  if (lane == 0) tinfo[t] = make_int2(tok.seq, (int32_t)(tok.seq < 0 ? 0 : vis));
+  if (tok.seq >= 0 && vis <= 0) {
+    uint4* o = reinterpret_cast<uint4*>(o_lat + t * H * DC);
+    for (int i = lane; i < H * DC / 8; i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = lane; i < H; i += 32) lse[t * H + i] = -INFINITY;
+  }
+}
+
+// Deals the tokens' units to the pairs (one block). In cost, token t with u_t > 0 units is kStartUnits + u_t
+// long; pair pp's range begins at the first unit whose cost starts at or after pp * total / pairs. Each pair's
+// range is written as (first token, its first unit, last token, its end unit), (-1, ...) if empty.
+__global__ void __launch_bounds__(1024)
+    paged_plan_kernel(const int2* tinfo, int64_t T, int32_t pairs, int64_t* cost, int4* pinfo) {
+  __shared__ int64_t warp_tot[32];
+  __shared__ int64_t total;
+  __shared__ int32_t btok[kMaxPairs + 1], bunit[kMaxPairs + 1];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto units = [&](int64_t t) -> int { return (max(tinfo[t].y, 0) + UNIT - 1) / UNIT; };
+  auto weight = [&](int u) -> int { return u > 0 ? u + kStartUnits : 0; };
+  const int64_t per = (T + 1023) / 1024;
+  const int64_t lo = min(T, tid * per), hi = min(T, lo + per);
+  int64_t sum = 0;
+  for (int64_t t = lo; t < hi; ++t) sum += weight(units(t));
+  int64_t x = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_tot[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t y = warp_tot[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += z;
+    }
+    warp_tot[lane] = y;
+    if (lane == 31) total = y;
+  }
+  __syncthreads();
+  int64_t at = x - sum + (warp > 0 ? warp_tot[warp - 1] : 0);
+  for (int64_t t = lo; t < hi; ++t) {
+    cost[t] = at;
+    at += weight(units(t));
+  }
+  __syncthreads();
+  // the boundaries: the first token whose end lies behind the boundary's cost, and the unit in it
+  for (int pp = tid; pp <= pairs; pp += blockDim.x) {
+    const int64_t c = total * pp / pairs;
+    int64_t a = 0, b = T;                     // the last token with cost <= c
+    while (b - a > 1) {
+      const int64_t mid = (a + b) >> 1;
+      if (cost[mid] <= c) a = mid; else b = mid;
+    }
+    int u = (int)max((int64_t)0, c - cost[a] - kStartUnits);
+    if (pp == pairs || u >= units(a)) {       // behind its last unit: the next token
+      ++a;
+      u = 0;
+      if (pp == pairs) a = T;
+    }
+    btok[pp] = (int32_t)a;
+    bunit[pp] = u;
+  }
+  __syncthreads();
+  for (int pp = tid; pp < pairs; pp += blockDim.x) {
+    int a = btok[pp], e = btok[pp + 1], ue = bunit[pp + 1];
+    int ua = bunit[pp];
+    while (a < T && units(a) == 0) { ++a; ua = 0; }         // tokens without units
+    if (ue == 0) {                                         // ends with the token before
+      do --e; while (e >= 0 && units(e) == 0);
+      ue = e >= 0 ? units(e) : 0;
+    }
+    const bool any = a < T && (a < e || (a == e && ua < ue));
+    pinfo[pp] = any ? make_int4(a, ua, e, ue) : make_int4(-1, 0, -2, 0);
+  }
+}
+
+// Exact merge of the tokens that cross ranges. Block (c, heads, columns) takes the token that begins in pair c's range
+// and goes on in the next: o = sum_s e^{m_s - M} O_s / sum_s e^{m_s - M} l_s over its pieces, in order.
+constexpr int kCombHeads = 32, kCombCols = 64;
+__global__ void __launch_bounds__(256)
+    paged_combine_kernel(const int2* tinfo, const int4* pinfo, int32_t pairs, const float4* part_o, const float2* part_ml,
+                         __nv_bfloat16* o_lat, float* lse) {
+  __shared__ int32_t slots[kMaxPairs];
+  __shared__ int32_t ns_sh;
+  __shared__ float wgt[kMaxPairs][kCombHeads];
+  __shared__ __align__(16) float tile[kCombHeads][kCombCols + 4];   // written as float4
+  const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31, grp = tid >> 5;
+  const int4 pc = pinfo[c];
+  if (pc.x < 0) return;
+  const int tok = pc.z, units = (tinfo[tok].y + UNIT - 1) / UNIT;
+  if (pc.w >= units || (pc.x == tok && pc.y > 0)) return;
+  if (tid == 0) {
+    int n = 0;
+    slots[n++] = 2 * c + (pc.x == tok ? 0 : 1);
+    for (int d = c + 1; d < pairs; ++d) {
+      const int4 pd = pinfo[d];
+      if (pd.x < 0) continue;
+      slots[n++] = 2 * d;
+      if (pd.z != tok || pd.w >= units) break;
+    }
+    ns_sh = n;
+  }
+  __syncthreads();
+  const int ns = ns_sh, h0 = kCombHeads * blockIdx.y, c0 = kCombCols * blockIdx.z;
+  // weights e^{m_s - M} / L of the pieces, by one warp (lane = head)
+  if (grp == 0) {
+    float M = -INFINITY, L = 0.f;
+    for (int s = 0; s < ns; ++s) M = fmaxf(M, part_ml[(int64_t)slots[s] * H + h0 + lane].x);
+    for (int s = 0; s < ns; ++s) {
+      const float2 ml = part_ml[(int64_t)slots[s] * H + h0 + lane];
+      const float e = ml.x > -INFINITY ? __expf(ml.x - M) : 0.f;
+      wgt[s][lane] = e;
+      L += e * ml.y;
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    for (int s = 0; s < ns; ++s) wgt[s][lane] *= inv;
+    if (blockIdx.z == 0) lse[(int64_t)tok * H + h0 + lane] = L == 0.f ? -INFINITY : M + logf(L);
+  }
+  __syncthreads();
+  // thread (lane = head, grp): column quads 2 grp, 2 grp + 1 of this block's 16
+  float4 acc[2];
+  acc[0] = acc[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < ns; ++s) {
+    const float4* src = part_o + ((int64_t)slots[s] * (DC / 4) + c0 / 4 + 2 * grp) * H + h0 + lane;
+    const float e = wgt[s][lane];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const float4 x = src[q * H];
+      acc[q].x += e * x.x; acc[q].y += e * x.y; acc[q].z += e * x.z; acc[q].w += e * x.w;
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 2; ++q) *reinterpret_cast<float4*>(&tile[lane][8 * grp + 4 * q]) = acc[q];
+  __syncthreads();
+  // head tid / 8, 8 columns each
+  const int h = tid >> 3, cc = 8 * (tid & 7);
+  const float* x = &tile[h][cc];
+  *reinterpret_cast<uint4*>(o_lat + ((int64_t)tok * H + h0 + h) * DC + c0 + cc) =
+      make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+}
+
+size_t align1k(size_t x) { return (x + 1023) / 1024 * 1024; }
+
+struct Scratch {
+  int2* tinfo;
+  int64_t* cost;
+  int4* pinfo;
+  float2* part_ml;
+  float4* part_o;
+  size_t bytes;
+};
+
+Scratch carve(void* ws, int64_t T) {
+  Scratch s;
+  char* p = (char*)ws;
+  s.tinfo = (int2*)p;
+  p += align1k((size_t)T * sizeof(int2));
+  s.cost = (int64_t*)p;
+  p += align1k((size_t)T * sizeof(int64_t));
+  s.pinfo = (int4*)p;
+  p += align1k(kMaxPairs * sizeof(int4));
+  s.part_ml = (float2*)p;
+  p += align1k((size_t)2 * kMaxPairs * H * sizeof(float2));
+  s.part_o = (float4*)p;
+  p += (size_t)2 * kMaxPairs * H * DC * sizeof(float);
+  s.bytes = (size_t)(p - (char*)ws);
+  return s;
+}
+
+}  // namespace
+
+size_t tc_paged_attention_bytes(int64_t total_q) { return carve(nullptr, total_q).bytes; }
+
+cudaError_t tc_paged_attention(const PagedView& v, const void* q_abs, const void* q_rope, const int32_t* blocks,
+                               int32_t top_k, float scale, void* o_lat, float* lse, void* ws, int num_sms, uint32_t* err,
+                               cudaStream_t st) {
+  const Scratch s = carve(ws, v.total_q);
+  CoreParams p;
+  memset(&p, 0, sizeof(p));
+  p.gran = v.page % 64 == 0 ? 64 : v.page % 32 == 0 ? 32 : 16;
+  cudaError_t e;
+  const int64_t rows = v.num_pages * v.page, TH = v.total_q * H;
+  if ((e = make_tmap_bf16(&p.kvmap, v.cache, DC + DR, rows, DC + DR, 64, p.gran)) != cudaSuccess) return e;
+  if ((e = make_tmap_bf16(&p.qmap, q_abs, DC, TH, DC, 64, HC)) != cudaSuccess) return e;
+  if ((e = make_tmap_bf16(&p.qrmap, q_rope, DR, TH, DR, 64, HC)) != cudaSuccess) return e;
+  p.v = v;
+  p.blocks = blocks;
+  p.top_k = top_k;
+  p.pairs = num_sms / 2 < kMaxPairs ? num_sms / 2 : kMaxPairs;
+  p.tinfo = s.tinfo;
+  p.pinfo = s.pinfo;
+  p.o_lat = (__nv_bfloat16*)o_lat;
+  p.lse = lse;
+  p.part_o = s.part_o;
+  p.part_ml = s.part_ml;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.err = err;
+  // per device, so set at every call (the runtime returns at once when nothing changes)
+  if ((e = cudaFuncSetAttribute(paged_core_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES)) !=
+      cudaSuccess)
+    return e;
+  paged_tokens_kernel<<<(unsigned)((v.total_q + 7) / 8), 256, 0, st>>>(v, blocks, top_k, s.tinfo, p.o_lat, lse, err);
+  paged_plan_kernel<<<1, 1024, 0, st>>>(s.tinfo, v.total_q, p.pairs, s.cost, s.pinfo);
+  paged_core_kernel<<<(unsigned)(2 * p.pairs), kThreads, SMEM_BYTES, st>>>(p);
+  note_launch(3);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (p.pairs > 1) {
+    paged_combine_kernel<<<dim3((unsigned)(p.pairs - 1), H / kCombHeads, DC / kCombCols), 256, 0, st>>>(
+        s.tinfo, s.pinfo, p.pairs, s.part_o, s.part_ml, p.o_lat, lse);
+    note_launch();
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace mla
