@@ -74,6 +74,12 @@ cudaError_t make_tmap_bf16(CUtensorMap* m, const void* ptr, int64_t inner, int64
 cudaError_t make_tmap_u8(CUtensorMap* m, const void* ptr, int64_t inner, int64_t outer, int64_t ld, int box_inner,
                          int box_outer);
 
+// 3-D bf16 TMA map over a dense row-major [rows, inner] matrix (inner a multiple of 64) as 64-column blocks: coordinates
+// (column in the block, row, block), box {64, box_rows, box_blocks}, each block of a box [box_rows][64], 128-byte
+// swizzle, zero fill out of bounds.
+cudaError_t make_tmap_bf16_blocks(CUtensorMap* m, const void* ptr, int64_t inner, int64_t rows, int box_rows,
+                                  int box_blocks);
+
 cudaError_t tc_gemm(const TcGemmDesc& g, cudaStream_t st);
 
 }  // namespace mla

@@ -22,9 +22,10 @@
 // last visible key and its box's end may hold anything, even NaN: their scores are masked, and their value
 // rows (at most two ring entries of a token's last step) are zeroed in shared memory before P.V.
 //
-// Roles (512 threads): warp 0 fills the ring of 16 KB entries in the order the MMAs take them (K of step j + 1
-// before V of step j); warp 1 of the leader CTA issues the MMAs; warp 2 loads a token's queries; warps 4-11 are
-// the softmax (thread = TMEM lane, two warps per lane quarter, 64 keys each) and rescale O when the running
+// Roles (512 threads): warps 0 and 3 fill the ring of 16 KB entries, keys and values, in the order the MMAs take
+// them (K of step j + 1 before V of step j); warp 1 of the leader CTA issues the MMAs; warp 2 loads a token's queries;
+// these run warp-uniform code with one elected lane at each TMA, MMA and commit (a lane-0 branch around the
+// whole loop cost 650 cycles a ring entry, three times what the copies take); warps 4-11 are the softmax (thread = TMEM lane, two warps per lane quarter, 64 keys each) and rescale O when the running
 // maximum has grown by 2^8; warps 12-15 write O out while the next token's first step runs.
 // Every wait is bounded (a timeout sets the error word and the role returns).
 #include <cuda_bf16.h>
@@ -44,12 +45,11 @@ constexpr int H = 128, DC = 512, DR = 64;
 constexpr int HC = H / 2;                      // heads per CTA
 constexpr int NK = 256;                        // keys per step
 constexpr int UNIT = 64;                       // keys per unit of the work split
-constexpr int GROUPS = NK / 16;
+constexpr int GROUPS = NK / 16;                // a step's rows are looked up in groups of 16 keys
 constexpr int kThreads = 512;
 constexpr int kMaxPairs = 74;
 constexpr int kStartUnits = 4;                 // a token's fixed cost (query load, epilogue), in units
 constexpr float kRescaleLog2 = 8.f;            // keep the running maximum until it grows by 2^8
-constexpr int kIssuers = 4;                    // TMA issuing lanes
 constexpr int kEntriesK = 9, kEntriesV = 8;    // ring entries of a step: [128 keys x 64], 2 x [64 keys x 64]
 constexpr int RING = 7;
 constexpr uint32_t ENTRY = 16384, BOX = 8192;
@@ -58,12 +58,11 @@ constexpr uint32_t P_BYTES = HC * NK * 2;
 
 constexpr uint32_t OFF_RED = 512;                                  // [2][4][64] floats: maxima of the four key blocks
 constexpr uint32_t OFF_STAT = OFF_RED + 2 * 4 * HC * 4;            // [5][64] floats: sums of the four key blocks, maximum
-constexpr uint32_t OFF_COORD = OFF_STAT + 5 * HC * 4;              // [4][16] row coordinates of the steps ahead
 constexpr uint32_t OFF_Q = 4096;
 constexpr uint32_t OFF_P = OFF_Q + Q_BYTES;
 constexpr uint32_t OFF_RING = OFF_P + P_BYTES;
 constexpr uint32_t SMEM_BYTES = OFF_RING + RING * ENTRY + 1024;
-static_assert(OFF_COORD + 4 * GROUPS * 4 <= OFF_Q, "statistics block");
+static_assert(OFF_STAT + 5 * HC * 4 <= OFF_Q, "statistics block");
 static_assert(OFF_Q % 1024 == 0 && OFF_P % 1024 == 0 && OFF_RING % 1024 == 0, "swizzle atom alignment");
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 
@@ -88,11 +87,12 @@ enum : int {
 static_assert(NBAR * 8 + 16 <= OFF_RED, "barrier block");
 
 struct CoreParams {
-  CUtensorMap kvmap;          // the pool as [rows, 576], box {64, gran}
+  CUtensorMap kmap;           // the pool as [rows, 576], box {64, gran}
+  CUtensorMap vmap;           // the pool as [9, rows, 64], box {64, gran, 2} (gran 64) or {64, gran, 1}
   CUtensorMap qmap, qrmap;    // q~ [T * 128, 512], q^R [T * 128, 64], box {64, 64}
   PagedView v;
   const int32_t* blocks;      // [T, top_k] chosen blocks; nullptr: all rows
-  int32_t top_k, gran, pairs;
+  int32_t top_k, pairs;
   const int2* tinfo;          // [T]: sequence, visible rows
   const int4* pinfo;          // [pairs]: first token, its first unit, last token, its end unit
   __nv_bfloat16* o_lat;
@@ -114,13 +114,27 @@ __device__ __forceinline__ void pair_relinquish() {
 __device__ __forceinline__ void pair_dealloc(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// Low word of a 128-byte-swizzle descriptor (start address, distance of 64-wide MN blocks); the high word is the
+// same for every operand here (8-row atoms 1024 bytes apart).
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
+}
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 // D (+)= A . B^T over both CTAs; the descriptors hold the same offsets in both.
-__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void pair_mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %5};\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
       : "memory");
 }
 // One arrival on the barrier at this offset in both CTAs once the MMAs issued so far are done.
@@ -138,8 +152,19 @@ __device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap* map, 
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void pair_load_3d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                             uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
+      "[%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+// One arrival on a barrier of either CTA. What it announces are tensor-memory reads (ordered by the tcgen05 fence
+// before it) and writes to this CTA's own shared memory (handed to the async proxy by the fence before it), so
+// the arrival itself needs no release at cluster scope, which costs 2000-3400 cycles here.
+__device__ __forceinline__ void arrive_pair(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity) {
   if (mbar_try_wait_cluster(bar, parity)) return true;
@@ -181,6 +206,68 @@ struct Walk {
   __device__ bool whole() const { return k0 == 0 && k1 == vis; }
 };
 
+// The steps of a pair's range, one after the other, across its tokens.
+struct Steps {
+  Walk w;
+  int k;                      // first key of the step
+  __device__ bool valid() const { return w.valid(); }
+  __device__ void next() {
+    k += NK;
+    if (k >= w.k1) {
+      w.next();
+      k = w.k0;
+    }
+  }
+};
+
+// Pool rows of the steps' groups of 16 keys, one group a lane (lanes 16-31 repeat): the block list is read two steps
+// ahead and the block table one, so that a step finds its rows in registers.
+struct Rows {
+  Steps s1, s2;               // the next step, the one behind it
+  int raw1, off1, blk2;       // table entry and offset for s1, block for s2 (-1: no visible key)
+  int g;
+  __device__ void block(const CoreParams& p) {
+    blk2 = -1;
+    const int j = s2.k + 16 * g;
+    if (s2.valid() && j < s2.w.k1) {
+      const int i = j / p.v.page;
+      blk2 = p.blocks ? p.blocks[(int64_t)s2.w.tok * p.top_k + i] : i;
+    }
+  }
+  __device__ void entry(const CoreParams& p) {
+    raw1 = -1;
+    off1 = blk2 < 0 ? -1 : (s1.k + 16 * g) % p.v.page;
+    if (blk2 >= 0) raw1 = p.v.table[(int64_t)s1.w.seq * p.v.stride + blk2];
+  }
+  __device__ void init(const CoreParams& p, const Walk& w, int lane) {
+    g = lane & (GROUPS - 1);
+    s2.w = w;
+    s2.k = w.valid() ? w.k0 : 0;
+    block(p);
+    s1 = s2;
+    entry(p);
+    if (s2.valid()) s2.next();
+    block(p);
+  }
+  // The rows of step s1 (this lane's group), and on to the next: a group behind the last visible key, or in a page
+  // outside the pool (flagged), is read out of range, which gives zeros.
+  __device__ int take(const CoreParams& p) {
+    const int raw = raw1, off = off1;
+    s1 = s2;
+    entry(p);
+    if (s2.valid()) s2.next();
+    block(p);
+    if (off < 0) return -4096;
+    if (raw < 0 || raw >= p.v.num_pages) {
+      flag_error(p.err, DEVERR_PAGE);
+      return -4096;
+    }
+    return raw * p.v.page + off;
+  }
+};
+
+// GRAN: rows of a TMA box, the largest of 64, 32, 16 that divides the page size.
+template <int GRAN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     paged_core_kernel(const __grid_constant__ CoreParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -191,7 +278,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t r = cluster_rank();
   const int pair = blockIdx.x >> 1;
-  auto lead = [&](int i) { return map_peer(bar(i), 0); };
+  const uint32_t lead0 = map_peer(sbase, 0);
+  auto lead = [&](int i) { return lead0 + 8u * (uint32_t)i; };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NBAR; ++i) {
@@ -203,7 +291,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(bar(i), cnt);
     }
     fence_mbar_init();
-    prefetch_tmap(&p.kvmap);
+    prefetch_tmap(&p.kmap);
+    prefetch_tmap(&p.vmap);
     prefetch_tmap(&p.qmap);
     prefetch_tmap(&p.qrmap);
   }
@@ -219,163 +308,195 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   w.init(p, p.pinfo[pair]);
   bool ok = true;
 
-  if (warp == 0) {
-    // -------------------------------------------------------------- ring producer
-    int32_t* coord = reinterpret_cast<int32_t*>(smem + OFF_COORD);
-    const int g = lane & (GROUPS - 1);
-    // pool row of the group's first key of the step at k, or a row out of range (read as zeros)
-    auto row_of = [&](const Walk& a, int k) -> int32_t {
-      const int j = k + 16 * g;
-      if (j >= a.k1) return -4096;
-      const int i = j / p.v.page;
-      const int64_t blk = p.blocks ? p.blocks[(int64_t)a.tok * p.top_k + i] : i;
-      const int64_t pg = paged_page(p.v, a.seq, blk, p.err);
-      return pg < 0 ? -4096 : (int32_t)(pg * p.v.page + j % p.v.page);
+  if (warp == 0 || warp == 3) {
+    // -------------------------------------------------------------- ring producers: keys, values
+    const bool keys = warp == 0;
+    Rows rows;
+    rows.init(p, w, lane);
+    // The ring holds entries of both kinds in the MMAs' order; this warp fills its own and passes the others. A
+    // barrier's parity tells two consecutive phases apart, so no more than RING entries are passed without a
+    // wait on the slot reached (which also means that everything RING entries back has been consumed).
+    int n = 0, slot = 0, ph = 1, since = 0, last = -1;
+    auto move = [&](int c) {
+      n += c;
+      slot += c;
+      if (slot >= RING) { slot -= RING; ph ^= 1; }
     };
-    int n = 0, last = -1, js = 0;
-    // entry n: this lane's if its turn; waits for the slot and announces its bytes
-    auto take = [&](bool tail, uint32_t* dst, uint32_t* b) -> bool {
-      const int cur = n++;
-      if (!ok || (cur & (kIssuers - 1)) != lane) return false;
-      const int slot = cur % RING;
-      if (!mbar_wait(bar(B_EMPTY + slot), ((cur / RING) & 1) ^ 1)) { ok = false; return false; }
-      *dst = sbase + OFF_RING + slot * ENTRY;
-      if (tail) {
-        // counted in this CTA, whose softmax warps zero rows of it before P.V takes it
-        mbar_expect_tx(bar(B_TAIL), ENTRY);
-        *b = bar(B_TAIL);
-        if (r == 0) mbar_arrive(bar(B_FULL + slot));
-      } else {
-        if (r == 0) mbar_expect_tx(bar(B_FULL + slot), 2 * ENTRY);
-        *b = lead(B_FULL + slot);
-        last = cur;
-      }
-      return true;
+    auto wait_slot = [&]() {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(B_EMPTY + slot), ph)) != 0;
+      since = 0;
     };
-    auto load_v = [&](const int32_t* c, int tail_kq) {
-      for (int e = 0; e < kEntriesV; ++e) {
-        uint32_t dst, b;
-        const int kq = e >> 1, x = 256 * (e & 1) + 128 * (int)r;
-        if (!take(kq == tail_kq, &dst, &b)) continue;
-        for (int s = 0; s < 64; s += p.gran) {
-          const int32_t y = c[(64 * kq + s) >> 4];
-          pair_load(dst + s * 128, &p.kvmap, x, y, b);
-          pair_load(dst + BOX + s * 128, &p.kvmap, x + 64, y, b);
-        }
+    auto filled = [&]() {
+      last = n;
+      move(1);
+      since = 1;
+    };
+    auto pass = [&](int c) {
+      while (ok && c > 0) {
+        const int d = min(c, RING - since);
+        move(d);
+        since += d;
+        c -= d;
+        if (since == RING) wait_slot();
       }
     };
-    if (w.valid()) {
-      const int32_t c0 = row_of(w, w.k0);
-      if (lane < GROUPS) coord[g] = c0;
-    }
-    __syncwarp();
-    for (; w.valid(); ) {
-      Walk nx = w;
-      nx.next();
-      const int ns = w.steps();
-      for (int j = 0; j < ns; ++j, ++js) {
-        const int32_t* c = coord + (js & 3) * GROUPS;
-        // the next step's rows come in while this step's entries are issued
-        int32_t ahead = -4096;
-        if (j + 1 < ns) ahead = row_of(w, w.k0 + (j + 1) * NK);
-        else if (nx.valid()) ahead = row_of(nx, nx.k0);
-        for (int e = 0; e < kEntriesK; ++e) {
-          uint32_t dst, b;
-          if (!take(false, &dst, &b)) continue;
-          for (int s = 0; s < 128; s += p.gran)
-            pair_load(dst + s * 128, &p.kvmap, 64 * e, c[(128 * (int)r + s) >> 4], b);
-        }
-        if (j > 0) load_v(coord + ((js - 1) & 3) * GROUPS, -1);
-        if (j == ns - 1) {
-          const int rem = w.k1 - (w.k0 + j * NK);
-          load_v(c, rem % 64 ? rem / 64 : -1);
+    auto keys_of = [&](int row) {             // K of a step: this CTA's 128 keys, 64 columns an entry
+      int y[128 / GRAN];
+#pragma unroll
+      for (int s = 0; s < 128 / GRAN; ++s) y[s] = __shfl_sync(0xffffffffu, row, 8 * (int)r + s * (GRAN / 16));
+      for (int e = 0; ok && e < kEntriesK; ++e) {
+        wait_slot();
+        if (!ok) break;
+        if (elect_one()) {
+          const uint32_t dst = sbase + OFF_RING + slot * ENTRY, b = lead(B_FULL + slot);
+          if (r == 0) mbar_expect_tx(bar(B_FULL + slot), 2 * ENTRY);
+#pragma unroll
+          for (int s = 0; s < 128 / GRAN; ++s) pair_load(dst + s * GRAN * 128, &p.kmap, 64 * e, y[s], b);
         }
         __syncwarp();
-        if (lane < GROUPS) coord[((js + 1) & 3) * GROUPS + g] = ahead;
-        ok = __all_sync(0xffffffffu, ok) != 0;
-        if (!ok) break;
+        filled();
       }
-      if (!ok) break;
-      w = nx;
+    };
+    auto values_of = [&](int row, int tail_kq) {   // V of a step: 256 keys, this CTA's 2 x 128 columns
+      for (int kq = 0; ok && kq < 4; ++kq) {
+        int y[64 / GRAN];
+#pragma unroll
+        for (int s = 0; s < 64 / GRAN; ++s) y[s] = __shfl_sync(0xffffffffu, row, 4 * kq + s * (GRAN / 16));
+        for (int nh = 0; ok && nh < 2; ++nh) {
+          wait_slot();
+          if (!ok) break;
+          if (elect_one()) {
+            const uint32_t dst = sbase + OFF_RING + slot * ENTRY;
+            uint32_t b = lead(B_FULL + slot);
+            if (kq == tail_kq) {
+              // counted in this CTA, whose softmax warps zero rows of it before P.V takes it
+              mbar_expect_tx(bar(B_TAIL), ENTRY);
+              if (r == 0) mbar_arrive(bar(B_FULL + slot));
+              b = bar(B_TAIL);
+            } else if (r == 0) {
+              mbar_expect_tx(bar(B_FULL + slot), 2 * ENTRY);
+            }
+            const int z = 4 * nh + 2 * (int)r;     // 64-column blocks z, z + 1
+#pragma unroll
+            for (int s = 0; s < 64 / GRAN; ++s) {
+              pair_load_3d(dst + s * GRAN * 128, &p.vmap, 0, y[s], z, b);
+              if (GRAN < 64) pair_load_3d(dst + BOX + s * GRAN * 128, &p.vmap, 0, y[s], z + 1, b);
+            }
+          }
+          __syncwarp();
+          filled();
+        }
+      }
+    };
+    for (; ok && w.valid(); w.next()) {
+      const int ns = w.steps(), rem = w.k1 - (w.k0 + (ns - 1) * NK);
+      const int tail_kq = rem % 64 ? rem / 64 : -1;
+      for (int j = 0; ok && j < ns; ++j) {
+        // this token's entries: K0 K1 V0 K2 V1 ... K(ns-1) V(ns-2) V(ns-1)
+        if (keys) {
+          keys_of(rows.take(p));
+          if (j > 0) pass(kEntriesV);
+          if (j == ns - 1) pass(kEntriesV);
+        } else {
+          if (j == 0) pass(kEntriesK);
+          if (j < ns - 1) pass(kEntriesK);
+          values_of(rows.take(p), j == ns - 1 ? tail_kq : -1);
+        }
+      }
     }
     if (!ok) {
       if (lane == 0) flag_error(p.err, DEVERR_TIMEOUT);
-      // this lane's entries still in flight (of both CTAs, seen at the leader's barriers)
-      if (r == 0 && lane < kIssuers)
-        for (int i = max(lane, last - RING + 1); i <= last; ++i)
-          if ((i & (kIssuers - 1)) == lane) mbar_wait(bar(B_FULL + i % RING), (i / RING) & 1);
+      // entries still in flight, those of the peer too (seen at the leader's barriers; a tail entry's bytes land
+      // within the same wait)
+      if (r == 0)
+        for (int i = max(0, last - RING + 1); i <= last; ++i) mbar_wait(bar(B_FULL + i % RING), (i / RING) & 1);
     }
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA issuer (leader CTA)
-    if (r == 0 && lane == 0) {
+    if (r == 0) {
       constexpr uint32_t id_qk = idesc_bf16(128, NK, 0, 0), id_pv = idesc_bf16(128, 256, 0, 1);
-      int n = 0, js = 0, gpc = 0, tails = 0;  // ring index, step, token, tokens that end inside 64 keys
+      const uint32_t q_lo = desc_lo(sbase + OFF_Q, 0), p_lo = desc_lo(sbase + OFF_P, 0);
+      const uint32_t k_lo = desc_lo(sbase + OFF_RING, 0), v_lo = desc_lo(sbase + OFF_RING, BOX);
+      auto wait_all = [&](uint32_t b, uint32_t par) { return __all_sync(0xffffffffu, wait_cluster(b, par)) != 0; };
+      int js = 0, gpc = 0, tails = 0;         // step, token, tokens that end inside 64 keys
+      int slot = 0, ph = 0;
+      auto next_entry = [&]() {
+        if (++slot == RING) { slot = 0; ph ^= 1; }
+      };
       auto qk = [&](int j) -> bool {
         const int sb = j & 1;
-        if (!wait_cluster(bar(B_SFREE + sb), ((j >> 1) & 1) ^ 1)) return false;
-        tc_fence_after();
+        if (!wait_all(bar(B_SFREE + sb), ((j >> 1) & 1) ^ 1)) return false;
         const uint32_t d = tmem + 256 + 128 * sb;
-        for (int e = 0; e < kEntriesK; ++e, ++n) {
-          const int slot = n % RING;
-          if (!wait_cluster(bar(B_FULL + slot), (n / RING) & 1)) return false;
+        for (int e = 0; e < kEntriesK; ++e) {
+          if (!wait_all(bar(B_FULL + slot), ph)) return false;
           tc_fence_after();
-          const uint64_t a = sw128_desc(sbase + OFF_Q + e * BOX, 0, 1024);
-          const uint64_t b = sw128_desc(sbase + OFF_RING + slot * ENTRY, 0, 1024);
+          const uint32_t a = q_lo + e * (BOX >> 4), b = k_lo + slot * (ENTRY >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) pair_mma(d, a + 2 * kk, b + 2 * kk, id_qk, (e | kk) ? 1u : 0u);
-          pair_commit(bar(B_EMPTY + slot));
+            for (int kk = 0; kk < 4; ++kk) pair_mma(d, a + 2 * kk, b + 2 * kk, id_qk, (e | kk) ? 1u : 0u);
+            pair_commit(bar(B_EMPTY + slot));
+            if (e == kEntriesK - 1) pair_commit(bar(B_SFULL + sb));
+          }
+          __syncwarp();
+          next_entry();
         }
-        pair_commit(bar(B_SFULL + sb));
         return true;
       };
       auto pv = [&](int j, bool first, int tail_kq) -> bool {
-        if (!wait_cluster(bar(B_PRDY), j & 1)) return false;
-        if (first && !wait_cluster(bar(B_OFREE), (gpc & 1) ^ 1)) return false;
-        tc_fence_after();
-        for (int e = 0; e < kEntriesV; ++e, ++n) {
-          const int slot = n % RING, kq = e >> 1;
-          if (!wait_cluster(bar(B_FULL + slot), (n / RING) & 1)) return false;
-          if (kq == tail_kq && (e & 1) == 0 && !wait_cluster(bar(B_TRDY), tails++ & 1)) return false;
+        if (!wait_all(bar(B_PRDY), j & 1)) return false;
+        if (first && !wait_all(bar(B_OFREE), (gpc & 1) ^ 1)) return false;
+        for (int e = 0; e < kEntriesV; ++e) {
+          const int kq = e >> 1;
+          if (!wait_all(bar(B_FULL + slot), ph)) return false;
+          if (kq == tail_kq && (e & 1) == 0 && !wait_all(bar(B_TRDY), tails++ & 1)) return false;
           tc_fence_after();
-          const uint64_t a = sw128_desc(sbase + OFF_P + kq * BOX, 0, 1024);
-          const uint64_t b = sw128_desc(sbase + OFF_RING + slot * ENTRY, BOX, 1024);
+          const uint32_t a = p_lo + kq * (BOX >> 4), b = v_lo + slot * (ENTRY >> 4);
+          const uint32_t keep = first && kq == 0 ? 0u : 1u;
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            pair_mma(tmem + 128 * (e & 1), a + 2 * kk, b + 128 * kk, id_pv, (first && kq == 0 && kk == 0) ? 0u : 1u);
-          pair_commit(bar(B_EMPTY + slot));
+            for (int kk = 0; kk < 4; ++kk)
+              pair_mma(tmem + 128 * (e & 1), a + 2 * kk, b + 128 * kk, id_pv, kk ? 1u : keep);
+            pair_commit(bar(B_EMPTY + slot));
+            if (e == kEntriesV - 1) pair_commit(bar(B_PVD));
+          }
+          __syncwarp();
+          next_entry();
         }
-        pair_commit(bar(B_PVD));
         return true;
       };
       for (; ok && w.valid(); w.next(), ++gpc) {
-        const int ns = w.steps();
-        ok = wait_cluster(bar(B_QFULL), gpc & 1);
-        tc_fence_after();
+        const int ns = w.steps(), rem = w.k1 - (w.k0 + (ns - 1) * NK);
+        ok = wait_all(bar(B_QFULL), gpc & 1);
         for (int j = 0; ok && j < ns; ++j) {
           ok = qk(js + j);
-          if (ok && j == ns - 1) pair_commit(bar(B_QEMPTY));
+          if (ok && j == ns - 1 && elect_one()) pair_commit(bar(B_QEMPTY));
+          __syncwarp();
           if (ok && j > 0) ok = pv(js + j - 1, j == 1, -1);
         }
-        const int rem = w.k1 - (w.k0 + (ns - 1) * NK);
         if (ok) ok = pv(js + ns - 1, ns == 1, rem % 64 ? rem / 64 : -1);
-        if (ok) pair_commit(bar(B_ODONE));
+        if (ok && elect_one()) pair_commit(bar(B_ODONE));
+        __syncwarp();
         js += ns;
       }
-      if (!ok) flag_error(p.err, DEVERR_TIMEOUT);
+      if (!ok && lane == 0) flag_error(p.err, DEVERR_TIMEOUT);
     }
   } else if (warp == 2) {
     // -------------------------------------------------------------- queries
-    if (lane == 0) {
-      int gpc = 0;
-      for (; w.valid(); w.next(), ++gpc) {
-        if (!mbar_wait(bar(B_QEMPTY), (gpc & 1) ^ 1)) { ok = false; break; }
+    int gpc = 0;
+    for (; w.valid(); w.next(), ++gpc) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(B_QEMPTY), (gpc & 1) ^ 1)) != 0;
+      if (!ok) break;
+      if (elect_one()) {
         if (r == 0) mbar_expect_tx(bar(B_QFULL), 2 * Q_BYTES);
         const int32_t y = w.tok * H + HC * (int)r;
         for (int c = 0; c < 8; ++c) pair_load(sbase + OFF_Q + c * BOX, &p.qmap, 64 * c, y, lead(B_QFULL));
         pair_load(sbase + OFF_Q + 8 * BOX, &p.qrmap, 0, y, lead(B_QFULL));
       }
-      if (!ok) flag_error(p.err, DEVERR_TIMEOUT);
-      if (!ok && r == 0 && gpc > 0) mbar_wait(bar(B_QFULL), (gpc - 1) & 1);
+      __syncwarp();
+    }
+    if (!ok) {
+      if (lane == 0) flag_error(p.err, DEVERR_TIMEOUT);
+      if (r == 0 && gpc > 0) mbar_wait(bar(B_QFULL), (gpc - 1) & 1);
     }
   } else if (warp >= 4 && warp < 12) {
     // -------------------------------------------------------------- softmax
@@ -404,7 +525,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_cluster(sfree + 8 * sb);
+        if (lane == 0) arrive_pair(sfree + 8 * sb);
         const int nvis = rem - 64 * kq;
         if (nvis < 64) {
 #pragma unroll
@@ -479,7 +600,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) arrive_cluster(prdy);
+        if (lane == 0) arrive_pair(prdy);
         if (j == ns - 1 && rem % 64) {
           // value rows behind the last visible key: zeros, since 0 * NaN is not 0
           if (!wait_u(bar(B_TAIL), tails & 1)) { ok = false; break; }
@@ -494,7 +615,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) arrive_cluster(trdy);
+          if (lane == 0) arrive_pair(trdy);
         }
       }
       if (!ok) break;
@@ -559,7 +680,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_cluster(ofree);
+      if (lane == 0) arrive_pair(ofree);
     }
     if (!ok && lane == 0) flag_error(p.err, DEVERR_TIMEOUT);
   }
@@ -748,6 +869,16 @@ __global__ void __launch_bounds__(256)
       make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
+template <int GRAN>
+cudaError_t launch_core(const CoreParams& p, cudaStream_t st) {
+  // per device, so set at every call
+  cudaError_t e = cudaFuncSetAttribute(paged_core_kernel<GRAN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  paged_core_kernel<GRAN><<<(unsigned)(2 * p.pairs), kThreads, SMEM_BYTES, st>>>(p);
+  note_launch();
+  return cudaGetLastError();
+}
+
 size_t align1k(size_t x) { return (x + 1023) / 1024 * 1024; }
 
 struct Scratch {
@@ -786,10 +917,11 @@ cudaError_t tc_paged_attention(const PagedView& v, const void* q_abs, const void
   const Scratch s = carve(ws, v.total_q);
   CoreParams p;
   memset(&p, 0, sizeof(p));
-  p.gran = v.page % 64 == 0 ? 64 : v.page % 32 == 0 ? 32 : 16;
+  const int gran = v.page % 64 == 0 ? 64 : v.page % 32 == 0 ? 32 : 16;
   cudaError_t e;
   const int64_t rows = v.num_pages * v.page, TH = v.total_q * H;
-  if ((e = make_tmap_bf16(&p.kvmap, v.cache, DC + DR, rows, DC + DR, 64, p.gran)) != cudaSuccess) return e;
+  if ((e = make_tmap_bf16(&p.kmap, v.cache, DC + DR, rows, DC + DR, 64, gran)) != cudaSuccess) return e;
+  if ((e = make_tmap_bf16_blocks(&p.vmap, v.cache, DC + DR, rows, gran, gran == 64 ? 2 : 1)) != cudaSuccess) return e;
   if ((e = make_tmap_bf16(&p.qmap, q_abs, DC, TH, DC, 64, HC)) != cudaSuccess) return e;
   if ((e = make_tmap_bf16(&p.qrmap, q_rope, DR, TH, DR, 64, HC)) != cudaSuccess) return e;
   p.v = v;
@@ -804,15 +936,12 @@ cudaError_t tc_paged_attention(const PagedView& v, const void* q_abs, const void
   p.part_ml = s.part_ml;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.err = err;
-  // per device, so set at every call (the runtime returns at once when nothing changes)
-  if ((e = cudaFuncSetAttribute(paged_core_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES)) !=
-      cudaSuccess)
-    return e;
   paged_tokens_kernel<<<(unsigned)((v.total_q + 7) / 8), 256, 0, st>>>(v, blocks, top_k, s.tinfo, p.o_lat, lse, err);
   paged_plan_kernel<<<1, 1024, 0, st>>>(s.tinfo, v.total_q, p.pairs, s.cost, s.pinfo);
-  paged_core_kernel<<<(unsigned)(2 * p.pairs), kThreads, SMEM_BYTES, st>>>(p);
-  note_launch(3);
+  note_launch(2);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = gran == 64 ? launch_core<64>(p, st) : gran == 32 ? launch_core<32>(p, st) : launch_core<16>(p, st);
+  if (e != cudaSuccess) return e;
   if (p.pairs > 1) {
     paged_combine_kernel<<<dim3((unsigned)(p.pairs - 1), H / kCombHeads, DC / kCombCols), 256, 0, st>>>(
         s.tinfo, s.pinfo, p.pairs, s.part_o, s.part_ml, p.o_lat, lse);
