@@ -22,8 +22,9 @@
 // last visible key and its box's end may hold anything, even NaN: their scores are masked, and their value
 // rows (at most two ring entries of a token's last step) are zeroed in shared memory before P.V.
 //
-// Roles (512 threads): warps 0 and 3 fill the ring of 16 KB entries, keys and values, in the order the MMAs take
-// them (K of step j + 1 before V of step j); warp 1 of the leader CTA issues the MMAs; warp 2 loads a token's queries;
+// Roles (512 threads): warps 0, 2 and 3 fill the ring of 16 KB entries, every third entry each, in the order the
+// MMAs take them (K of step j + 1 before V of step j; one thread issues a copy every 500 cycles or so, the copies
+// take 270), and warp 2 loads a token's queries; warp 1 of the leader CTA issues the MMAs;
 // these run warp-uniform code with one elected lane at each TMA, MMA and commit (a lane-0 branch around the
 // whole loop cost 650 cycles a ring entry, three times what the copies take); warps 4-11 are the softmax (thread = TMEM lane, two warps per lane quarter, 64 keys each) and rescale O when the running
 // maximum has grown by 2^8; warps 12-15 write O out while the next token's first step runs.
@@ -308,45 +309,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   w.init(p, p.pinfo[pair]);
   bool ok = true;
 
-  if (warp == 0 || warp == 3) {
-    // -------------------------------------------------------------- ring producers: keys, values
-    const bool keys = warp == 0;
+  if (warp == 0 || warp == 2 || warp == 3) {
+    // -------------------------------------------------------------- ring producers
+    // The three warps take every third entry. (A barrier's parity tells two consecutive phases apart: a warp's own
+    // entries are 3 apart, so it never looks at a slot that is more than one lap behind.)
+    const int me = warp == 0 ? 0 : warp - 1;
     Rows rows;
     rows.init(p, w, lane);
-    // The ring holds entries of both kinds in the MMAs' order; this warp fills its own and passes the others. A
-    // barrier's parity tells two consecutive phases apart, so no more than RING entries are passed without a
-    // wait on the slot reached (which also means that everything RING entries back has been consumed).
-    int n = 0, slot = 0, ph = 1, since = 0, last = -1;
-    auto move = [&](int c) {
-      n += c;
-      slot += c;
-      if (slot >= RING) { slot -= RING; ph ^= 1; }
+    int base = 0, bph = 1, turn = me;         // slot and parity of the block of entries at hand, this warp's first of it
+    int n = 0, last = -1;                     // ring index of the block, this warp's last entry
+    int gpc = 0;
+    // waits for the slot of entry e of the block; false when it gave up
+    auto ready = [&](int e, int* slot) -> bool {
+      int s = base + e, ph = bph;
+      if (s >= RING) { s -= RING; ph ^= 1; }
+      if (s >= RING) { s -= RING; ph ^= 1; }
+      *slot = s;
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(B_EMPTY + s), ph)) != 0;
+      return ok;
     };
-    auto wait_slot = [&]() {
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(B_EMPTY + slot), ph)) != 0;
-      since = 0;
-    };
-    auto filled = [&]() {
-      last = n;
-      move(1);
-      since = 1;
-    };
-    auto pass = [&](int c) {
-      while (ok && c > 0) {
-        const int d = min(c, RING - since);
-        move(d);
-        since += d;
-        c -= d;
-        if (since == RING) wait_slot();
-      }
+    auto leave = [&](int count) {
+      n += count;
+      base += count;
+      if (base >= RING) { base -= RING; bph ^= 1; }
+      if (base >= RING) { base -= RING; bph ^= 1; }
+      turn = (turn + 9 - count) % 3;          // count is 8 or 9
     };
     auto keys_of = [&](int row) {             // K of a step: this CTA's 128 keys, 64 columns an entry
       int y[128 / GRAN];
 #pragma unroll
       for (int s = 0; s < 128 / GRAN; ++s) y[s] = __shfl_sync(0xffffffffu, row, 8 * (int)r + s * (GRAN / 16));
-      for (int e = 0; ok && e < kEntriesK; ++e) {
-        wait_slot();
-        if (!ok) break;
+      for (int e = turn, slot; e < kEntriesK && ready(e, &slot); e += 3) {
         if (elect_one()) {
           const uint32_t dst = sbase + OFF_RING + slot * ENTRY, b = lead(B_FULL + slot);
           if (r == 0) mbar_expect_tx(bar(B_FULL + slot), 2 * ENTRY);
@@ -354,62 +347,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int s = 0; s < 128 / GRAN; ++s) pair_load(dst + s * GRAN * 128, &p.kmap, 64 * e, y[s], b);
         }
         __syncwarp();
-        filled();
+        last = n + e;
       }
+      leave(kEntriesK);
     };
-    auto values_of = [&](int row, int tail_kq) {   // V of a step: 256 keys, this CTA's 2 x 128 columns
-      for (int kq = 0; ok && kq < 4; ++kq) {
+    auto values_of = [&](int row, int tail_kq) {   // V of a step: 64 keys x 128 of this CTA's columns an entry
+      for (int e = turn, slot; e < kEntriesV && ready(e, &slot); e += 3) {
+        const int kq = e >> 1;
         int y[64 / GRAN];
 #pragma unroll
         for (int s = 0; s < 64 / GRAN; ++s) y[s] = __shfl_sync(0xffffffffu, row, 4 * kq + s * (GRAN / 16));
-        for (int nh = 0; ok && nh < 2; ++nh) {
-          wait_slot();
-          if (!ok) break;
-          if (elect_one()) {
-            const uint32_t dst = sbase + OFF_RING + slot * ENTRY;
-            uint32_t b = lead(B_FULL + slot);
-            if (kq == tail_kq) {
-              // counted in this CTA, whose softmax warps zero rows of it before P.V takes it
-              mbar_expect_tx(bar(B_TAIL), ENTRY);
-              if (r == 0) mbar_arrive(bar(B_FULL + slot));
-              b = bar(B_TAIL);
-            } else if (r == 0) {
-              mbar_expect_tx(bar(B_FULL + slot), 2 * ENTRY);
-            }
-            const int z = 4 * nh + 2 * (int)r;     // 64-column blocks z, z + 1
-#pragma unroll
-            for (int s = 0; s < 64 / GRAN; ++s) {
-              pair_load_3d(dst + s * GRAN * 128, &p.vmap, 0, y[s], z, b);
-              if (GRAN < 64) pair_load_3d(dst + BOX + s * GRAN * 128, &p.vmap, 0, y[s], z + 1, b);
-            }
+        if (elect_one()) {
+          const uint32_t dst = sbase + OFF_RING + slot * ENTRY;
+          uint32_t b = lead(B_FULL + slot);
+          if (kq == tail_kq) {
+            // counted in this CTA, whose softmax warps zero rows of it before P.V takes it
+            mbar_expect_tx(bar(B_TAIL), ENTRY);
+            if (r == 0) mbar_arrive(bar(B_FULL + slot));
+            b = bar(B_TAIL);
+          } else if (r == 0) {
+            mbar_expect_tx(bar(B_FULL + slot), 2 * ENTRY);
           }
-          __syncwarp();
-          filled();
+          const int z = 4 * (e & 1) + 2 * (int)r;  // 64-column blocks z, z + 1
+#pragma unroll
+          for (int s = 0; s < 64 / GRAN; ++s) {
+            pair_load_3d(dst + s * GRAN * 128, &p.vmap, 0, y[s], z, b);
+            if (GRAN < 64) pair_load_3d(dst + BOX + s * GRAN * 128, &p.vmap, 0, y[s], z + 1, b);
+          }
         }
+        __syncwarp();
+        last = n + e;
       }
+      leave(kEntriesV);
     };
-    for (; ok && w.valid(); w.next()) {
-      const int ns = w.steps(), rem = w.k1 - (w.k0 + (ns - 1) * NK);
-      const int tail_kq = rem % 64 ? rem / 64 : -1;
-      for (int j = 0; ok && j < ns; ++j) {
-        // this token's entries: K0 K1 V0 K2 V1 ... K(ns-1) V(ns-2) V(ns-1)
-        if (keys) {
-          keys_of(rows.take(p));
-          if (j > 0) pass(kEntriesV);
-          if (j == ns - 1) pass(kEntriesV);
-        } else {
-          if (j == 0) pass(kEntriesK);
-          if (j < ns - 1) pass(kEntriesK);
-          values_of(rows.take(p), j == ns - 1 ? tail_kq : -1);
+    for (; ok && w.valid(); w.next(), ++gpc) {
+      if (me == 1) {
+        // the token's queries, once the last QK^T of the token before is done with the buffer
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(B_QEMPTY), (gpc & 1) ^ 1)) != 0;
+        if (!ok) break;
+        if (elect_one()) {
+          if (r == 0) mbar_expect_tx(bar(B_QFULL), 2 * Q_BYTES);
+          const int32_t y = w.tok * H + HC * (int)r;
+          for (int c = 0; c < 8; ++c) pair_load(sbase + OFF_Q + c * BOX, &p.qmap, 64 * c, y, lead(B_QFULL));
+          pair_load(sbase + OFF_Q + 8 * BOX, &p.qrmap, 0, y, lead(B_QFULL));
         }
+        __syncwarp();
+      }
+      // the token's entries: K0 K1 V0 K2 V1 ... K(ns-1) V(ns-2) V(ns-1)
+      const int ns = w.steps(), rem = w.k1 - (w.k0 + (ns - 1) * NK);
+      int row = -4096;
+      for (int j = 0; ok && j < ns; ++j) {
+        const int before = row;
+        row = rows.take(p);
+        keys_of(row);
+        if (ok && j > 0) values_of(before, -1);
+        if (ok && j == ns - 1) values_of(row, rem % 64 ? rem / 64 : -1);
       }
     }
     if (!ok) {
       if (lane == 0) flag_error(p.err, DEVERR_TIMEOUT);
-      // entries still in flight, those of the peer too (seen at the leader's barriers; a tail entry's bytes land
-      // within the same wait)
-      if (r == 0)
+      // copies still in flight, those of the peer too (seen at the leader's barriers; a tail entry's bytes land
+      // within the same waits)
+      if (r == 0) {
         for (int i = max(0, last - RING + 1); i <= last; ++i) mbar_wait(bar(B_FULL + i % RING), (i / RING) & 1);
+        if (me == 1 && gpc > 0) mbar_wait(bar(B_QFULL), (gpc - 1) & 1);
+      }
     }
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA issuer (leader CTA)
@@ -479,24 +481,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         js += ns;
       }
       if (!ok && lane == 0) flag_error(p.err, DEVERR_TIMEOUT);
-    }
-  } else if (warp == 2) {
-    // -------------------------------------------------------------- queries
-    int gpc = 0;
-    for (; w.valid(); w.next(), ++gpc) {
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(B_QEMPTY), (gpc & 1) ^ 1)) != 0;
-      if (!ok) break;
-      if (elect_one()) {
-        if (r == 0) mbar_expect_tx(bar(B_QFULL), 2 * Q_BYTES);
-        const int32_t y = w.tok * H + HC * (int)r;
-        for (int c = 0; c < 8; ++c) pair_load(sbase + OFF_Q + c * BOX, &p.qmap, 64 * c, y, lead(B_QFULL));
-        pair_load(sbase + OFF_Q + 8 * BOX, &p.qrmap, 0, y, lead(B_QFULL));
-      }
-      __syncwarp();
-    }
-    if (!ok) {
-      if (lane == 0) flag_error(p.err, DEVERR_TIMEOUT);
-      if (r == 0 && gpc > 0) mbar_wait(bar(B_QFULL), (gpc - 1) & 1);
     }
   } else if (warp >= 4 && warp < 12) {
     // -------------------------------------------------------------- softmax
