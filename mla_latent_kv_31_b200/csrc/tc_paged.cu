@@ -167,16 +167,22 @@ __device__ __forceinline__ void pair_load_3d(uint32_t dst, const CUtensorMap* ma
 __device__ __forceinline__ void arrive_pair(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = globaltimer();
-  for (;;) {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait_cluster(bar, parity)) return true;
-    if (globaltimer() - t0 > kWaitTimeoutNs) return false;
+// Bounded waits on the SM's own clock (about a second; reading the global timer at each miss is slower).
+constexpr long long kWaitCycles = 2000000000ll;
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
+  long long t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    if ((i & 63) == 0) {
+      const long long t = clock64();
+      if (t0 == 0) t0 = t;
+      else if (t - t0 > kWaitCycles) return false;
+    }
   }
 }
+__device__ __forceinline__ bool wait_own(uint32_t bar, uint32_t parity) { return wait_for<false>(bar, parity); }
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity) { return wait_for<true>(bar, parity); }
 
 // The tokens of a pair's range, and of each the keys [k0, k1) that fall into it.
 struct Walk {
@@ -325,7 +331,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (s >= RING) { s -= RING; ph ^= 1; }
       if (s >= RING) { s -= RING; ph ^= 1; }
       *slot = s;
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(B_EMPTY + s), ph)) != 0;
+      ok = __all_sync(0xffffffffu, wait_own(bar(B_EMPTY + s), ph)) != 0;
       return ok;
     };
     auto leave = [&](int count) {
@@ -383,7 +389,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (; ok && w.valid(); w.next(), ++gpc) {
       if (me == 1) {
         // the token's queries, once the last QK^T of the token before is done with the buffer
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(B_QEMPTY), (gpc & 1) ^ 1)) != 0;
+        ok = __all_sync(0xffffffffu, wait_own(bar(B_QEMPTY), (gpc & 1) ^ 1)) != 0;
         if (!ok) break;
         if (elect_one()) {
           if (r == 0) mbar_expect_tx(bar(B_QFULL), 2 * Q_BYTES);
@@ -409,8 +415,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // copies still in flight, those of the peer too (seen at the leader's barriers; a tail entry's bytes land
       // within the same waits)
       if (r == 0) {
-        for (int i = max(0, last - RING + 1); i <= last; ++i) mbar_wait(bar(B_FULL + i % RING), (i / RING) & 1);
-        if (me == 1 && gpc > 0) mbar_wait(bar(B_QFULL), (gpc - 1) & 1);
+        for (int i = max(0, last - RING + 1); i <= last; ++i) wait_own(bar(B_FULL + i % RING), (i / RING) & 1);
+        if (me == 1 && gpc > 0) wait_own(bar(B_QFULL), (gpc - 1) & 1);
       }
     }
   } else if (warp == 1) {
@@ -493,7 +499,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     float* stat = reinterpret_cast<float*>(smem + OFF_STAT);
     const float c2 = p.scale_log2, thr = kRescaleLog2 / c2;
     const uint32_t sfree = lead(B_SFREE), prdy = lead(B_PRDY), trdy = lead(B_TRDY);
-    auto wait_u = [&](uint32_t b, uint32_t par) { return __all_sync(0xffffffffu, mbar_wait(b, par)) != 0; };
+    auto wait_u = [&](uint32_t b, uint32_t par) { return __all_sync(0xffffffffu, wait_own(b, par)) != 0; };
     int js = 0, gpc = 0, tails = 0, nbase = 0;
     for (; ok && w.valid(); w.next(), ++gpc) {
       const int ns = w.steps();
@@ -619,7 +625,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t trow = tmem + ((uint32_t)(32 * quarter) << 16);
     const float* stat = reinterpret_cast<const float*>(smem + OFF_STAT);
     const uint32_t ofree = lead(B_OFREE);
-    auto wait_u = [&](uint32_t b, uint32_t par) { return __all_sync(0xffffffffu, mbar_wait(b, par)) != 0; };
+    auto wait_u = [&](uint32_t b, uint32_t par) { return __all_sync(0xffffffffu, wait_own(b, par)) != 0; };
     int gpc = 0;
     for (; ok && w.valid(); w.next(), ++gpc) {
       if (!wait_u(bar(B_LRDY), gpc & 1)) { ok = false; break; }
