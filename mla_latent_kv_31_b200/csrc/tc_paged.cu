@@ -50,6 +50,7 @@ constexpr int GROUPS = NK / 16;                // a step's rows are looked up in
 constexpr int kThreads = 512;
 constexpr int kMaxPairs = 74;
 constexpr int kStartUnits = 4;                 // a token's fixed cost (query load, epilogue), in units
+constexpr int64_t kPlanTokens = 64;            // tokens looked up in the plan's own launch
 constexpr float kRescaleLog2 = 8.f;            // keep the running maximum until it grows by 2^8
 constexpr int kEntriesK = 9, kEntriesV = 8;    // ring entries of a step: [128 keys x 64], 2 x [64 keys x 64]
 constexpr int RING = 7;
@@ -96,6 +97,7 @@ struct CoreParams {
   int32_t top_k, pairs;
   const int2* tinfo;          // [T]: sequence, visible rows
   const int4* pinfo;          // [pairs]: first token, its first unit, last token, its end unit
+  const int2* pfirst;         // [pairs]: the first token's tinfo
   __nv_bfloat16* o_lat;
   float* lse;
   float4* part_o;             // [2 * pairs][DC / 4][H]
@@ -169,11 +171,22 @@ __device__ __forceinline__ void arrive_pair(uint32_t bar) {
 }
 // Bounded waits on the SM's own clock (about a second; reading the global timer at each miss is slower).
 constexpr long long kWaitCycles = 2000000000ll;
-template <bool CLUSTER>
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool test_bar(uint32_t bar, uint32_t parity) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ bool wait_own(uint32_t bar, uint32_t parity) {
+  if (test_bar(bar, parity)) return true;      // (try_wait costs about 60 cycles more when there is nothing to wait for)
   long long t0 = 0;
   for (uint32_t i = 1;; ++i) {
-    if (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     if ((i & 63) == 0) {
       const long long t = clock64();
       if (t0 == 0) t0 = t;
@@ -181,32 +194,36 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
     }
   }
 }
-__device__ __forceinline__ bool wait_own(uint32_t bar, uint32_t parity) { return wait_for<false>(bar, parity); }
-__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity) { return wait_for<true>(bar, parity); }
+
+// Programmatic dependent launch: the next kernel of the chain may start its prologue; this one waits for the kernel
+// before it (and with it all earlier ones) to be complete and visible.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // The tokens of a pair's range, and of each the keys [k0, k1) that fall into it.
 struct Walk {
   const int2* tinfo;
   int tok, tok1, e1;
   int seq, vis, k0, k1;
-  __device__ void load(int u) {
-    const int2 ti = tinfo[tok];
+  __device__ void set(int2 ti, int u) {
     seq = ti.x;
     vis = ti.y;
     k0 = u * UNIT;
     k1 = tok == tok1 ? min(vis, e1 * UNIT) : vis;
   }
-  __device__ void init(const CoreParams& p, int4 pi) {
+  __device__ void init(const CoreParams& p, int pair) {
+    const int4 pi = p.pinfo[pair];
+    const int2 first = p.pfirst[pair];
     tinfo = p.tinfo;
     tok = pi.x; tok1 = pi.z; e1 = pi.w;
-    if (valid()) load(pi.y);
+    if (valid()) set(first, pi.y);
   }
   __device__ bool valid() const { return tok >= 0 && tok <= tok1; }
   __device__ void next() {
     do {
       ++tok;
       if (tok > tok1) return;
-      load(0);
+      set(tinfo[tok], 0);
     } while (vis <= 0);
   }
   __device__ int steps() const { return (k1 - k0 + NK - 1) / NK; }
@@ -311,8 +328,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<const uint32_t*>(smem + 8 * NBAR);
+  let_next_start();
+  wait_for_previous();
   Walk w;
-  w.init(p, p.pinfo[pair]);
+  w.init(p, pair);
   bool ok = true;
 
   if (warp == 0 || warp == 2 || warp == 3) {
@@ -320,6 +339,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // The three warps take every third entry. (A barrier's parity tells two consecutive phases apart: a warp's own
     // entries are 3 apart, so it never looks at a slot that is more than one lap behind.)
     const int me = warp == 0 ? 0 : warp - 1;
+    auto load_q = [&](int g) {
+      // the token's queries, once the last QK^T of the token before is done with the buffer
+      ok = __all_sync(0xffffffffu, wait_own(bar(B_QEMPTY), (g & 1) ^ 1)) != 0;
+      if (ok && elect_one()) {
+        if (r == 0) mbar_expect_tx(bar(B_QFULL), 2 * Q_BYTES);
+        const int32_t y = w.tok * H + HC * (int)r;
+        for (int c = 0; c < 8; ++c) pair_load(sbase + OFF_Q + c * BOX, &p.qmap, 64 * c, y, lead(B_QFULL));
+        pair_load(sbase + OFF_Q + 8 * BOX, &p.qrmap, 0, y, lead(B_QFULL));
+      }
+      __syncwarp();
+    };
+    if (me == 1 && w.valid()) load_q(0);      // ahead of the block table's latency
     Rows rows;
     rows.init(p, w, lane);
     int base = 0, bph = 1, turn = me;         // slot and parity of the block of entries at hand, this warp's first of it
@@ -387,18 +418,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       leave(kEntriesV);
     };
     for (; ok && w.valid(); w.next(), ++gpc) {
-      if (me == 1) {
-        // the token's queries, once the last QK^T of the token before is done with the buffer
-        ok = __all_sync(0xffffffffu, wait_own(bar(B_QEMPTY), (gpc & 1) ^ 1)) != 0;
-        if (!ok) break;
-        if (elect_one()) {
-          if (r == 0) mbar_expect_tx(bar(B_QFULL), 2 * Q_BYTES);
-          const int32_t y = w.tok * H + HC * (int)r;
-          for (int c = 0; c < 8; ++c) pair_load(sbase + OFF_Q + c * BOX, &p.qmap, 64 * c, y, lead(B_QFULL));
-          pair_load(sbase + OFF_Q + 8 * BOX, &p.qrmap, 0, y, lead(B_QFULL));
-        }
-        __syncwarp();
-      }
+      if (me == 1 && gpc > 0) load_q(gpc);
       // the token's entries: K0 K1 V0 K2 V1 ... K(ns-1) V(ns-2) V(ns-1)
       const int ns = w.steps(), rem = w.k1 - (w.k0 + (ns - 1) * NK);
       int row = -4096;
@@ -425,7 +445,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       constexpr uint32_t id_qk = idesc_bf16(128, NK, 0, 0), id_pv = idesc_bf16(128, 256, 0, 1);
       const uint32_t q_lo = desc_lo(sbase + OFF_Q, 0), p_lo = desc_lo(sbase + OFF_P, 0);
       const uint32_t k_lo = desc_lo(sbase + OFF_RING, 0), v_lo = desc_lo(sbase + OFF_RING, BOX);
-      auto wait_all = [&](uint32_t b, uint32_t par) { return __all_sync(0xffffffffu, wait_cluster(b, par)) != 0; };
+      auto wait_all = [&](uint32_t b, uint32_t par) { return __all_sync(0xffffffffu, wait_own(b, par)) != 0; };
       int js = 0, gpc = 0, tails = 0;         // step, token, tokens that end inside 64 keys
       int slot = 0, ph = 0;
       auto next_entry = [&]() {
@@ -684,18 +704,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ---- plan ---------------------------------------------------------------------------------------------------
-// Sequence and visible rows of every new token, one warp each; the checks of the batch; the empty rows.
-__global__ void __launch_bounds__(256)
-    paged_tokens_kernel(PagedView v, const int32_t* blocks, int32_t top_k, int2* tinfo, __nv_bfloat16* o_lat, float* lse,
-                        uint32_t* err) {
-  if (blockIdx.x == 0) paged_check(v, err);
-  const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (t >= v.total_q) return;
+struct PlanParams {
+  PagedView v;
+  const int32_t* blocks;
+  int32_t top_k, pairs;
+  int2* tinfo;
+  int64_t* cost;
+  int4* pinfo;
+  int2* pfirst;
+  __nv_bfloat16* o_lat;
+  float* lse;
+  uint32_t* err;
+};
+
+// Sequence and visible rows of new token t, by one warp; an empty row is written here.
+__device__ __forceinline__ void plan_token(const PlanParams& p, int64_t t, int lane) {
+  const PagedView& v = p.v;
   const PagedToken tok = paged_token(v, t);
   int64_t vis = tok.pos + 1;
-  if (blocks && vis > 0) {
-    const int32_t* list = blocks + t * top_k;
+  if (p.blocks && vis > 0) {
+    const int top_k = p.top_k;
+    const int32_t* list = p.blocks + t * top_k;
     const int64_t own = tok.pos / v.page;
     int n = top_k, bad = 0, at = -1;          // first -1, a fault, the last block
     for (int i0 = 0; i0 < n; i0 += 32) {
@@ -709,28 +738,48 @@ __global__ void __launch_bounds__(256)
       if (cnt < 32) n = i0 + cnt;
     }
     if (__any_sync(0xffffffffu, bad)) {
-      if (lane == 0) flag_error(err, DEVERR_BLOCKS);
+      if (lane == 0) flag_error(p.err, DEVERR_BLOCKS);
       n = 0;
     }
     vis = n == 0 ? 0 : (int64_t)(n - 1) * v.page + (at == own ? tok.pos % v.page + 1 : v.page);
   }
-  if (lane == 0) tinfo[t] = make_int2(tok.seq, (int32_t)(tok.seq < 0 ? 0 : vis));
+  if (lane == 0) p.tinfo[t] = make_int2(tok.seq, (int32_t)(tok.seq < 0 ? 0 : vis));
   if (tok.seq >= 0 && vis <= 0) {
-    uint4* o = reinterpret_cast<uint4*>(o_lat + t * H * DC);
+    uint4* o = reinterpret_cast<uint4*>(p.o_lat + t * H * DC);
     for (int i = lane; i < H * DC / 8; i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
-    for (int i = lane; i < H; i += 32) lse[t * H + i] = -INFINITY;
+    for (int i = lane; i < H; i += 32) p.lse[t * H + i] = -INFINITY;
   }
 }
 
-// Deals the tokens' units to the pairs (one block). In cost, token t with u_t > 0 units is kStartUnits + u_t
+// The tokens of a large batch, one warp each, and the checks of the batch.
+__global__ void __launch_bounds__(256) paged_tokens_kernel(const __grid_constant__ PlanParams p) {
+  let_next_start();
+  if (blockIdx.x == 0) paged_check(p.v, p.err);
+  const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (t < p.v.total_q) plan_token(p, t, threadIdx.x & 31);
+}
+
+// Deals the tokens' units to the pairs (one block; with TOKENS it also looks the tokens up first). In cost, token t with u_t > 0 units is kStartUnits + u_t
 // long; pair pp's range begins at the first unit whose cost starts at or after pp * total / pairs. Each pair's
 // range is written as (first token, its first unit, last token, its end unit), (-1, ...) if empty.
-__global__ void __launch_bounds__(1024)
-    paged_plan_kernel(const int2* tinfo, int64_t T, int32_t pairs, int64_t* cost, int4* pinfo) {
+template <bool TOKENS>
+__global__ void __launch_bounds__(1024) paged_plan_kernel(const __grid_constant__ PlanParams p) {
   __shared__ int64_t warp_tot[32];
   __shared__ int64_t total;
   __shared__ int32_t btok[kMaxPairs + 1], bunit[kMaxPairs + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t T = p.v.total_q;
+  const int pairs = p.pairs;
+  int2* tinfo = p.tinfo;
+  int64_t* cost = p.cost;
+  let_next_start();
+  if (TOKENS) {
+    paged_check(p.v, p.err);
+    for (int64_t t = warp; t < T; t += 32) plan_token(p, t, lane);
+    __syncthreads();
+  } else {
+    wait_for_previous();
+  }
   auto units = [&](int64_t t) -> int { return (max(tinfo[t].y, 0) + UNIT - 1) / UNIT; };
   auto weight = [&](int u) -> int { return u > 0 ? u + kStartUnits : 0; };
   const int64_t per = (T + 1023) / 1024;
@@ -789,7 +838,8 @@ __global__ void __launch_bounds__(1024)
       ue = e >= 0 ? units(e) : 0;
     }
     const bool any = a < T && (a < e || (a == e && ua < ue));
-    pinfo[pp] = any ? make_int4(a, ua, e, ue) : make_int4(-1, 0, -2, 0);
+    p.pinfo[pp] = any ? make_int4(a, ua, e, ue) : make_int4(-1, 0, -2, 0);
+    if (any) p.pfirst[pp] = tinfo[a];
   }
 }
 
@@ -799,20 +849,25 @@ constexpr int kCombHeads = 32, kCombCols = 64;
 __global__ void __launch_bounds__(256)
     paged_combine_kernel(const int2* tinfo, const int4* pinfo, int32_t pairs, const float4* part_o, const float2* part_ml,
                          __nv_bfloat16* o_lat, float* lse) {
+  __shared__ int4 ranges[kMaxPairs];
   __shared__ int32_t slots[kMaxPairs];
   __shared__ int32_t ns_sh;
+  __shared__ float2 ml[kMaxPairs][kCombHeads];
   __shared__ float wgt[kMaxPairs][kCombHeads];
   __shared__ __align__(16) float tile[kCombHeads][kCombCols + 4];   // written as float4
   const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31, grp = tid >> 5;
+  wait_for_previous();
   const int4 pc = pinfo[c];
   if (pc.x < 0) return;
   const int tok = pc.z, units = (tinfo[tok].y + UNIT - 1) / UNIT;
   if (pc.w >= units || (pc.x == tok && pc.y > 0)) return;
+  for (int d = tid; d < pairs; d += blockDim.x) ranges[d] = pinfo[d];
+  __syncthreads();
   if (tid == 0) {
     int n = 0;
     slots[n++] = 2 * c + (pc.x == tok ? 0 : 1);
     for (int d = c + 1; d < pairs; ++d) {
-      const int4 pd = pinfo[d];
+      const int4 pd = ranges[d];
       if (pd.x < 0) continue;
       slots[n++] = 2 * d;
       if (pd.z != tok || pd.w >= units) break;
@@ -821,25 +876,21 @@ __global__ void __launch_bounds__(256)
   }
   __syncthreads();
   const int ns = ns_sh, h0 = kCombHeads * blockIdx.y, c0 = kCombCols * blockIdx.z;
-  // weights e^{m_s - M} / L of the pieces, by one warp (lane = head)
-  if (grp == 0) {
-    float M = -INFINITY, L = 0.f;
-    for (int s = 0; s < ns; ++s) M = fmaxf(M, part_ml[(int64_t)slots[s] * H + h0 + lane].x);
-    for (int s = 0; s < ns; ++s) {
-      const float2 ml = part_ml[(int64_t)slots[s] * H + h0 + lane];
-      const float e = ml.x > -INFINITY ? __expf(ml.x - M) : 0.f;
-      wgt[s][lane] = e;
-      L += e * ml.y;
-    }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    for (int s = 0; s < ns; ++s) wgt[s][lane] *= inv;
-    if (blockIdx.z == 0) lse[(int64_t)tok * H + h0 + lane] = L == 0.f ? -INFINITY : M + logf(L);
-  }
+  for (int s = grp; s < ns; s += 8) ml[s][lane] = part_ml[(int64_t)slots[s] * H + h0 + lane];
+  __syncthreads();
+  // weights e^{m_s - M} / L of the pieces (lane = head; the warps share the pieces, each finds M and L itself)
+  float M = -INFINITY, L = 0.f;
+  for (int s = 0; s < ns; ++s) M = fmaxf(M, ml[s][lane].x);
+  for (int s = 0; s < ns; ++s)
+    if (ml[s][lane].x > -INFINITY) L += __expf(ml[s][lane].x - M) * ml[s][lane].y;
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  for (int s = grp; s < ns; s += 8) wgt[s][lane] = ml[s][lane].x > -INFINITY ? __expf(ml[s][lane].x - M) * inv : 0.f;
+  if (grp == 0 && blockIdx.z == 0) lse[(int64_t)tok * H + h0 + lane] = L == 0.f ? -INFINITY : M + logf(L);
   __syncthreads();
   // thread (lane = head, grp): column quads 2 grp, 2 grp + 1 of this block's 16
   float4 acc[2];
   acc[0] = acc[1] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
   for (int s = 0; s < ns; ++s) {
     const float4* src = part_o + ((int64_t)slots[s] * (DC / 4) + c0 / 4 + 2 * grp) * H + h0 + lane;
     const float e = wgt[s][lane];
@@ -859,14 +910,30 @@ __global__ void __launch_bounds__(256)
       make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
+// Launches a kernel of the chain behind the one before it: its blocks may start early and wait in
+// wait_for_previous(), so that launch latency and prologue overlap the kernel before.
+template <typename... Params, typename... Args>
+cudaError_t launch_next(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, Args... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int GRAN>
 cudaError_t launch_core(const CoreParams& p, cudaStream_t st) {
   // per device, so set at every call
   cudaError_t e = cudaFuncSetAttribute(paged_core_kernel<GRAN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  paged_core_kernel<GRAN><<<(unsigned)(2 * p.pairs), kThreads, SMEM_BYTES, st>>>(p);
-  note_launch();
-  return cudaGetLastError();
+  return launch_next(paged_core_kernel<GRAN>, dim3(2 * p.pairs), kThreads, SMEM_BYTES, st, p);
 }
 
 size_t align1k(size_t x) { return (x + 1023) / 1024 * 1024; }
@@ -875,6 +942,7 @@ struct Scratch {
   int2* tinfo;
   int64_t* cost;
   int4* pinfo;
+  int2* pfirst;
   float2* part_ml;
   float4* part_o;
   size_t bytes;
@@ -889,6 +957,8 @@ Scratch carve(void* ws, int64_t T) {
   p += align1k((size_t)T * sizeof(int64_t));
   s.pinfo = (int4*)p;
   p += align1k(kMaxPairs * sizeof(int4));
+  s.pfirst = (int2*)p;
+  p += align1k(kMaxPairs * sizeof(int2));
   s.part_ml = (float2*)p;
   p += align1k((size_t)2 * kMaxPairs * H * sizeof(float2));
   s.part_o = (float4*)p;
@@ -920,24 +990,44 @@ cudaError_t tc_paged_attention(const PagedView& v, const void* q_abs, const void
   p.pairs = num_sms / 2 < kMaxPairs ? num_sms / 2 : kMaxPairs;
   p.tinfo = s.tinfo;
   p.pinfo = s.pinfo;
+  p.pfirst = s.pfirst;
   p.o_lat = (__nv_bfloat16*)o_lat;
   p.lse = lse;
   p.part_o = s.part_o;
   p.part_ml = s.part_ml;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.err = err;
-  paged_tokens_kernel<<<(unsigned)((v.total_q + 7) / 8), 256, 0, st>>>(v, blocks, top_k, s.tinfo, p.o_lat, lse, err);
-  paged_plan_kernel<<<1, 1024, 0, st>>>(s.tinfo, v.total_q, p.pairs, s.cost, s.pinfo);
-  note_launch(2);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  PlanParams pp;
+  pp.v = v;
+  pp.blocks = blocks;
+  pp.top_k = top_k;
+  pp.pairs = p.pairs;
+  pp.tinfo = s.tinfo;
+  pp.cost = s.cost;
+  pp.pinfo = s.pinfo;
+  pp.pfirst = s.pfirst;
+  pp.o_lat = p.o_lat;
+  pp.lse = lse;
+  pp.err = err;
+  // One block looks up few tokens in the plan's own launch; each of its 32 warps takes a token in about 1 us (a list of
+  // blocks is read for it), so more than kPlanTokens of them get a launch of their own.
+  if (v.total_q <= kPlanTokens) {
+    paged_plan_kernel<true><<<1, 1024, 0, st>>>(pp);
+    note_launch();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  } else {
+    paged_tokens_kernel<<<(unsigned)((v.total_q + 7) / 8), 256, 0, st>>>(pp);
+    note_launch();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_next(paged_plan_kernel<false>, dim3(1), 1024, 0, st, pp)) != cudaSuccess) return e;
+  }
   e = gran == 64 ? launch_core<64>(p, st) : gran == 32 ? launch_core<32>(p, st) : launch_core<16>(p, st);
   if (e != cudaSuccess) return e;
-  if (p.pairs > 1) {
-    paged_combine_kernel<<<dim3((unsigned)(p.pairs - 1), H / kCombHeads, DC / kCombCols), 256, 0, st>>>(
-        s.tinfo, s.pinfo, p.pairs, s.part_o, s.part_ml, p.o_lat, lse);
-    note_launch();
-  }
-  return cudaGetLastError();
+  if (p.pairs > 1)
+    e = launch_next(paged_combine_kernel, dim3((unsigned)(p.pairs - 1), H / kCombHeads, DC / kCombCols), 256, 0, st,
+                    (const int2*)s.tinfo, (const int4*)s.pinfo, p.pairs, (const float4*)s.part_o, (const float2*)s.part_ml,
+                    p.o_lat, lse);
+  return e;
 }
 
 }  // namespace mla
