@@ -712,6 +712,7 @@ struct PlanParams {
   int64_t* cost;
   int4* pinfo;
   int2* pfirst;
+  int32_t* splits;            // [pairs]: the pairs in whose range a token begins that goes on in the next, then -1
   __nv_bfloat16* o_lat;
   float* lse;
   uint32_t* err;
@@ -767,6 +768,7 @@ __global__ void __launch_bounds__(1024) paged_plan_kernel(const __grid_constant_
   __shared__ int64_t warp_tot[32];
   __shared__ int64_t total;
   __shared__ int32_t btok[kMaxPairs + 1], bunit[kMaxPairs + 1];
+  __shared__ bool begins[kMaxPairs];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t T = p.v.total_q;
   const int pairs = p.pairs;
@@ -840,30 +842,43 @@ __global__ void __launch_bounds__(1024) paged_plan_kernel(const __grid_constant_
     const bool any = a < T && (a < e || (a == e && ua < ue));
     p.pinfo[pp] = any ? make_int4(a, ua, e, ue) : make_int4(-1, 0, -2, 0);
     if (any) p.pfirst[pp] = tinfo[a];
+    begins[pp] = any && ue < units(e) && !(a == e && ua > 0);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int n = 0;
+    for (int p0 = 0; p0 < pairs; p0 += 32) {
+      const bool is = p0 + lane < pairs && begins[p0 + lane];
+      const uint32_t m = __ballot_sync(0xffffffffu, is);
+      if (is) p.splits[n + __popc(m & ((1u << lane) - 1u))] = p0 + lane;
+      n += __popc(m);
+    }
+    for (int k = n + lane; k < pairs; k += 32) p.splits[k] = -1;
   }
 }
 
-// Exact merge of the tokens that cross ranges. Block (c, heads, columns) takes the token that begins in pair c's range
-// and goes on in the next: o = sum_s e^{m_s - M} O_s / sum_s e^{m_s - M} l_s over its pieces, in order.
-constexpr int kCombHeads = 32, kCombCols = 64;
+// Exact merge of the tokens that cross ranges. Block (k, heads, columns) takes the k-th of them, the one that begins
+// in the range of pair splits[k] and goes on in the next: o = sum_s e^{m_s - M} O_s / sum_s e^{m_s - M} l_s over its
+// pieces, in order.
+constexpr int kCombHeads = 32, kCombCols = 32;
 __global__ void __launch_bounds__(256)
-    paged_combine_kernel(const int2* tinfo, const int4* pinfo, int32_t pairs, const float4* part_o, const float2* part_ml,
-                         __nv_bfloat16* o_lat, float* lse) {
+    paged_combine_kernel(const int2* tinfo, const int4* pinfo, const int32_t* splits, int32_t pairs,
+                         const float4* part_o, const float2* part_ml, __nv_bfloat16* o_lat, float* lse) {
   __shared__ int4 ranges[kMaxPairs];
   __shared__ int32_t slots[kMaxPairs];
   __shared__ int32_t ns_sh;
-  __shared__ float2 ml[kMaxPairs][kCombHeads];
-  __shared__ float wgt[kMaxPairs][kCombHeads];
+  __shared__ float2 ml[kMaxPairs][kCombHeads];     // maximum and sum of each piece, then its weight
   __shared__ __align__(16) float tile[kCombHeads][kCombCols + 4];   // written as float4
-  const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31, grp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, grp = tid >> 5;
   wait_for_previous();
-  const int4 pc = pinfo[c];
-  if (pc.x < 0) return;
-  const int tok = pc.z, units = (tinfo[tok].y + UNIT - 1) / UNIT;
-  if (pc.w >= units || (pc.x == tok && pc.y > 0)) return;
+  const int c = splits[blockIdx.x];
+  if (c < 0) return;
   for (int d = tid; d < pairs; d += blockDim.x) ranges[d] = pinfo[d];
   __syncthreads();
+  const int4 pc = ranges[c];
+  const int tok = pc.z;
   if (tid == 0) {
+    const int units = (tinfo[tok].y + UNIT - 1) / UNIT;
     int n = 0;
     slots[n++] = 2 * c + (pc.x == tok ? 0 : 1);
     for (int d = c + 1; d < pairs; ++d) {
@@ -884,30 +899,26 @@ __global__ void __launch_bounds__(256)
   for (int s = 0; s < ns; ++s)
     if (ml[s][lane].x > -INFINITY) L += __expf(ml[s][lane].x - M) * ml[s][lane].y;
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  for (int s = grp; s < ns; s += 8) wgt[s][lane] = ml[s][lane].x > -INFINITY ? __expf(ml[s][lane].x - M) * inv : 0.f;
+  __syncthreads();
+  for (int s = grp; s < ns; s += 8) ml[s][lane].x = ml[s][lane].x > -INFINITY ? __expf(ml[s][lane].x - M) * inv : 0.f;
   if (grp == 0 && blockIdx.z == 0) lse[(int64_t)tok * H + h0 + lane] = L == 0.f ? -INFINITY : M + logf(L);
   __syncthreads();
-  // thread (lane = head, grp): column quads 2 grp, 2 grp + 1 of this block's 16
-  float4 acc[2];
-  acc[0] = acc[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+  // thread (lane = head, grp): the column quad grp of this block's 8
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float4* src = part_o + (int64_t)(c0 / 4 + grp) * H + h0 + lane;
 #pragma unroll 8
   for (int s = 0; s < ns; ++s) {
-    const float4* src = part_o + ((int64_t)slots[s] * (DC / 4) + c0 / 4 + 2 * grp) * H + h0 + lane;
-    const float e = wgt[s][lane];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const float4 x = src[q * H];
-      acc[q].x += e * x.x; acc[q].y += e * x.y; acc[q].z += e * x.z; acc[q].w += e * x.w;
-    }
+    const float4 x = src[(int64_t)slots[s] * (DC / 4) * H];
+    const float e = ml[s][lane].x;
+    acc.x += e * x.x; acc.y += e * x.y; acc.z += e * x.z; acc.w += e * x.w;
   }
-#pragma unroll
-  for (int q = 0; q < 2; ++q) *reinterpret_cast<float4*>(&tile[lane][8 * grp + 4 * q]) = acc[q];
+  *reinterpret_cast<float4*>(&tile[lane][4 * grp]) = acc;
   __syncthreads();
-  // head tid / 8, 8 columns each
-  const int h = tid >> 3, cc = 8 * (tid & 7);
+  // head tid / 8, 4 columns each
+  const int h = tid >> 3, cc = 4 * (tid & 7);
   const float* x = &tile[h][cc];
-  *reinterpret_cast<uint4*>(o_lat + ((int64_t)tok * H + h0 + h) * DC + c0 + cc) =
-      make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+  *reinterpret_cast<uint2*>(o_lat + ((int64_t)tok * H + h0 + h) * DC + c0 + cc) =
+      make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
 }
 
 // Launches a kernel of the chain behind the one before it: its blocks may start early and wait in
@@ -943,6 +954,7 @@ struct Scratch {
   int64_t* cost;
   int4* pinfo;
   int2* pfirst;
+  int32_t* splits;
   float2* part_ml;
   float4* part_o;
   size_t bytes;
@@ -959,6 +971,8 @@ Scratch carve(void* ws, int64_t T) {
   p += align1k(kMaxPairs * sizeof(int4));
   s.pfirst = (int2*)p;
   p += align1k(kMaxPairs * sizeof(int2));
+  s.splits = (int32_t*)p;
+  p += align1k(kMaxPairs * sizeof(int32_t));
   s.part_ml = (float2*)p;
   p += align1k((size_t)2 * kMaxPairs * H * sizeof(float2));
   s.part_o = (float4*)p;
@@ -1006,6 +1020,7 @@ cudaError_t tc_paged_attention(const PagedView& v, const void* q_abs, const void
   pp.cost = s.cost;
   pp.pinfo = s.pinfo;
   pp.pfirst = s.pfirst;
+  pp.splits = s.splits;
   pp.o_lat = p.o_lat;
   pp.lse = lse;
   pp.err = err;
@@ -1023,10 +1038,12 @@ cudaError_t tc_paged_attention(const PagedView& v, const void* q_abs, const void
   }
   e = gran == 64 ? launch_core<64>(p, st) : gran == 32 ? launch_core<32>(p, st) : launch_core<16>(p, st);
   if (e != cudaSuccess) return e;
-  if (p.pairs > 1)
-    e = launch_next(paged_combine_kernel, dim3((unsigned)(p.pairs - 1), H / kCombHeads, DC / kCombCols), 256, 0, st,
-                    (const int2*)s.tinfo, (const int4*)s.pinfo, p.pairs, (const float4*)s.part_o, (const float2*)s.part_ml,
-                    p.o_lat, lse);
+  // at most one token per boundary, and no more than there are, goes on in the next pair's range
+  const int64_t most = p.pairs - 1 < v.total_q ? p.pairs - 1 : v.total_q;
+  if (most > 0)
+    e = launch_next(paged_combine_kernel, dim3((unsigned)most, H / kCombHeads, DC / kCombCols), 256, 0, st,
+                    (const int2*)s.tinfo, (const int4*)s.pinfo, (const int32_t*)s.splits, p.pairs,
+                    (const float4*)s.part_o, (const float2*)s.part_ml, p.o_lat, lse);
   return e;
 }
 
