@@ -123,7 +123,7 @@ mla_status_t mla_attn_paged_sparse(mla_handle_t* h, const mla_paged_t* batch, co
 
 mla_status_t mla_paged_select_workspace(const mla_handle_t* h, int64_t total_q, int64_t max_pages, size_t* bytes) {
   if (!h || !bytes || total_q <= 0 || max_pages <= 0) return MLA_ERR_INVALID_ARG;
-  *bytes = mla::paged_select_bytes(h->dims.n_h, h->dims.d_c, h->dims.d_r, total_q, max_pages);
+  *bytes = mla::paged_select_bytes(tc_dims(h), h->dims.n_h, h->dims.d_c, h->dims.d_r, total_q, max_pages);
   return MLA_OK;
 }
 
@@ -146,7 +146,7 @@ mla_status_t mla_paged_select(mla_handle_t* h, const mla_paged_t* batch, const v
   if (!g.ok) return MLA_ERR_CUDA;
   if ((s = ensure_device(h)) != MLA_OK) return s;
   return cuda_status(mla::paged_select(v, tc_dims(h), q_abs, q_rope, summaries, top_k, n_first, n_last, blocks, ws,
-                                       h->d_err, (cudaStream_t)stream));
+                                       h->num_sms, h->d_err, (cudaStream_t)stream));
 }
 
 }  // extern "C"

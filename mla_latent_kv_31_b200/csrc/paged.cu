@@ -4,6 +4,7 @@
 #include <math.h>
 
 #include "paged.cuh"
+#include "tc_paged.cuh"
 
 namespace mla {
 namespace {
@@ -181,15 +182,14 @@ __global__ void __launch_bounds__(ATT)
 }
 
 // ---- selection ----------------------------------------------------------------------------------------------
-// Codes and scale of each query row [q~_i | q^R_i] (one warp per row).
-template <typename T>
+// Codes and scale of each fp32 query row [q~_i | q^R_i] (one warp per row); bf16 takes tc_select.cu.
 __global__ void __launch_bounds__(256)
-    query_codes_kernel(PagedView v, const T* q_abs, const T* q_rope, int8_t* codes, float* scales, uint32_t* err) {
+    query_codes_kernel(PagedView v, const float* q_abs, const float* q_rope, int8_t* codes, float* scales, uint32_t* err) {
   if (blockIdx.x == 0) paged_check(v, err);
   const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31, W = v.d_c + v.d_r;
   if (r >= v.total_q * v.n_h || r / v.n_h >= v.cu_q[v.B]) return;
-  auto at = [&](int c) { return c < v.d_c ? to_f(q_abs[r * v.d_c + c]) : to_f(q_rope[r * v.d_r + c - v.d_c]); };
+  auto at = [&](int c) { return c < v.d_c ? q_abs[r * v.d_c + c] : q_rope[r * v.d_r + c - v.d_c]; };
   float amax = 0.f;
   for (int c = lane; c < W; c += 32) amax = fmaxf(amax, fabsf(at(c)));
   const float s = code_scale(warp_max(amax));
@@ -242,57 +242,77 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// The chosen blocks of one token, by a radix select (8 bits a pass) and an ordered write.
-__global__ void __launch_bounds__(256)
+// The chosen blocks of one token: the threshold bit by bit (the largest key that at least `want` keys reach; a
+// count over the keys for each bit below the first in which they differ), then an ordered write. Counting costs
+// about 100 cycles a bit; a histogram's atomics serialise, since the keys share their leading bits.
+// Up to kSelectKeys keys are kept in shared memory, more are read from L2 at every pass.
+constexpr int kSelectThreads = 512, kSelectKeys = 8192;
+__global__ void __launch_bounds__(kSelectThreads)
     select_kernel(PagedView v, const float* scores, int32_t top_k, int32_t n_first, int32_t n_last, int32_t* blocks) {
-  __shared__ int hist[256];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_left;
-  __shared__ int wsum[8][2];
+  __shared__ uint32_t keys[kSelectKeys];
+  __shared__ uint32_t red[2][kSelectThreads / 32];
+  __shared__ int wsum[kSelectThreads / 32][2];
   const int64_t t = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int NW = kSelectThreads / 32;
   const PagedToken tok = paged_token(v, t);
   if (tok.seq < 0) return;
   int32_t* out = blocks + t * top_k;
-  const int64_t nb = tok.pos < 0 ? 0 : tok.pos / v.page + 1;
+  const int nb = tok.pos < 0 ? 0 : (int)(tok.pos / v.page) + 1;
   if (nb <= top_k) {
-    for (int i = tid; i < top_k; i += blockDim.x) out[i] = i < nb ? i : -1;
+    for (int i = tid; i < top_k; i += kSelectThreads) out[i] = i < nb ? i : -1;
     return;
   }
-  const float* sc = scores + t * v.max_pages;
-  const int64_t lo = n_first, hi = nb - n_last;       // candidates
+  const int lo = n_first, hi = nb - n_last;           // candidates
   const int want = top_k - n_first - n_last;
-  for (int i = tid; i < n_first; i += blockDim.x) out[i] = i;
-  for (int i = tid; i < n_last; i += blockDim.x) out[top_k - n_last + i] = (int32_t)(hi + i);
+  for (int i = tid; i < n_first; i += kSelectThreads) out[i] = i;
+  for (int i = tid; i < n_last; i += kSelectThreads) out[top_k - n_last + i] = hi + i;
   if (want == 0) return;
-  uint32_t prefix = 0, mask = 0;
-  int left = want;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    hist[tid] = 0;
-    __syncthreads();
-    for (int64_t g = lo + tid; g < hi; g += blockDim.x) {
-      const uint32_t k = key_of(sc[g]);
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
-    }
-    __syncthreads();
-    if (tid == 0) {
-      int d = 255, n = left;
-      while (hist[d] < n) n -= hist[d--];
-      s_prefix = prefix | ((uint32_t)d << shift);
-      s_left = n;
-    }
-    __syncthreads();
-    prefix = s_prefix;
-    left = s_left;
-    mask |= 255u << shift;
-    __syncthreads();
+  const float* sc = scores + t * v.max_pages;
+  const bool held = hi - lo <= kSelectKeys;
+  auto key = [&](int g) { return held ? keys[g - lo] : key_of(sc[g]); };
+  uint32_t mn = 0xffffffffu, mx = 0;
+  for (int g = lo + tid; g < hi; g += kSelectThreads) {
+    const uint32_t k = key_of(sc[g]);
+    if (held) keys[g - lo] = k;
+    mn = min(mn, k);
+    mx = max(mx, k);
   }
-  // all keys above `prefix`, and the first `left` of those equal to it, in the order of the blocks
+  mn = __reduce_min_sync(0xffffffffu, mn);
+  mx = __reduce_max_sync(0xffffffffu, mx);
+  if (lane == 0) {
+    red[0][warp] = mn;
+    red[1][warp] = mx;
+  }
+  __syncthreads();
+  for (int w = 0; w < NW; ++w) {
+    mn = min(mn, red[0][w]);
+    mx = max(mx, red[1][w]);
+  }
+  // keys agree above bit `top`
+  const int top = mn == mx ? -1 : 31 - __clz(mn ^ mx);
+  uint32_t thr = top < 0 ? mx : top == 31 ? 0u : mx & ~((2u << top) - 1u);
+  int par = 0;
+  auto count = [&](uint32_t floor_key) -> int {        // keys >= floor_key
+    int c = 0;
+    for (int g = lo + tid; g < hi; g += kSelectThreads) c += key(g) >= floor_key;
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (lane == 0) wsum[warp][par] = c;
+    __syncthreads();
+    int all = 0;
+    for (int w = 0; w < NW; ++w) all += wsum[w][par];
+    par ^= 1;                                          // the next count writes the other column
+    return all;
+  };
+  for (int bit = top; bit >= 0; --bit)
+    if (count(thr | (1u << bit)) >= want) thr |= 1u << bit;
+  const int left = want - (thr == 0xffffffffu ? 0 : count(thr + 1));     // of the keys equal to thr, the first `left`
+  __syncthreads();
   int done = n_first, eq_done = 0;
-  for (int64_t g0 = lo; g0 < hi; g0 += blockDim.x) {
-    const int64_t g = g0 + tid;
-    const uint32_t k = g < hi ? key_of(sc[g]) : 0;
-    const bool gt = g < hi && k > prefix, eq = g < hi && k == prefix;
+  for (int g0 = lo; g0 < hi; g0 += kSelectThreads) {
+    const int g = g0 + tid;
+    const uint32_t k = g < hi ? key(g) : 0;
+    const bool gt = g < hi && k > thr, eq = g < hi && k == thr;
     const uint32_t below = (1u << lane) - 1u;
     const uint32_t mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
     if (lane == 0) {
@@ -301,7 +321,7 @@ __global__ void __launch_bounds__(256)
     }
     __syncthreads();
     int g_before = __popc(mg & below), e_before = __popc(me & below), g_all = 0, e_all = 0;
-    for (int w = 0; w < 8; ++w) {
+    for (int w = 0; w < NW; ++w) {
       if (w < warp) {
         g_before += wsum[w][0];
         e_before += wsum[w][1];
@@ -309,8 +329,8 @@ __global__ void __launch_bounds__(256)
       g_all += wsum[w][0];
       e_all += wsum[w][1];
     }
-    const int rank = eq_done + e_before;              // of this key among the equal ones
-    if (gt || (eq && rank < left)) out[done + g_before + min(rank, left) - min(eq_done, left)] = (int32_t)g;
+    const int rank = eq_done + e_before;               // of this key among the equal ones
+    if (gt || (eq && rank < left)) out[done + g_before + min(rank, left) - min(eq_done, left)] = g;
     done += g_all + min(eq_done + e_all, left) - min(eq_done, left);
     eq_done += e_all;
     __syncthreads();
@@ -354,33 +374,33 @@ cudaError_t paged_attention_simt(const PagedView& v, const void* q_abs, const vo
   return cudaGetLastError();
 }
 
-size_t paged_select_bytes(int32_t n_h, int32_t d_c, int32_t d_r, int64_t total_q, int64_t max_pages) {
-  const size_t rows = (size_t)total_q * n_h;
-  return align1k(rows * (d_c + d_r)) + align1k(rows * 4) + align1k((size_t)total_q * max_pages * 4);
+size_t paged_select_bytes(bool bf16, int32_t n_h, int32_t d_c, int32_t d_r, int64_t total_q, int64_t max_pages) {
+  const size_t rows = (size_t)total_q * n_h, scores = align1k((size_t)total_q * max_pages * 4);
+  return bf16 ? scores : scores + align1k(rows * (d_c + d_r)) + align1k(rows * 4);
 }
 
 cudaError_t paged_select(const PagedView& v, bool bf16, const void* q_abs, const void* q_rope, const void* summaries,
-                         int32_t top_k, int32_t n_first, int32_t n_last, int32_t* blocks, void* ws, uint32_t* err,
-                         cudaStream_t st) {
-  const size_t rows = (size_t)v.total_q * v.n_h, W = (size_t)v.d_c + v.d_r;
-  int8_t* codes = (int8_t*)ws;
-  float* scales = (float*)((char*)ws + align1k(rows * W));
-  float* scores = (float*)((char*)scales + align1k(rows * 4));
-  const unsigned qgrid = (unsigned)((rows + 7) / 8);
-  if (bf16)
-    query_codes_kernel<__nv_bfloat16><<<qgrid, 256, 0, st>>>(v, (const __nv_bfloat16*)q_abs,
-                                                             (const __nv_bfloat16*)q_rope, codes, scales, err);
-  else
-    query_codes_kernel<float><<<qgrid, 256, 0, st>>>(v, (const float*)q_abs, (const float*)q_rope, codes, scales, err);
-  note_launch();
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  score_kernel<<<dim3((unsigned)((v.max_pages + 31) / 32), (unsigned)v.total_q), 32 * SCORE_WARPS,
-                 32 * ((W / 4) | 1) * 4, st>>>(v, codes, scales, (const uint8_t*)summaries,
-                                               (int64_t)summary_pitch(v.d_c, v.d_r), top_k, scores, err);
-  note_launch();
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  select_kernel<<<(unsigned)v.total_q, 256, 0, st>>>(v, scores, top_k, n_first, n_last, blocks);
+                         int32_t top_k, int32_t n_first, int32_t n_last, int32_t* blocks, void* ws, int num_sms,
+                         uint32_t* err, cudaStream_t st) {
+  float* scores = (float*)ws;
+  cudaError_t e;
+  if (bf16) {
+    if ((e = tc_select_scores(v, q_abs, q_rope, summaries, top_k, scores, num_sms, err, st)) != cudaSuccess) return e;
+  } else {
+    const size_t rows = (size_t)v.total_q * v.n_h, W = (size_t)v.d_c + v.d_r;
+    int8_t* codes = (int8_t*)ws + align1k((size_t)v.total_q * v.max_pages * 4);
+    float* scales = (float*)(codes + align1k(rows * W));
+    query_codes_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(v, (const float*)q_abs, (const float*)q_rope, codes,
+                                                                   scales, err);
+    note_launch();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    score_kernel<<<dim3((unsigned)((v.max_pages + 31) / 32), (unsigned)v.total_q), 32 * SCORE_WARPS,
+                   32 * ((W / 4) | 1) * 4, st>>>(v, codes, scales, (const uint8_t*)summaries,
+                                                 (int64_t)summary_pitch(v.d_c, v.d_r), top_k, scores, err);
+    note_launch();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  select_kernel<<<(unsigned)v.total_q, kSelectThreads, 0, st>>>(v, scores, top_k, n_first, n_last, blocks);
   note_launch();
   return cudaGetLastError();
 }

@@ -100,9 +100,9 @@ cudaError_t paged_attention_simt(const PagedView& v, const void* q_abs, const vo
                                  const int32_t* blocks, int32_t top_k, float scale, void* o_lat, float* lse,
                                  uint32_t* err, cudaStream_t st);
 
-size_t paged_select_bytes(int32_t n_h, int32_t d_c, int32_t d_r, int64_t total_q, int64_t max_pages);
+size_t paged_select_bytes(bool bf16, int32_t n_h, int32_t d_c, int32_t d_r, int64_t total_q, int64_t max_pages);
 cudaError_t paged_select(const PagedView& v, bool bf16, const void* q_abs, const void* q_rope, const void* summaries,
-                         int32_t top_k, int32_t n_first, int32_t n_last, int32_t* blocks, void* ws, uint32_t* err,
-                         cudaStream_t st);
+                         int32_t top_k, int32_t n_first, int32_t n_last, int32_t* blocks, void* ws, int num_sms,
+                         uint32_t* err, cudaStream_t st);
 
 }  // namespace mla

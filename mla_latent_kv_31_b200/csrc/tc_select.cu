@@ -1,0 +1,268 @@
+// Scores of the choice of blocks (mla_paged_select) at the DeepSeek-V3 sizes on the tensor cores: for token t and
+// block g, max_i s_i (x_i . y_g) with int8 codes x_i of the 128 query rows [q~_i | q^R_i] and y_g of the block's
+// summary, times the summary's scale. The products are whole numbers (kind::i8, int32 accumulation): exact.
+//
+// A CTA takes one token and every gridDim.x-th tile of 128 blocks. It quantises the token's queries into shared memory
+// once (they are read from HBM once per CTA), then per tile gathers 128 summary rows (cp.async, the rows of a tile
+// lie anywhere) and multiplies: M = 128 blocks, N = 128 heads, K = 576, 18 MMAs of K = 32. With the blocks on the
+// lanes the maximum over the heads stays in a thread. Two buffers of summaries and two accumulators, so that the
+// next tile is fetched and multiplied while a tile's maxima are taken.
+// Bounds: the queries' bytes (147 KB a token) for chunks; the chain of latencies for a few tokens.
+#include <cuda_bf16.h>
+
+#include "paged.cuh"
+#include "sm100.cuh"
+#include "tc_paged.cuh"
+
+namespace mla {
+namespace {
+
+using namespace sm100;
+
+constexpr int H = 128, DC = 512, DR = 64, W = DC + DR;
+constexpr int TILE = 128;                       // blocks per tile
+constexpr int kThreads = 512;
+constexpr uint32_t KBOX = 128 * 128;            // [128 rows x 128 codes], 128-byte swizzle
+// A row is 4.5 boxes wide: the two summary buffers share the ninth box (codes 512 .. 575 in its left or right half),
+// which leaves room for both beside the queries.
+constexpr uint32_t OFF_Q = 0;                                  // 5 boxes
+constexpr uint32_t OFF_Y = OFF_Q + 5 * KBOX;                   // 2 x 4 boxes, then the shared one
+constexpr uint32_t OFF_YH = OFF_Y + 8 * KBOX;
+constexpr uint32_t OFF_SQ = OFF_YH + KBOX;                     // [128] scales of the queries
+constexpr uint32_t OFF_BAR = OFF_SQ + H * 4;                   // 2 barriers, TMEM address
+constexpr uint32_t SMEM_BYTES = OFF_BAR + 32 + 1024;
+static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+// The right half of the queries' fifth box is free: chunk c (4 .. 7) of row r holds 16 bytes of what goes with
+// block r of a tile: the summaries' scales of the two buffers (4), the maxima of the column groups 1 .. 3 (5).
+__device__ __forceinline__ uint32_t row_chunk(int r, int c) {
+  return OFF_Q + 4 * KBOX + r * 128 + ((c ^ (r & 7)) << 4);
+}
+
+// kind::i8: signed 8-bit A and B, 32-bit integer D, both K-major.
+constexpr uint32_t idesc_i8(int M, int N) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_i8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// 16 bytes from global to shared memory, or zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool zero) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(zero ? 0 : 16) : "memory");
+}
+
+// x / s to the nearest whole number (ties to even) as an IEEE division gives it, without dividing: x * (1 / s) is
+// within 2e-5 of it for |x / s| <= 127, so only values that near to a tie take the division.
+__device__ __forceinline__ int code_fast(float x, float s, float inv) {
+  const float r = x * inv;
+  float n = rintf(r);
+  if (fabsf(fabsf(r - n) - 0.5f) < 1e-4f) n = rintf(__fdiv_rn(x, s));
+  return x == x ? (int)fminf(fmaxf(n, -127.f), 127.f) : 0;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    select_score_kernel(PagedView v, const __nv_bfloat16* q_abs, const __nv_bfloat16* q_rope, const uint8_t* summaries,
+                        int64_t pitch, int32_t top_k, float* scores, uint32_t* err) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_addr(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t t = blockIdx.y;
+  if (blockIdx.x == 0 && t == 0) paged_check(v, err);
+  const PagedToken tok = paged_token(v, t);
+  if (tok.pos < 0) return;
+  const int nb = (int)(tok.pos / v.page) + 1;
+  const int stride = gridDim.x, first = blockIdx.x;
+  const int tiles = (nb + TILE - 1) / TILE;
+  if (nb <= top_k || first >= tiles) return;
+  const int n = (tiles - first + stride - 1) / stride;        // tiles of this CTA
+  auto bar = [&](int i) { return sbase + OFF_BAR + 8u * (uint32_t)i; };
+
+  // The page of this thread's row (four threads a row) of the i-th tile, -1 for none.
+  auto page_of = [&](int i) -> int {
+    const int g = (first + i * stride) * TILE + (tid >> 2);
+    if (i >= n || g >= nb) return -1;
+    const int p = v.table[(int64_t)tok.seq * v.stride + g];
+    if (p < 0 || p >= v.num_pages) {
+      flag_error(err, DEVERR_PAGE);
+      return -1;
+    }
+    return p;
+  };
+  // Summary rows of the i-th tile into buffer i & 1: chunks (tid & 3) + 4 k of the thread's row.
+  auto fetch = [&](int i, int page) {
+    const int row = tid >> 2, b = i & 1;
+    const uint8_t* src = summaries + (int64_t)(page < 0 ? 0 : page) * pitch;
+    const uint32_t drow = row * 128;
+#pragma unroll
+    for (int k = 0; k < 9; ++k) {
+      const int c = (tid & 3) + 4 * k;                        // 16-byte chunk 0 .. 35
+      const uint32_t dst = k < 8 ? OFF_Y + (4 * b + (c >> 3)) * KBOX + drow + (((c & 7) ^ (row & 7)) << 4)
+                                 : OFF_YH + drow + (((4 * b + (c & 3)) ^ (row & 7)) << 4);
+      copy16(sbase + dst, src + 16 * c, page < 0);
+    }
+    if ((tid & 3) == 0)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(sbase + row_chunk(row, 4) + 4 * b),
+                   "l"(src + W), "r"(page < 0 ? 0 : 4)
+                   : "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+
+  int page = page_of(0);
+  if (tid == 0) {
+    mbar_init(bar(0), 1);
+    mbar_init(bar(1), 1);
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(bar(2), 256);
+    tmem_relinquish();
+  }
+  fetch(0, page);
+  int page_next = page_of(1);
+  // ---- the queries' codes, a warp a row: lane takes chunks of 8 elements lane, lane + 32 and (lanes 0-7) 64 + lane
+  float* sq = reinterpret_cast<float*>(smem + OFF_SQ);
+#pragma unroll 2
+  for (int i = warp; i < H; i += kThreads / 32) {
+    const uint4* qa = reinterpret_cast<const uint4*>(q_abs + (t * H + i) * DC);
+    const uint4* qr = reinterpret_cast<const uint4*>(q_rope + (t * H + i) * DR);
+    uint4 u[3];
+    u[0] = qa[lane];
+    u[1] = qa[lane + 32];
+    u[2] = lane < 8 ? qr[lane] : make_uint4(0u, 0u, 0u, 0u);
+    float amax = 0.f;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+    }
+    float s = __fdiv_rn(warp_max(amax), 127.f);
+    if (!(s > 0.f && s < INFINITY)) s = 0.f;
+    const float inv = s > 0.f ? 1.f / s : 0.f;
+    if (lane == 0) sq[i] = s;
+    // a scale so small that its reciprocal overflows is divided by
+    const bool div = !(inv < INFINITY);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      if (k == 2 && lane >= 8) break;
+      const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+      uint32_t packed[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t x = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t pair = w[2 * q + (e >> 1)];
+          const float f = e & 1 ? bf16_hi(pair) : bf16_lo(pair);
+          const int code = s == 0.f ? 0 : div ? code_fast(__fdiv_rn(f, s), 1.f, 1.f) : code_fast(f, s, inv);
+          x |= (uint32_t)(code & 255) << (8 * e);
+        }
+        packed[q] = x;
+      }
+      const int c = lane + 32 * k;                            // 8-code chunk 0 .. 71
+      const uint32_t dst = OFF_Q + (c >> 4) * KBOX + i * 128 + ((((c & 15) >> 1) ^ (i & 7)) << 4) + (c & 1) * 8;
+      *reinterpret_cast<uint2*>(smem + dst) = make_uint2(packed[0], packed[1]);
+    }
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<const uint32_t*>(smem + OFF_BAR + 16);
+  const int quarter = warp & 3, cg = warp >> 2;               // lanes 32 quarter .., heads 32 cg ..
+  constexpr uint32_t idesc = idesc_i8(TILE, H);
+  bool ok = true;
+  for (int i = 0; i <= n; ++i) {
+    if (i < n) {
+      // every copy of tile i has landed (the only group in flight) and is visible to the MMAs
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncthreads();
+      if (tid == 0) {
+        tc_fence_after();
+        const int b = i & 1;
+        const uint32_t d = tmem + 128 * b;
+#pragma unroll
+        for (int k = 0; k < 18; ++k) {
+          const uint32_t ya = k < 16 ? OFF_Y + (4 * b + (k >> 2)) * KBOX : OFF_YH;
+          const int ko = k < 16 ? 2 * (k & 3) : 4 * b + 2 * (k - 16);
+          mma_i8(d, sw128_desc(sbase + ya, 0, 1024) + ko, sw128_desc(sbase + OFF_Q + (k >> 2) * KBOX, 0, 1024) + 2 * (k & 3),
+                 idesc, k > 0 ? 1u : 0u);
+        }
+        mma_commit(bar(b));
+      }
+    }
+    float scale = 0.f;
+    const int row = 32 * quarter + lane;
+    if (i > 0) {
+      const int b = (i - 1) & 1;
+      if (cg == 0) scale = *reinterpret_cast<const float*>(smem + row_chunk(row, 4) + 4 * b);
+      // tile i - 1 multiplied: its buffer takes tile i + 1
+      ok = __syncthreads_and(mbar_wait(bar(b), ((i - 1) >> 1) & 1));
+      if (!ok) break;
+      tc_fence_after();
+    }
+    if (i + 1 < n) {
+      fetch(i + 1, page_next);
+      page_next = page_of(i + 2);
+    }
+    if (i > 0) {
+      const int b = (i - 1) & 1;
+      const int g = (first + (i - 1) * stride) * TILE + row;
+      uint32_t d[32];
+      tmem_ld32(tmem + ((uint32_t)(32 * quarter) << 16) + 128 * b + 32 * cg, d);
+      tmem_wait_ld();
+      float mx = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 32; c += 4) {
+        const float4 s4 = *reinterpret_cast<const float4*>(sq + 32 * cg + c);
+        mx = fmaxf(mx, fmaxf(fmaxf((float)(int)d[c] * s4.x, (float)(int)d[c + 1] * s4.y),
+                             fmaxf((float)(int)d[c + 2] * s4.z, (float)(int)d[c + 3] * s4.w)));
+      }
+      float* part = reinterpret_cast<float*>(smem + row_chunk(row, 5));
+      if (cg > 0) part[cg - 1] = mx;
+      tc_fence_before();
+      __syncthreads();
+      if (cg == 0 && g < nb) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) mx = fmaxf(mx, part[k]);
+        scores[t * v.max_pages + g] = mx * scale + 0.f;       // + 0: a -0 ties with a 0
+      }
+    }
+  }
+  if (!ok) {
+    if (tid == 0) flag_error(err, DEVERR_TIMEOUT);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  }
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
+}  // namespace
+
+cudaError_t tc_select_scores(const PagedView& v, const void* q_abs, const void* q_rope, const void* summaries,
+                             int32_t top_k, float* scores, int num_sms, uint32_t* err, cudaStream_t st) {
+  // per device, so set at every call
+  cudaError_t e = cudaFuncSetAttribute(select_score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  // enough CTAs a token to fill the SMs (one CTA each), no more than it can have tiles
+  const int64_t tiles = (v.max_pages + TILE - 1) / TILE;
+  int64_t split = num_sms / v.total_q;
+  split = split < 1 ? 1 : split > tiles ? tiles : split;
+  select_score_kernel<<<dim3((unsigned)split, (unsigned)v.total_q), kThreads, SMEM_BYTES, st>>>(
+      v, (const __nv_bfloat16*)q_abs, (const __nv_bfloat16*)q_rope, (const uint8_t*)summaries,
+      (int64_t)summary_pitch(DC, DR), top_k, scores, err);
+  note_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace mla
