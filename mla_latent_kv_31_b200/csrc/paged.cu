@@ -243,8 +243,8 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 }
 
 // The chosen blocks of one token: the threshold bit by bit (the largest key that at least `want` keys reach; a
-// count over the keys for each bit below the first in which they differ), then an ordered write. Counting costs
-// about 100 cycles a bit; a histogram's atomics serialise, since the keys share their leading bits.
+// count over the keys for each bit below the first in which they differ, until exactly `want` are above), then
+// an ordered write. (A histogram's atomics would serialise: the keys share their leading bits.)
 // Up to kSelectKeys keys are kept in shared memory, more are read from L2 at every pass.
 constexpr int kSelectThreads = 512, kSelectKeys = 8192;
 __global__ void __launch_bounds__(kSelectThreads)
@@ -285,10 +285,8 @@ __global__ void __launch_bounds__(kSelectThreads)
     red[1][warp] = mx;
   }
   __syncthreads();
-  for (int w = 0; w < NW; ++w) {
-    mn = min(mn, red[0][w]);
-    mx = max(mx, red[1][w]);
-  }
+  mn = __reduce_min_sync(0xffffffffu, red[0][lane & (NW - 1)]);
+  mx = __reduce_max_sync(0xffffffffu, red[1][lane & (NW - 1)]);
   // keys agree above bit `top`
   const int top = mn == mx ? -1 : 31 - __clz(mn ^ mx);
   uint32_t thr = top < 0 ? mx : top == 31 ? 0u : mx & ~((2u << top) - 1u);
@@ -299,14 +297,22 @@ __global__ void __launch_bounds__(kSelectThreads)
     c = __reduce_add_sync(0xffffffffu, c);
     if (lane == 0) wsum[warp][par] = c;
     __syncthreads();
-    int all = 0;
-    for (int w = 0; w < NW; ++w) all += wsum[w][par];
+    const int all = __reduce_add_sync(0xffffffffu, lane < NW ? wsum[lane][par] : 0);
     par ^= 1;                                          // the next count writes the other column
     return all;
   };
-  for (int bit = top; bit >= 0; --bit)
-    if (count(thr | (1u << bit)) >= want) thr |= 1u << bit;
-  const int left = want - (thr == 0xffffffffu ? 0 : count(thr + 1));     // of the keys equal to thr, the first `left`
+  int left = -1;                                       // of the keys equal to thr, the first `left` are taken
+  for (int bit = top; bit >= 0; --bit) {
+    const uint32_t cand = thr | (1u << bit);
+    const int c = count(cand);
+    if (c == want) {                                   // exactly the keys above cand - 1
+      thr = cand - 1;
+      left = 0;
+      break;
+    }
+    if (c > want) thr = cand;
+  }
+  if (left < 0) left = want - (thr == 0xffffffffu ? 0 : count(thr + 1));
   __syncthreads();
   int done = n_first, eq_done = 0;
   for (int g0 = lo; g0 < hi; g0 += kSelectThreads) {

@@ -55,13 +55,37 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool zero)
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(zero ? 0 : 16) : "memory");
 }
 
-// x / s to the nearest whole number (ties to even) as an IEEE division gives it, without dividing: x * (1 / s) is
-// within 2e-5 of it for |x / s| <= 127, so only values that near to a tie take the division.
-__device__ __forceinline__ int code_fast(float x, float s, float inv) {
-  const float r = x * inv;
-  float n = rintf(r);
-  if (fabsf(fabsf(r - n) - 0.5f) < 1e-4f) n = rintf(__fdiv_rn(x, s));
-  return x == x ? (int)fminf(fmaxf(n, -127.f), 127.f) : 0;
+// The codes of 8 elements by IEEE division (rare: see codes8).
+__device__ __noinline__ uint2 codes8_exact(uint4 u, float s) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  uint32_t out[2] = {0u, 0u};
+#pragma unroll 1
+  for (int e = 0; e < 8; ++e) {
+    const float f = e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
+    const float n = rintf(__fdiv_rn(f, s));
+    const int code = n == n ? (int)fminf(fmaxf(n, -127.f), 127.f) : 0;
+    out[e >> 2] |= (uint32_t)(code & 255) << (8 * (e & 3));
+  }
+  return make_uint2(out[0], out[1]);
+}
+// x / s to the nearest whole number (ties to even) for 8 elements, as an IEEE division gives it, without dividing:
+// x * (1 / s) is within 3e-5 of the quotient for |x / s| <= 127, so only a value that near to a tie, a NaN or a
+// scale whose reciprocal overflows takes the divisions. Adding 1.5 * 2^23 rounds to the nearest even whole
+// number and leaves it, as two's complement, in the low byte.
+__device__ __forceinline__ uint2 codes8(uint4 u, float s, float inv) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  uint32_t t[8];
+  bool rare = !(inv < INFINITY);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float r = (e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1])) * inv;
+    const float m = r + 12582912.f;
+    t[e] = __float_as_uint(m);
+    rare |= !(fabsf(r - (m - 12582912.f)) <= 0.4999f);
+  }
+  if (rare) return codes8_exact(u, s);
+  return make_uint2(__byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410));
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -124,49 +148,43 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   fetch(0, page);
   int page_next = page_of(1);
-  // ---- the queries' codes, a warp a row: lane takes chunks of 8 elements lane, lane + 32 and (lanes 0-7) 64 + lane
+  // ---- the queries' codes, a warp a row, four rows in flight: lane takes the chunks of 8 elements lane, lane + 32 and
+  // (lanes 0-7) 64 + lane
   float* sq = reinterpret_cast<float*>(smem + OFF_SQ);
-#pragma unroll 2
-  for (int i = warp; i < H; i += kThreads / 32) {
-    const uint4* qa = reinterpret_cast<const uint4*>(q_abs + (t * H + i) * DC);
-    const uint4* qr = reinterpret_cast<const uint4*>(q_rope + (t * H + i) * DR);
-    uint4 u[3];
-    u[0] = qa[lane];
-    u[1] = qa[lane + 32];
-    u[2] = lane < 8 ? qr[lane] : make_uint4(0u, 0u, 0u, 0u);
-    float amax = 0.f;
+  constexpr int ROWS = 4;
+#pragma unroll 1
+  for (int i0 = ROWS * warp; i0 < H; i0 += ROWS * (kThreads / 32)) {
+    uint4 u[ROWS][3];
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+    for (int j = 0; j < ROWS; ++j) {
+      const uint4* qa = reinterpret_cast<const uint4*>(q_abs + (t * H + i0 + j) * DC);
+      const uint4* qr = reinterpret_cast<const uint4*>(q_rope + (t * H + i0 + j) * DR);
+      u[j][0] = qa[lane];
+      u[j][1] = qa[lane + 32];
+      u[j][2] = lane < 8 ? qr[lane] : make_uint4(0u, 0u, 0u, 0u);
     }
-    float s = __fdiv_rn(warp_max(amax), 127.f);
-    if (!(s > 0.f && s < INFINITY)) s = 0.f;
-    const float inv = s > 0.f ? 1.f / s : 0.f;
-    if (lane == 0) sq[i] = s;
-    // a scale so small that its reciprocal overflows is divided by
-    const bool div = !(inv < INFINITY);
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      if (k == 2 && lane >= 8) break;
-      const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
-      uint32_t packed[2];
+    for (int j = 0; j < ROWS; ++j) {
+      const int i = i0 + j;
+      float amax = 0.f;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t x = 0;
+      for (int k = 0; k < 3; ++k) {
+        const uint32_t w[4] = {u[j][k].x, u[j][k].y, u[j][k].z, u[j][k].w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t pair = w[2 * q + (e >> 1)];
-          const float f = e & 1 ? bf16_hi(pair) : bf16_lo(pair);
-          const int code = s == 0.f ? 0 : div ? code_fast(__fdiv_rn(f, s), 1.f, 1.f) : code_fast(f, s, inv);
-          x |= (uint32_t)(code & 255) << (8 * e);
-        }
-        packed[q] = x;
+        for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
       }
-      const int c = lane + 32 * k;                            // 8-code chunk 0 .. 71
-      const uint32_t dst = OFF_Q + (c >> 4) * KBOX + i * 128 + ((((c & 15) >> 1) ^ (i & 7)) << 4) + (c & 1) * 8;
-      *reinterpret_cast<uint2*>(smem + dst) = make_uint2(packed[0], packed[1]);
+      float s = __fdiv_rn(warp_max(amax), 127.f);
+      if (!(s > 0.f && s < INFINITY)) s = 0.f;
+      const float inv = 1.f / s;
+      if (lane == 0) sq[i] = s;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        if (k == 2 && lane >= 8) continue;
+        const uint2 codes = s == 0.f ? make_uint2(0u, 0u) : codes8(u[j][k], s, inv);
+        const int c = lane + 32 * k;                          // 8-code chunk 0 .. 71
+        const uint32_t dst = OFF_Q + (c >> 4) * KBOX + i * 128 + ((((c & 15) >> 1) ^ (i & 7)) << 4) + (c & 1) * 8;
+        *reinterpret_cast<uint2*>(smem + dst) = codes;
+      }
     }
   }
   fence_proxy_async_smem();
