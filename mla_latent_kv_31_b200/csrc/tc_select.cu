@@ -75,17 +75,35 @@ __device__ __noinline__ uint2 codes8_exact(uint4 u, float s) {
 __device__ __forceinline__ uint2 codes8(uint4 u, float s, float inv) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
   uint32_t t[8];
+  const uint64_t inv2 = f2_pack(inv, inv), magic = f2_pack(12582912.f, 12582912.f), unmagic = f2_pack(-12582912.f, -12582912.f);
+  const uint64_t minus = f2_pack(-1.f, -1.f);
   bool rare = !(inv < INFINITY);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float r = (e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1])) * inv;
-    const float m = r + 12582912.f;
-    t[e] = __float_as_uint(m);
-    rare |= !(fabsf(r - (m - 12582912.f)) <= 0.4999f);
+  for (int e = 0; e < 4; ++e) {
+    const uint64_t r = f2_mul(f2_pack(bf16_lo(w[e]), bf16_hi(w[e])), inv2);
+    const uint64_t m = f2_add(r, magic);
+    float m0, m1, d0, d1;
+    f2_unpack(m, m0, m1);
+    f2_unpack(f2_fma(f2_add(m, unmagic), minus, r), d0, d1);
+    t[2 * e] = __float_as_uint(m0);
+    t[2 * e + 1] = __float_as_uint(m1);
+    rare |= !(fabsf(d0) <= 0.4999f) || !(fabsf(d1) <= 0.4999f);
   }
   if (rare) return codes8_exact(u, s);
   return make_uint2(__byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410),
                     __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410));
+}
+// The largest magnitudes of the 8 elements, two at a time in bf16 (NaN is passed over).
+__device__ __forceinline__ __nv_bfloat162 max8(uint4 u) {
+  auto mag = [](uint32_t w) {
+    w &= 0x7fff7fffu;
+    return *reinterpret_cast<__nv_bfloat162*>(&w);
+  };
+  return __hmax2(__hmax2(mag(u.x), mag(u.y)), __hmax2(mag(u.z), mag(u.w)));
+}
+// ... as the bits of one fp32 value, which order like it; a NaN is 0.
+__device__ __forceinline__ uint32_t max_bits(__nv_bfloat162 m) {
+  return __float_as_uint(fmaxf(fmaxf(__low2float(m), __high2float(m)), 0.f));
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -96,6 +114,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sbase = smem_addr(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t t = blockIdx.y;
+  // A warp quantises 8 query rows: all of their loads are in flight while the token is looked up. Lane: the chunks of 8
+  // elements lane and lane + 32 of each row, and q^R's chunk lane % 8 of rows lane / 8 and 4 + lane / 8.
+  constexpr int ROWS = H / (kThreads / 32);
+  const int i0 = ROWS * warp;
+  uint4 u[ROWS][2], ur[2];
+  {
+    const uint4* qa = reinterpret_cast<const uint4*>(q_abs + (t * H + i0) * DC) + lane;
+    const uint4* qr = reinterpret_cast<const uint4*>(q_rope + (t * H + i0) * DR) + lane;
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      u[j][0] = qa[j * (DC / 8)];
+      u[j][1] = qa[j * (DC / 8) + 32];
+    }
+    ur[0] = qr[0];
+    ur[1] = qr[32];
+  }
   if (blockIdx.x == 0 && t == 0) paged_check(v, err);
   const PagedToken tok = paged_token(v, t);
   if (tok.pos < 0) return;
@@ -148,44 +182,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   fetch(0, page);
   int page_next = page_of(1);
-  // ---- the queries' codes, a warp a row, four rows in flight: lane takes the chunks of 8 elements lane, lane + 32 and
-  // (lanes 0-7) 64 + lane
+  // ---- the queries' codes
   float* sq = reinterpret_cast<float*>(smem + OFF_SQ);
-  constexpr int ROWS = 4;
-#pragma unroll 1
-  for (int i0 = ROWS * warp; i0 < H; i0 += ROWS * (kThreads / 32)) {
-    uint4 u[ROWS][3];
+  auto put = [&](int i, int c, uint2 codes) {                 // 8-code chunk c (0 .. 71) of row i
+    const uint32_t dst = OFF_Q + (c >> 4) * KBOX + i * 128 + ((((c & 15) >> 1) ^ (i & 7)) << 4) + (c & 1) * 8;
+    *reinterpret_cast<uint2*>(smem + dst) = codes;
+  };
+  float srow[2] = {0.f, 0.f};                                 // scales of the rows of ur
 #pragma unroll
-    for (int j = 0; j < ROWS; ++j) {
-      const uint4* qa = reinterpret_cast<const uint4*>(q_abs + (t * H + i0 + j) * DC);
-      const uint4* qr = reinterpret_cast<const uint4*>(q_rope + (t * H + i0 + j) * DR);
-      u[j][0] = qa[lane];
-      u[j][1] = qa[lane + 32];
-      u[j][2] = lane < 8 ? qr[lane] : make_uint4(0u, 0u, 0u, 0u);
-    }
+  for (int h = 0; h < 2; ++h) {
+    uint32_t mr = max_bits(max8(ur[h]));
 #pragma unroll
-    for (int j = 0; j < ROWS; ++j) {
-      const int i = i0 + j;
-      float amax = 0.f;
+    for (int o = 1; o < 8; o <<= 1) mr = max(mr, __shfl_xor_sync(0xffffffffu, mr, o));
 #pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        const uint32_t w[4] = {u[j][k].x, u[j][k].y, u[j][k].z, u[j][k].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
-      }
-      float s = __fdiv_rn(warp_max(amax), 127.f);
+    for (int k = 0; k < 4; ++k) {
+      const int j = 4 * h + k;
+      const uint32_t own = max(max_bits(max8(u[j][0])), max_bits(max8(u[j][1])));
+      const float amax = __uint_as_float(max(__reduce_max_sync(0xffffffffu, own), __shfl_sync(0xffffffffu, mr, 8 * k)));
+      float s = __fdiv_rn(amax, 127.f);
       if (!(s > 0.f && s < INFINITY)) s = 0.f;
       const float inv = 1.f / s;
-      if (lane == 0) sq[i] = s;
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        if (k == 2 && lane >= 8) continue;
-        const uint2 codes = s == 0.f ? make_uint2(0u, 0u) : codes8(u[j][k], s, inv);
-        const int c = lane + 32 * k;                          // 8-code chunk 0 .. 71
-        const uint32_t dst = OFF_Q + (c >> 4) * KBOX + i * 128 + ((((c & 15) >> 1) ^ (i & 7)) << 4) + (c & 1) * 8;
-        *reinterpret_cast<uint2*>(smem + dst) = codes;
-      }
+      put(i0 + j, lane, s == 0.f ? make_uint2(0u, 0u) : codes8(u[j][0], s, inv));
+      put(i0 + j, lane + 32, s == 0.f ? make_uint2(0u, 0u) : codes8(u[j][1], s, inv));
+      if (lane == 0) sq[i0 + j] = s;
+      if ((lane >> 3) == k) srow[h] = s;
     }
+    put(i0 + 4 * h + (lane >> 3), 64 + (lane & 7), srow[h] == 0.f ? make_uint2(0u, 0u) : codes8(ur[h], srow[h], 1.f / srow[h]));
   }
   fence_proxy_async_smem();
   tc_fence_before();
