@@ -55,29 +55,31 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool zero)
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(zero ? 0 : 16) : "memory");
 }
 
-// The codes of 8 elements by IEEE division (rare: see codes8).
-__device__ __noinline__ uint2 codes8_exact(uint4 u, float s) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  uint32_t out[2] = {0u, 0u};
-#pragma unroll 1
-  for (int e = 0; e < 8; ++e) {
-    const float f = e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
-    const float n = rintf(__fdiv_rn(f, s));
-    const int code = n == n ? (int)fminf(fmaxf(n, -127.f), 127.f) : 0;
-    out[e >> 2] |= (uint32_t)(code & 255) << (8 * (e & 3));
+// The elements of `near` (a bit each) of 8 again, by IEEE division.
+__device__ __noinline__ uint2 codes8_exact(uint4 u, float s, uint32_t near, uint2 codes) {
+  while (near) {
+    const int e = __ffs(near) - 1;
+    near &= near - 1;
+    const uint32_t w = (e >> 1) == 0 ? u.x : (e >> 1) == 1 ? u.y : (e >> 1) == 2 ? u.z : u.w;
+    const float n = rintf(__fdiv_rn(e & 1 ? bf16_hi(w) : bf16_lo(w), s));
+    const uint32_t code = n == n ? (uint32_t)(int)fminf(fmaxf(n, -127.f), 127.f) & 255u : 0u;
+    const int sh = 8 * (e & 3);
+    if (e < 4) codes.x = (codes.x & ~(255u << sh)) | (code << sh);
+    else codes.y = (codes.y & ~(255u << sh)) | (code << sh);
   }
-  return make_uint2(out[0], out[1]);
+  return codes;
 }
-// x / s to the nearest whole number (ties to even) for 8 elements, as an IEEE division gives it, without dividing:
-// x * (1 / s) is within 3e-5 of the quotient for |x / s| <= 127, so only a value that near to a tie, a NaN or a
-// scale whose reciprocal overflows takes the divisions. Adding 1.5 * 2^23 rounds to the nearest even whole
-// number and leaves it, as two's complement, in the low byte.
+// x / s to the nearest whole number (ties to even) for 8 elements, as an IEEE division gives it: x * (1 / s) is within
+// 3e-5 of the quotient for |x / s| <= 127, so only a value that near to a tie, a NaN or a scale whose reciprocal
+// overflows is divided. (Half of the row's largest magnitude, 63.5, is such a value, and about every second row of
+// bf16 numbers has one.) Adding 1.5 * 2^23 rounds to the nearest even whole number and leaves it, as two's
+// complement, in the low byte.
 __device__ __forceinline__ uint2 codes8(uint4 u, float s, float inv) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
   uint32_t t[8];
   const uint64_t inv2 = f2_pack(inv, inv), magic = f2_pack(12582912.f, 12582912.f), unmagic = f2_pack(-12582912.f, -12582912.f);
   const uint64_t minus = f2_pack(-1.f, -1.f);
-  bool rare = !(inv < INFINITY);
+  uint32_t near = inv < INFINITY ? 0u : 255u;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const uint64_t r = f2_mul(f2_pack(bf16_lo(w[e]), bf16_hi(w[e])), inv2);
@@ -87,11 +89,12 @@ __device__ __forceinline__ uint2 codes8(uint4 u, float s, float inv) {
     f2_unpack(f2_fma(f2_add(m, unmagic), minus, r), d0, d1);
     t[2 * e] = __float_as_uint(m0);
     t[2 * e + 1] = __float_as_uint(m1);
-    rare |= !(fabsf(d0) <= 0.4999f) || !(fabsf(d1) <= 0.4999f);
+    if (!(fabsf(d0) <= 0.4999f)) near |= 1u << (2 * e);
+    if (!(fabsf(d1) <= 0.4999f)) near |= 2u << (2 * e);
   }
-  if (rare) return codes8_exact(u, s);
-  return make_uint2(__byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410),
-                    __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410));
+  const uint2 codes = make_uint2(__byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410),
+                                 __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410));
+  return near ? codes8_exact(u, s, near, codes) : codes;
 }
 // The largest magnitudes of the 8 elements, two at a time in bf16 (NaN is passed over).
 __device__ __forceinline__ __nv_bfloat162 max8(uint4 u) {
