@@ -20,13 +20,93 @@ __device__ __forceinline__ void rope_angle(const RopeTable& rt, const LayerOpts&
 }
 
 // ---- append -----------------------------------------------------------------------------------------------
-// One block per new token: its row [c | R_pos k] into its page and, with q, its n_h rotated queries.
-template <typename T>
+// One block per new token: its row [c | R_pos k] into its page and, with q, its n_h rotated queries. The bytes bound it
+// for long chunks (a token's 2 x 1152 + 2 x 16384 at the DeepSeek-V3 sizes), the chain lookup - sine - store else,
+// so every load is issued before the lookup and the angles (in double) are taken by one warp.
+__device__ __forceinline__ uint4 rotate8(uint4 u, const float2* cs, float mul) {       // 4 pairs of bf16
+  uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float x0 = __uint_as_float(w[e] << 16), x1 = __uint_as_float(w[e] & 0xffff0000u);
+    const __nv_bfloat162 y = __floats2bfloat162_rn((x0 * cs[e].x - x1 * cs[e].y) * mul, (x0 * cs[e].y + x1 * cs[e].x) * mul);
+    w[e] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+constexpr int AP_THREADS = 256;
+constexpr int AP_H = 128, AP_DC = 512, AP_DR = 64;
+__global__ void __launch_bounds__(AP_THREADS)
+    append_bf16_kernel(PagedView v, const __nv_bfloat16* kv, int64_t kv_stride, const __nv_bfloat16* q,
+                       __nv_bfloat16* q_out, LayerOpts o, RopeTable rt, uint32_t* err) {
+  __shared__ float2 cs[AP_DR / 2];
+  __shared__ float red[32];
+  constexpr int QC = AP_H * AP_DR / 8 / AP_THREADS;          // 16-byte chunks of the queries per thread
+  let_next_start();
+  const int tid = threadIdx.x;
+  const int64_t t = blockIdx.x;
+  uint4 uq[QC], uk = make_uint4(0u, 0u, 0u, 0u);
+  const uint4* qs = reinterpret_cast<const uint4*>(q + t * AP_H * AP_DR);
+  if (q) {
+#pragma unroll
+    for (int k = 0; k < QC; ++k) uq[k] = qs[tid + k * AP_THREADS];
+  }
+  const bool has_row = tid < (AP_DC + AP_DR) / 8;
+  if (has_row) uk = reinterpret_cast<const uint4*>(kv + t * kv_stride)[tid];
+  if (t == 0) paged_check(v, err);
+  const PagedToken tok = paged_token(v, t);
+  if (tok.pos < 0) return;
+  const int64_t page = paged_page(v, tok.seq, tok.pos / v.page, err);
+  if (tid < AP_DR / 2) rope_angle(rt, o, tok.pos, tid, AP_DR, &cs[tid].x, &cs[tid].y);
+  float inv = 1.f;
+  if (o.g_kv) {
+    float ss = 0.f;
+    if (tid < AP_DC / 8) {
+      const uint32_t w[4] = {uk.x, uk.y, uk.z, uk.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x0 = __uint_as_float(w[e] << 16), x1 = __uint_as_float(w[e] & 0xffff0000u);
+        ss = fmaf(x0, x0, fmaf(x1, x1, ss));
+      }
+    }
+    inv = 1.f / sqrtf(block_sum(ss, red) / (float)AP_DC + o.eps);
+  }
+  __syncthreads();
+  if (has_row && page >= 0) {
+    uint4* row = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(v.cache) +
+                                          (page * v.page + tok.pos % v.page) * (AP_DC + AP_DR));
+    if (tid >= AP_DC / 8) {
+      uk = rotate8(uk, cs + 4 * (tid - AP_DC / 8), rt.mul);
+    } else if (o.g_kv) {
+      const uint4 g = reinterpret_cast<const uint4*>(o.g_kv)[tid];
+      uint32_t w[4] = {uk.x, uk.y, uk.z, uk.w};
+      const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 y = __floats2bfloat162_rn(
+            __uint_as_float(w[e] << 16) * inv * __uint_as_float(gw[e] << 16),
+            __uint_as_float(w[e] & 0xffff0000u) * inv * __uint_as_float(gw[e] & 0xffff0000u));
+        w[e] = *reinterpret_cast<const uint32_t*>(&y);
+      }
+      uk = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    row[tid] = uk;
+  }
+  if (q) {
+    uint4* qd = reinterpret_cast<uint4*>(q_out + t * AP_H * AP_DR);
+    const float2* c = cs + 4 * (tid & 7);                    // AP_THREADS is a multiple of a head's 8 chunks
+#pragma unroll
+    for (int k = 0; k < QC; ++k) qd[tid + k * AP_THREADS] = rotate8(uq[k], c, rt.mul);
+  }
+}
+
+// The fp32 configuration, any sizes.
 __global__ void __launch_bounds__(128)
-    append_kernel(PagedView v, const T* kv, int64_t kv_stride, const T* q, T* q_out, LayerOpts o, RopeTable rt,
-                  uint32_t* err) {
+    append_kernel(PagedView v, const float* kv, int64_t kv_stride, const float* q, float* q_out, LayerOpts o,
+                  RopeTable rt, uint32_t* err) {
   extern __shared__ float2 cs[];      // [d_r / 2] cos, sin
   __shared__ float red[32];
+  let_next_start();
   const int tid = threadIdx.x;
   const int64_t t = blockIdx.x;
   if (t == 0) paged_check(v, err);
@@ -35,30 +115,30 @@ __global__ void __launch_bounds__(128)
   const int64_t page = paged_page(v, tok.seq, tok.pos / v.page, err);
   for (int m = tid; m < v.d_r / 2; m += blockDim.x) rope_angle(rt, o, tok.pos, m, v.d_r, &cs[m].x, &cs[m].y);
   __syncthreads();
-  const T* src = kv + t * kv_stride;
+  const float* src = kv + t * kv_stride;
   if (page >= 0) {
-    T* row = reinterpret_cast<T*>(v.cache) + (page * v.page + tok.pos % v.page) * (v.d_c + v.d_r);
+    float* row = reinterpret_cast<float*>(v.cache) + (page * v.page + tok.pos % v.page) * (v.d_c + v.d_r);
     float inv = 1.f;
     if (o.g_kv) {
       float ss = 0.f;
-      for (int c = tid; c < v.d_c; c += blockDim.x) ss = fmaf(to_f(src[c]), to_f(src[c]), ss);
+      for (int c = tid; c < v.d_c; c += blockDim.x) ss = fmaf(src[c], src[c], ss);
       inv = 1.f / sqrtf(block_sum(ss, red) / (float)v.d_c + o.eps);
     }
     for (int c = tid; c < v.d_c; c += blockDim.x)
-      row[c] = o.g_kv ? from_f<T>(to_f(src[c]) * inv * to_f(reinterpret_cast<const T*>(o.g_kv)[c])) : src[c];
+      row[c] = o.g_kv ? src[c] * inv * reinterpret_cast<const float*>(o.g_kv)[c] : src[c];
     for (int m = tid; m < v.d_r / 2; m += blockDim.x) {
-      const float x0 = to_f(src[v.d_c + 2 * m]), x1 = to_f(src[v.d_c + 2 * m + 1]);
-      row[v.d_c + 2 * m] = from_f<T>((x0 * cs[m].x - x1 * cs[m].y) * rt.mul);
-      row[v.d_c + 2 * m + 1] = from_f<T>((x0 * cs[m].y + x1 * cs[m].x) * rt.mul);
+      const float x0 = src[v.d_c + 2 * m], x1 = src[v.d_c + 2 * m + 1];
+      row[v.d_c + 2 * m] = (x0 * cs[m].x - x1 * cs[m].y) * rt.mul;
+      row[v.d_c + 2 * m + 1] = (x0 * cs[m].y + x1 * cs[m].x) * rt.mul;
     }
   }
   if (!q) return;
   const int64_t base = t * v.n_h * v.d_r;
   for (int i = tid; i < v.n_h * (v.d_r / 2); i += blockDim.x) {
     const float2 w = cs[i % (v.d_r / 2)];
-    const float x0 = to_f(q[base + 2 * i]), x1 = to_f(q[base + 2 * i + 1]);
-    q_out[base + 2 * i] = from_f<T>((x0 * w.x - x1 * w.y) * rt.mul);
-    q_out[base + 2 * i + 1] = from_f<T>((x0 * w.y + x1 * w.x) * rt.mul);
+    const float x0 = q[base + 2 * i], x1 = q[base + 2 * i + 1];
+    q_out[base + 2 * i] = (x0 * w.x - x1 * w.y) * rt.mul;
+    q_out[base + 2 * i + 1] = (x0 * w.y + x1 * w.x) * rt.mul;
   }
 }
 
@@ -74,54 +154,97 @@ __device__ __forceinline__ int code_of(float x, float s) {
   return r >= 127.f ? 127 : r <= -127.f ? -127 : (int)r;
 }
 
-// Summaries of the pages that the new tokens complete. Block i looks at `group` tokens; a token that is its
-// page's last row stands for the page.
+// Summaries of the pages that the new tokens complete. Block i looks at `group` tokens; a token that is its page's last
+// row stands for the page. The lookups come before the wait for the append's rows. Four groups of threads take a
+// quarter of the rows each (page sizes are multiples of 16), 16 of them in flight; their sums meet in shared memory.
+// The sums are in double: of bf16 values they are exact, so the summary does not depend on the order.
+constexpr int SUM_GROUPS = 4;
 template <typename T>
-__global__ void __launch_bounds__(256)
-    summarise_kernel(PagedView v, int group, uint8_t* summaries, int64_t pitch) {
-  extern __shared__ float mean[];     // [W]
+__global__ void __launch_bounds__(512) summarise_kernel(PagedView v, int group, uint8_t* summaries, int64_t pitch) {
+  extern __shared__ double part[];    // [SUM_GROUPS][W]
   __shared__ float red[32];
   const int tid = threadIdx.x, W = v.d_c + v.d_r;
+  bool waited = false;
   for (int k = 0; k < group; ++k) {
     const int64_t t = (int64_t)blockIdx.x * group + k;
-    if (t >= v.total_q) return;
+    if (t >= v.total_q) break;
     const PagedToken tok = paged_token(v, t);
-    if (tok.seq < 0) return;
+    if (tok.seq < 0) break;
     if (tok.pos < 0 || tok.pos % v.page != v.page - 1) continue;
     const int32_t p = v.table[(int64_t)tok.seq * v.stride + tok.pos / v.page];
     if (p < 0 || p >= v.num_pages) continue;      // flagged by the append
+    if (!waited) wait_for_previous();
+    waited = true;
     const T* rows = reinterpret_cast<const T*>(v.cache) + (int64_t)p * v.page * W;
+    constexpr int E = sizeof(T) == 2 ? 8 : 1;     // columns per thread: 16 bytes of bf16 (W is a multiple of 8 there)
+    const int cols = W / E, per = v.page / SUM_GROUPS;
+    for (int i = tid; i < cols * SUM_GROUPS; i += blockDim.x) {
+      const int g = i / cols, c = i % cols;
+      const T* src = rows + (int64_t)g * per * W + c * E;
+      double sum[E] = {};
+      if constexpr (E == 8) {
+        for (int r0 = 0; r0 < per; r0 += 16) {
+          uint4 u[16];
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (r0 + r < per) u[r] = *reinterpret_cast<const uint4*>(src + (int64_t)(r0 + r) * W);
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (r0 + r < per) {
+              const uint32_t w[4] = {u[r].x, u[r].y, u[r].z, u[r].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                sum[2 * e] += (double)__uint_as_float(w[e] << 16);
+                sum[2 * e + 1] += (double)__uint_as_float(w[e] & 0xffff0000u);
+              }
+            }
+        }
+      } else {
+#pragma unroll 8
+        for (int r = 0; r < per; ++r) sum[0] += (double)to_f(src[(int64_t)r * W]);
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) part[g * W + c * E + e] = sum[e];
+    }
+    __syncthreads();
     float amax = 0.f;
     for (int c = tid; c < W; c += blockDim.x) {
-      double sum = 0.0;               // of 8-bit mantissas: exact in double, whatever the order
-      for (int r = 0; r < v.page; ++r) sum += (double)to_f(rows[(int64_t)r * W + c]);
-      mean[c] = (float)(sum / v.page);
-      amax = fmaxf(amax, fabsf(mean[c]));
+      double sum = 0.0;
+#pragma unroll
+      for (int g = 0; g < SUM_GROUPS; ++g) sum += part[g * W + c];
+      const float mean = (float)(sum / v.page);
+      reinterpret_cast<float*>(part)[2 * c] = mean;          // in place of group 0's sum
+      amax = fmaxf(amax, fabsf(mean));
     }
     const float s = code_scale(block_max(amax, red));
     uint8_t* out = summaries + (int64_t)p * pitch;
     for (int c = tid; c < pitch; c += blockDim.x)
-      if (c < W) out[c] = (uint8_t)(int8_t)code_of(mean[c], s);
+      if (c < W) out[c] = (uint8_t)(int8_t)code_of(reinterpret_cast<float*>(part)[2 * c], s);
       else if (c >= W + 4) out[c] = 0;
     if (tid == 0) *reinterpret_cast<float*>(out + W) = s;
     __syncthreads();
   }
+  if (!waited) wait_for_previous();   // this kernel must not be complete before the append is
 }
 
 // ---- attention by CUDA cores --------------------------------------------------------------------------------
-constexpr int ATT = 128;
-constexpr int ATT_MAX_DV = 512;
-
+// The fp32 configuration (tcgen05 has no fp32 product): one block per (token, head). Rows come through shared memory,
+// `chunk` at a time (what fits 64 KB), so that global reads are contiguous; two threads share a key's product, and
+// the 256 threads split into groups of d_c threads that share the chunk's keys in P.V.
+constexpr int ATT = 256;
+constexpr int ATT_SMEM = 65536;
 __global__ void __launch_bounds__(ATT)
     paged_attention_kernel(PagedView v, const float* q_abs, const float* q_rope, const int32_t* blocks, int32_t top_k,
-                           float scale, float* o_lat, float* lse, uint32_t* err) {
+                           float scale, int32_t chunk, float* o_lat, float* lse, uint32_t* err) {
+  extern __shared__ float rows[];     // [chunk][W | 1]
   __shared__ float qs[1024];
-  __shared__ float ps[ATT];
-  __shared__ int64_t row_of[ATT];
+  __shared__ float ps[ATT / 2];
+  __shared__ int64_t row_of[ATT / 2];
+  __shared__ float acc_sh[ATT];
   __shared__ float red[32];
   __shared__ int list_scratch[2];
   const int64_t t = blockIdx.x;
-  const int head = blockIdx.y, tid = threadIdx.x, W = v.d_c + v.d_r;
+  const int head = blockIdx.y, tid = threadIdx.x, W = v.d_c + v.d_r, ld = W | 1;
   if (t == 0 && head == 0) paged_check(v, err);
   const PagedToken tok = paged_token(v, t);
   if (tok.seq < 0) return;
@@ -129,54 +252,71 @@ __global__ void __launch_bounds__(ATT)
   int64_t n = tok.pos + 1;
   if (list) n = tok.pos < 0 ? 0 : paged_list_rows(list, top_k, tok.pos, v.page, list_scratch, err);
   const int64_t oq = t * v.n_h + head;
-  for (int c = tid; c < W; c += ATT)
-    qs[c] = c < v.d_c ? q_abs[oq * v.d_c + c] : q_rope[oq * v.d_r + c - v.d_c];
-  __syncthreads();
-  const float* rows = reinterpret_cast<const float*>(v.cache);
-  float m = -INFINITY, l = 0.f;
-  float acc[ATT_MAX_DV / ATT] = {};
-  for (int64_t c0 = 0; c0 < n; c0 += ATT) {
-    const int64_t j = c0 + tid;
+  for (int c = tid; c < W; c += ATT) qs[c] = c < v.d_c ? q_abs[oq * v.d_c + c] : q_rope[oq * v.d_r + c - v.d_c];
+  const float* cache = reinterpret_cast<const float*>(v.cache);
+  // P.V: group kg of G takes the keys kg, kg + G, ...; with d_c > ATT a thread takes columns col, col + ATT
+  const int width = min(v.d_c, ATT), G = ATT / width, kg = tid / width, col = tid % width;
+  float m = -INFINITY, l = 0.f, acc[2] = {0.f, 0.f};
+  for (int64_t c0 = 0; c0 < n; c0 += chunk) {
+    const int cnt = (int)min((int64_t)chunk, n - c0);
+    for (int j = tid; j < cnt; j += ATT) {
+      const int64_t k = c0 + j;
+      const int64_t page = paged_page(v, tok.seq, list ? list[k / v.page] : k / v.page, err);
+      row_of[j] = page < 0 ? -1 : page * v.page + k % v.page;
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int i = tid; i < cnt * W; i += ATT) {
+      const int j = i / W, c = i - j * W;
+      const int64_t r = row_of[j];
+      rows[j * ld + c] = r < 0 ? 0.f : cache[r * W + c];       // a page outside the pool counts as rows of zeros
+    }
+    __syncthreads();
+    const int j = tid >> 1;
     float s = -INFINITY;
-    row_of[tid] = -1;
-    if (j < n) {
-      const int64_t g = list ? list[j / v.page] : j / v.page;
-      const int64_t page = paged_page(v, tok.seq, g, err);
-      float d = 0.f;                  // a page outside the pool counts as rows of zeros
-      if (page >= 0) {
-        row_of[tid] = page * v.page + j % v.page;
-        const float* k = rows + row_of[tid] * W;
-        for (int c = 0; c < W; ++c) d = fmaf(qs[c], k[c], d);
+    {
+      // two chains of sums per thread, then the neighbour's half
+      const int half = (W + 1) / 2, lo = (tid & 1) * half, hi = min(W, lo + half);
+      const float* k = rows + min(j, cnt - 1) * ld;
+      float d0 = 0.f, d1 = 0.f;
+      int c = lo;
+#pragma unroll 4
+      for (; c + 1 < hi; c += 2) {
+        d0 = fmaf(qs[c], k[c], d0);
+        d1 = fmaf(qs[c + 1], k[c + 1], d1);
       }
-      s = d * scale;
+      if (c < hi) d0 = fmaf(qs[c], k[c], d0);
+      d0 += d1;
+      d0 += __shfl_xor_sync(0xffffffffu, d0, 1);
+      if (j < cnt) s = d0 * scale;
     }
     const float m_new = fmaxf(m, block_max(s, red));
     const float alpha = m == -INFINITY ? 0.f : __expf(m - m_new);
-    const float p = j < n ? __expf(s - m_new) : 0.f;
-    ps[tid] = p;
-    l = l * alpha + block_sum(p, red);
-#pragma unroll
-    for (int i = 0; i < ATT_MAX_DV / ATT; ++i) acc[i] *= alpha;
+    const float p = j < cnt ? __expf(s - m_new) : 0.f;
+    if ((tid & 1) == 0 && j < cnt) ps[j] = p;
+    l = l * alpha + block_sum((tid & 1) == 0 ? p : 0.f, red);
+    acc[0] *= alpha;
+    acc[1] *= alpha;
     __syncthreads();
-    const int cnt = (int)min((int64_t)ATT, n - c0);
-    for (int jj = 0; jj < cnt; ++jj) {
-      if (row_of[jj] < 0) continue;
-      const float pj = ps[jj];
-      const float* vr = rows + row_of[jj] * W;
-#pragma unroll
-      for (int i = 0; i < ATT_MAX_DV / ATT; ++i) {
-        const int c = tid + i * ATT;
-        if (c < v.d_c) acc[i] = fmaf(pj, vr[c], acc[i]);
+    if (kg < G) {
+#pragma unroll 4
+      for (int jj = kg; jj < cnt; jj += G) {
+        const float pj = ps[jj];
+        acc[0] = fmaf(pj, rows[jj * ld + col], acc[0]);
+        if (col + ATT < v.d_c) acc[1] = fmaf(pj, rows[jj * ld + col + ATT], acc[1]);
       }
     }
     m = m_new;
     __syncthreads();
   }
   const float inv = n > 0 ? 1.f / l : 0.f;
-#pragma unroll
-  for (int i = 0; i < ATT_MAX_DV / ATT; ++i) {
-    const int c = tid + i * ATT;
-    if (c < v.d_c) o_lat[oq * v.d_c + c] = acc[i] * inv;
+  acc_sh[tid] = acc[0];
+  __syncthreads();
+  if (kg == 0) {
+    float sum = acc[0];
+    for (int g = 1; g < G; ++g) sum += acc_sh[g * width + col];
+    o_lat[oq * v.d_c + col] = sum * inv;
+    if (col + ATT < v.d_c) o_lat[oq * v.d_c + col + ATT] = acc[1] * inv;
   }
   if (tid == 0) lse[oq] = n > 0 ? m + logf(l) : -INFINITY;
 }
@@ -346,21 +486,6 @@ __global__ void __launch_bounds__(kSelectThreads)
 size_t align16(size_t x) { return (x + 15) / 16 * 16; }
 size_t align1k(size_t x) { return (x + 1023) / 1024 * 1024; }
 
-template <typename T>
-cudaError_t append_launch(const PagedView& v, const void* kv, int64_t kv_stride, const void* q, void* q_out,
-                          void* summaries, const LayerOpts& o, const RopeTable& rt, uint32_t* err, cudaStream_t st) {
-  append_kernel<T><<<(unsigned)v.total_q, 128, (size_t)v.d_r * 4, st>>>(
-      v, (const T*)kv, kv_stride, (const T*)q, (T*)q_out, o, rt, err);
-  note_launch();
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || !summaries) return e;
-  const int group = (int)((v.total_q + 2047) / 2048);
-  summarise_kernel<T><<<(unsigned)((v.total_q + group - 1) / group), 256, (size_t)(v.d_c + v.d_r) * 4, st>>>(
-      v, group, (uint8_t*)summaries, (int64_t)summary_pitch(v.d_c, v.d_r));
-  note_launch();
-  return cudaGetLastError();
-}
-
 }  // namespace
 
 size_t summary_pitch(int32_t d_c, int32_t d_r) { return align16((size_t)d_c + d_r + 4); }
@@ -368,14 +493,32 @@ size_t summary_pitch(int32_t d_c, int32_t d_r) { return align16((size_t)d_c + d_
 cudaError_t paged_append(const PagedView& v, bool bf16, const void* kv, int64_t kv_stride, const void* q_rope,
                          void* q_out, void* summaries, const LayerOpts& o, const RopeTable& rope, uint32_t* err,
                          cudaStream_t st) {
-  return bf16 ? append_launch<__nv_bfloat16>(v, kv, kv_stride, q_rope, q_out, summaries, o, rope, err, st)
-              : append_launch<float>(v, kv, kv_stride, q_rope, q_out, summaries, o, rope, err, st);
+  if (bf16)
+    append_bf16_kernel<<<(unsigned)v.total_q, AP_THREADS, 0, st>>>(
+        v, (const __nv_bfloat16*)kv, kv_stride, (const __nv_bfloat16*)q_rope, (__nv_bfloat16*)q_out, o, rope, err);
+  else
+    append_kernel<<<(unsigned)v.total_q, 128, (size_t)v.d_r * 4, st>>>(v, (const float*)kv, kv_stride, (const float*)q_rope,
+                                                                      (float*)q_out, o, rope, err);
+  note_launch();
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !summaries) return e;
+  // enough blocks for every page to be on its own where tokens are few; else each looks at several tokens
+  const int group = (int)((v.total_q + 2047) / 2048);
+  const dim3 grid((unsigned)((v.total_q + group - 1) / group));
+  const size_t smem = (size_t)SUM_GROUPS * (v.d_c + v.d_r) * sizeof(double);
+  const int64_t pitch = (int64_t)summary_pitch(v.d_c, v.d_r);
+  return bf16 ? launch_next(summarise_kernel<__nv_bfloat16>, grid, 288, smem, st, v, group, (uint8_t*)summaries, pitch)
+              : launch_next(summarise_kernel<float>, grid, 512, smem, st, v, group, (uint8_t*)summaries, pitch);
 }
 
 cudaError_t paged_attention_simt(const PagedView& v, const void* q_abs, const void* q_rope, const int32_t* blocks,
                                  int32_t top_k, float scale, void* o_lat, float* lse, uint32_t* err, cudaStream_t st) {
-  paged_attention_kernel<<<dim3((unsigned)v.total_q, (unsigned)v.n_h), ATT, 0, st>>>(
-      v, (const float*)q_abs, (const float*)q_rope, blocks, top_k, scale, (float*)o_lat, lse, err);
+  const size_t row = (size_t)((v.d_c + v.d_r) | 1) * 4;
+  const int chunk = (int)(ATT_SMEM / row < ATT / 2 ? ATT_SMEM / row : ATT / 2);
+  cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ATT_SMEM);
+  if (e != cudaSuccess) return e;
+  paged_attention_kernel<<<dim3((unsigned)v.total_q, (unsigned)v.n_h), ATT, chunk * row, st>>>(
+      v, (const float*)q_abs, (const float*)q_rope, blocks, top_k, scale, chunk, (float*)o_lat, lse, err);
   note_launch();
   return cudaGetLastError();
 }

@@ -89,6 +89,29 @@ __device__ inline int64_t paged_list_rows(const int32_t* list, int32_t top_k, in
   return (int64_t)(n - 1) * page + (last == pos / page ? pos % page + 1 : page);
 }
 
+// Programmatic dependent launch: the next kernel of the chain may start its prologue; this one waits for the kernel
+// before it (and with it all earlier ones) to be complete and visible.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launches a kernel of the chain behind the one before it: its blocks may start early and wait in
+// wait_for_previous(), so that launch latency and prologue overlap the kernel before.
+template <typename... Params, typename... Args>
+cudaError_t launch_next(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, Args... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 size_t summary_pitch(int32_t d_c, int32_t d_r);   // bytes of a summary row
 
 cudaError_t paged_append(const PagedView& v, bool bf16, const void* kv, int64_t kv_stride, const void* q_rope,

@@ -195,11 +195,6 @@ __device__ __forceinline__ bool wait_own(uint32_t bar, uint32_t parity) {
   }
 }
 
-// Programmatic dependent launch: the next kernel of the chain may start its prologue; this one waits for the kernel
-// before it (and with it all earlier ones) to be complete and visible.
-__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // The tokens of a pair's range, and of each the keys [k0, k1) that fall into it.
 struct Walk {
   const int2* tinfo;
@@ -919,24 +914,6 @@ __global__ void __launch_bounds__(256)
   const float* x = &tile[h][cc];
   *reinterpret_cast<uint2*>(o_lat + ((int64_t)tok * H + h0 + h) * DC + c0 + cc) =
       make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-}
-
-// Launches a kernel of the chain behind the one before it: its blocks may start early and wait in
-// wait_for_previous(), so that launch latency and prologue overlap the kernel before.
-template <typename... Params, typename... Args>
-cudaError_t launch_next(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, Args... args) {
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  note_launch();
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <int GRAN>

@@ -223,18 +223,29 @@ class PagedBatch:
 
     def __init__(self, cache, block_table, cu_q, kv_lens, total_q: int):
         import torch
-        B = kv_lens.shape[0]
-        for name, x, dtype, shape in (("block_table", block_table, torch.int32, (B, None)),
-                                      ("cu_q", cu_q, torch.int64, (B + 1,)), ("kv_lens", kv_lens, torch.int64, (B,)),
-                                      ("cache", cache, cache.dtype, (None, None, None))):
-            _expect(name, x, dtype, shape, cache.device, contiguous=name != "block_table")
-        if block_table.shape[1] > 1 and block_table.stride(1) != 1:
+        B, dev = kv_lens.shape[0], cache.device
+        if not (block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == B
+                and block_table.device == dev and _is(cu_q, torch.int64, (B + 1,), dev)
+                and _is(kv_lens, torch.int64, (B,), dev) and cache.dim() == 3 and cache.is_contiguous()):
+            for name, x, dtype, shape in (("block_table", block_table, torch.int32, (B, None)),
+                                          ("cu_q", cu_q, torch.int64, (B + 1,)),
+                                          ("kv_lens", kv_lens, torch.int64, (B,)),
+                                          ("cache", cache, cache.dtype, (None, None, None))):
+                _expect(name, x, dtype, shape, dev, contiguous=name != "block_table")
+        max_pages = block_table.shape[1]
+        if max_pages > 1 and block_table.stride(1) != 1:
             raise ValueError("block_table: the entries of a row must be adjacent")
         self.tensors = (cache, block_table, cu_q, kv_lens)    # borrowed by the calls
-        self.cache, self.total_q, self.B, self.max_pages = cache, total_q, B, block_table.shape[1]
-        stride = block_table.stride(0) if B > 1 else block_table.shape[1]
-        self.c = MlaPaged(cache.data_ptr(), cache.shape[0], cache.shape[1], block_table.data_ptr(),
-                          block_table.shape[1], stride, cu_q.data_ptr(), kv_lens.data_ptr(), B, total_q)
+        self.cache, self.total_q, self.B, self.max_pages = cache, total_q, B, max_pages
+        self.c = MlaPaged(cache.data_ptr(), cache.shape[0], cache.shape[1], block_table.data_ptr(), max_pages,
+                          block_table.stride(0) if B > 1 else max_pages, cu_q.data_ptr(), kv_lens.data_ptr(), B,
+                          total_q)
+        self.ref = ctypes.byref(self.c)
+
+
+def _is(x, dtype, shape, device):
+    """Whether x is a dense tensor of this dtype, shape and device."""
+    return x.dtype == dtype and x.shape == shape and x.device == device and x.is_contiguous()
 
 
 def _expect(name, x, dtype, shape, device, contiguous=True):
@@ -255,7 +266,7 @@ def mla_paged_summary_bytes(handle) -> int:
 
 
 def mla_paged_append(handle, batch, kv, kv_stride, q_rope=None, q_out=None, summaries=None, stream=None, device=0):
-    _check(lib().mla_paged_append(handle, ctypes.byref(batch.c), _ptr(kv), kv_stride, _ptr(q_rope), _ptr(q_out),
+    _check(lib().mla_paged_append(handle, batch.ref, _ptr(kv), kv_stride, _ptr(q_rope), _ptr(q_out),
                                   _ptr(summaries), _stream(stream, device)), "mla_paged_append")
 
 
@@ -266,7 +277,7 @@ def mla_attn_paged_workspace(handle, B: int, total_q: int) -> int:
 
 
 def mla_attn_paged(handle, batch, q_abs, q_rope, o_lat, lse, ws, ws_bytes, stream=None, device=0):
-    _check(lib().mla_attn_paged(handle, ctypes.byref(batch.c), _ptr(q_abs), _ptr(q_rope), _ptr(o_lat), _ptr(lse),
+    _check(lib().mla_attn_paged(handle, batch.ref, _ptr(q_abs), _ptr(q_rope), _ptr(o_lat), _ptr(lse),
                                 _ptr(ws), ws_bytes, _stream(stream, device)), "mla_attn_paged")
 
 
@@ -278,14 +289,14 @@ def mla_paged_select_workspace(handle, total_q: int, max_pages: int) -> int:
 
 def mla_paged_select(handle, batch, q_abs, q_rope, summaries, top_k, n_first, n_last, blocks, ws, ws_bytes,
                      stream=None, device=0):
-    _check(lib().mla_paged_select(handle, ctypes.byref(batch.c), _ptr(q_abs), _ptr(q_rope), _ptr(summaries), top_k,
+    _check(lib().mla_paged_select(handle, batch.ref, _ptr(q_abs), _ptr(q_rope), _ptr(summaries), top_k,
                                   n_first, n_last, _ptr(blocks), _ptr(ws), ws_bytes, _stream(stream, device)),
            "mla_paged_select")
 
 
 def mla_attn_paged_sparse(handle, batch, q_abs, q_rope, blocks, top_k, o_lat, lse, ws, ws_bytes, stream=None,
                           device=0):
-    _check(lib().mla_attn_paged_sparse(handle, ctypes.byref(batch.c), _ptr(q_abs), _ptr(q_rope), _ptr(blocks), top_k,
+    _check(lib().mla_attn_paged_sparse(handle, batch.ref, _ptr(q_abs), _ptr(q_rope), _ptr(blocks), top_k,
                                        _ptr(o_lat), _ptr(lse), _ptr(ws), ws_bytes, _stream(stream, device)),
            "mla_attn_paged_sparse")
 
@@ -364,6 +375,7 @@ class MLA:
         self.torch = torch
         self.dims, self.dtype, self.device = dims, dtype, device
         self.tdtype = torch.bfloat16 if dtype == MLA_BF16 else torch.float32
+        self.torch_device = torch.device("cuda", device)
         self.handle = mla_create(dims, dtype, device)
         weights = weights or {}
         self.weights = {n: weights[n] for n in WEIGHT_NAMES} if weights else {}
@@ -483,17 +495,15 @@ class MLA:
         return o_lat, lse
 
     # --- the paged latent cache (PagedBatch)
-    def _expect_rows(self, batch, **tensors):
-        """Checks tensors [total_q, ...] given as name=(tensor, trailing shape, dtype or None for the handle's)."""
-        if batch.cache.dtype != self.tdtype or batch.cache.shape[2] != self.dims.d_c + self.dims.d_r:
-            raise ValueError(f"cache: expected {self.tdtype} rows of {self.dims.d_c + self.dims.d_r}, "
-                             f"got {batch.cache.dtype} {list(batch.cache.shape)}")
-        dev = self.torch.device("cuda", self.device)
-        if batch.cache.device != dev:
-            raise ValueError(f"cache: on {batch.cache.device}, the handle is on {dev}")
-        for name, (x, shape, dtype) in tensors.items():
-            if x is not None:
-                _expect(name, x, dtype or self.tdtype, (batch.total_q, *shape), batch.cache.device)
+    def _expect_rows(self, batch, tensors):
+        """Checks the cache's rows and tensors [total_q, ...], each (name, tensor, trailing shape, dtype)."""
+        cache, dev = batch.cache, self.torch_device
+        if cache.dtype != self.tdtype or cache.shape[2] != self.dims.d_c + self.dims.d_r or cache.device != dev:
+            raise ValueError(f"cache: expected {self.tdtype} rows of {self.dims.d_c + self.dims.d_r} on {dev}, "
+                             f"got {cache.dtype} {list(cache.shape)} on {cache.device}")
+        for name, x, shape, dtype in tensors:
+            if not _is(x, dtype, (batch.total_q, *shape), dev):
+                _expect(name, x, dtype, (batch.total_q, *shape), dev)
 
     def new_summaries(self, num_pages: int):
         """Zeroed summary rows of num_pages pages."""
@@ -501,18 +511,24 @@ class MLA:
                                 device=f"cuda:{self.device}")
 
     def _expect_summaries(self, batch, summaries):
-        _expect("summaries", summaries, self.torch.uint8, (batch.cache.shape[0], mla_paged_summary_bytes(self.handle)),
-                batch.cache.device)
+        d = self.dims
+        shape = (batch.cache.shape[0], (d.d_c + d.d_r + 4 + 15) // 16 * 16)
+        if not _is(summaries, self.torch.uint8, shape, self.torch_device):
+            _expect("summaries", summaries, self.torch.uint8, shape, self.torch_device)
 
     def paged_append(self, batch, kv, q_rope=None, q_out=None, summaries=None):
         """Writes the new tokens' rows (kv [total_q, d_c + d_r], rows may be strided) to their pages; with q_rope
         returns the rotated queries (q_out, which may be q_rope itself)."""
-        d = self.dims
-        qs = ((d.n_h, d.d_r), None)
-        if q_rope is not None and q_out is None:
-            q_out = self.torch.empty_like(q_rope)
-        self._expect_rows(batch, q_rope=(q_rope, *qs), q_out=(q_out, *qs))
-        _expect("kv", kv, self.tdtype, (batch.total_q, d.d_c + d.d_r), batch.cache.device, contiguous=False)
+        d, T = self.dims, batch.total_q
+        if q_rope is None:
+            self._expect_rows(batch, ())
+        else:
+            self._expect_rows(batch, (("q_rope", q_rope, (d.n_h, d.d_r), self.tdtype),
+                                      ("q_out", q_rope if q_out is None else q_out, (d.n_h, d.d_r), self.tdtype)))
+            if q_out is None:
+                q_out = self.torch.empty_like(q_rope)
+        if kv.dtype != self.tdtype or kv.shape != (T, d.d_c + d.d_r) or kv.device != self.torch_device:
+            _expect("kv", kv, self.tdtype, (T, d.d_c + d.d_r), self.torch_device, contiguous=False)
         if kv.stride(1) != 1:
             raise ValueError("kv: the elements of a row must be adjacent")
         if summaries is not None:
@@ -531,14 +547,20 @@ class MLA:
 
     def _attn_paged(self, batch, q_abs, q_rope, blocks, o_lat, lse):
         torch, d, T = self.torch, self.dims, batch.total_q
+        rows = [("q_abs", q_abs, (d.n_h, d.d_c), self.tdtype), ("q_rope", q_rope, (d.n_h, d.d_r), self.tdtype)]
+        top_k = 0
+        if blocks is not None:
+            top_k = blocks.shape[-1]
+            rows.append(("blocks", blocks, (top_k,), torch.int32))
+        if o_lat is not None:
+            rows.append(("o_lat", o_lat, (d.n_h, d.d_c), self.tdtype))
+        if lse is not None:
+            rows.append(("lse", lse, (d.n_h,), torch.float32))
+        self._expect_rows(batch, rows)
         if o_lat is None:
-            o_lat = torch.empty(T, d.n_h, d.d_c, dtype=self.tdtype, device=q_abs.device)
+            o_lat = torch.empty((T, d.n_h, d.d_c), dtype=self.tdtype, device=self.torch_device)
         if lse is None:
-            lse = torch.empty(T, d.n_h, dtype=torch.float32, device=q_abs.device)
-        top_k = 0 if blocks is None else blocks.shape[-1]
-        self._expect_rows(batch, q_abs=(q_abs, (d.n_h, d.d_c), None), q_rope=(q_rope, (d.n_h, d.d_r), None),
-                          o_lat=(o_lat, (d.n_h, d.d_c), None), lse=(lse, (d.n_h,), torch.float32),
-                          blocks=(blocks, (top_k,), torch.int32))
+            lse = torch.empty((T, d.n_h), dtype=torch.float32, device=self.torch_device)
         ws = self.workspace(mla_attn_paged_workspace(self.handle, batch.B, T))
         if blocks is None:
             mla_attn_paged(self.handle, batch, q_abs, q_rope, o_lat, lse, ws, ws.numel(), device=self.device)
@@ -551,11 +573,13 @@ class MLA:
                      blocks=None):
         """The blocks each new token attends to, [total_q, top_k] int32."""
         d = self.dims
-        if blocks is None:
-            blocks = self.torch.empty(batch.total_q, top_k, dtype=self.torch.int32, device=q_abs.device)
-        self._expect_rows(batch, q_abs=(q_abs, (d.n_h, d.d_c), None), q_rope=(q_rope, (d.n_h, d.d_r), None),
-                          blocks=(blocks, (top_k,), self.torch.int32))
+        rows = [("q_abs", q_abs, (d.n_h, d.d_c), self.tdtype), ("q_rope", q_rope, (d.n_h, d.d_r), self.tdtype)]
+        if blocks is not None:
+            rows.append(("blocks", blocks, (top_k,), self.torch.int32))
+        self._expect_rows(batch, rows)
         self._expect_summaries(batch, summaries)
+        if blocks is None:
+            blocks = self.torch.empty((batch.total_q, top_k), dtype=self.torch.int32, device=self.torch_device)
         ws = self.workspace(mla_paged_select_workspace(self.handle, batch.total_q, batch.max_pages))
         mla_paged_select(self.handle, batch, q_abs, q_rope, summaries, top_k, n_first, n_last, blocks, ws, ws.numel(),
                          device=self.device)
