@@ -254,6 +254,7 @@ __global__ void __launch_bounds__(ATT)
   const int64_t oq = t * v.n_h + head;
   for (int c = tid; c < W; c += ATT) qs[c] = c < v.d_c ? q_abs[oq * v.d_c + c] : q_rope[oq * v.d_r + c - v.d_c];
   const float* cache = reinterpret_cast<const float*>(v.cache);
+  const bool vec = W % 4 == 0;        // rows start on 16 bytes
   // P.V: group kg of G takes the keys kg, kg + G, ...; with d_c > ATT a thread takes columns col, col + ATT
   const int width = min(v.d_c, ATT), G = ATT / width, kg = tid / width, col = tid % width;
   float m = -INFINITY, l = 0.f, acc[2] = {0.f, 0.f};
@@ -265,28 +266,50 @@ __global__ void __launch_bounds__(ATT)
       row_of[j] = page < 0 ? -1 : page * v.page + k % v.page;
     }
     __syncthreads();
-#pragma unroll 4
-    for (int i = tid; i < cnt * W; i += ATT) {
-      const int j = i / W, c = i - j * W;
-      const int64_t r = row_of[j];
-      rows[j * ld + c] = r < 0 ? 0.f : cache[r * W + c];       // a page outside the pool counts as rows of zeros
+    // a warp a row, four rows in flight; a page outside the pool counts as rows of zeros
+    const int lane = tid & 31;
+    for (int j0 = tid >> 5; j0 < cnt; j0 += 4 * (ATT / 32)) {
+      if (vec) {
+        for (int c = lane; c < W / 4; c += 32) {
+          float4 u[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int j = j0 + k * (ATT / 32);
+            u[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (j < cnt && row_of[j] >= 0) u[k] = reinterpret_cast<const float4*>(cache + row_of[j] * W)[c];
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int j = j0 + k * (ATT / 32);
+            if (j >= cnt) break;
+            float* dst = rows + j * ld + 4 * c;
+            dst[0] = u[k].x; dst[1] = u[k].y; dst[2] = u[k].z; dst[3] = u[k].w;
+          }
+        }
+      } else {
+        for (int k = 0; k < 4; ++k) {
+          const int j = j0 + k * (ATT / 32);
+          if (j >= cnt) break;
+          for (int c = lane; c < W; c += 32) rows[j * ld + c] = row_of[j] < 0 ? 0.f : cache[row_of[j] * W + c];
+        }
+      }
     }
     __syncthreads();
     const int j = tid >> 1;
     float s = -INFINITY;
     {
-      // two chains of sums per thread, then the neighbour's half
+      // four chains of sums per thread, then the neighbour's half
       const int half = (W + 1) / 2, lo = (tid & 1) * half, hi = min(W, lo + half);
       const float* k = rows + min(j, cnt - 1) * ld;
-      float d0 = 0.f, d1 = 0.f;
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
       int c = lo;
 #pragma unroll 4
-      for (; c + 1 < hi; c += 2) {
-        d0 = fmaf(qs[c], k[c], d0);
-        d1 = fmaf(qs[c + 1], k[c + 1], d1);
+      for (; c + 3 < hi; c += 4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[e] = fmaf(qs[c + e], k[c + e], d[e]);
       }
-      if (c < hi) d0 = fmaf(qs[c], k[c], d0);
-      d0 += d1;
+      for (; c < hi; ++c) d[0] = fmaf(qs[c], k[c], d[0]);
+      float d0 = (d[0] + d[1]) + (d[2] + d[3]);
       d0 += __shfl_xor_sync(0xffffffffu, d0, 1);
       if (j < cnt) s = d0 * scale;
     }
@@ -299,7 +322,7 @@ __global__ void __launch_bounds__(ATT)
     acc[1] *= alpha;
     __syncthreads();
     if (kg < G) {
-#pragma unroll 4
+#pragma unroll 8
       for (int jj = kg; jj < cnt; jj += G) {
         const float pj = ps[jj];
         acc[0] = fmaf(pj, rows[jj * ld + col], acc[0]);

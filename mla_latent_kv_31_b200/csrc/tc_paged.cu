@@ -524,27 +524,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int rem = w.k1 - (w.k0 + j * NK);              // visible keys from the step's first on
         if (!wait_u(bar(B_SFULL + sb), (js >> 1) & 1)) { ok = false; break; }
         tc_fence_after();
-        float s[64];
-        tmem_ld32(trow + 256 + 128 * sb + 64 * half, reinterpret_cast<uint32_t*>(s));
-        tmem_ld32(trow + 256 + 128 * sb + 64 * half + 32, reinterpret_cast<uint32_t*>(s) + 32);
-        tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_pair(sfree + 8 * sb);
+        // Two passes over the scores, 32 columns at a time from tensor memory (64 columns held in registers take the
+        // same time, but 128 registers with spills instead of 94)
+        const uint32_t scol = trow + 256 + 128 * sb + 64 * half;
         const int nvis = rem - 64 * kq;
-        if (nvis < 64) {
+        auto load = [&](int h, float* s) {
+          tmem_ld32(scol + 32 * h, reinterpret_cast<uint32_t*>(s));
+          tmem_wait_ld();
+          if (nvis < 32 * h + 32) {
 #pragma unroll
-          for (int c = 0; c < 64; ++c) s[c] = c < nvis ? s[c] : -INFINITY;
+            for (int c = 0; c < 32; ++c) s[c] = 32 * h + c < nvis ? s[c] : -INFINITY;
+          }
+        };
+        float own = -INFINITY;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          float s[32];
+          load(h, s);
+#pragma unroll
+          for (int k = 16; k > 0; k >>= 1)
+#pragma unroll
+            for (int c = 0; c < k; ++c) s[c] = fmaxf(s[c], s[c + k]);
+          own = fmaxf(own, s[0]);
         }
-        float mx[16];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) mx[c] = fmaxf(fmaxf(s[4 * c], s[4 * c + 1]), fmaxf(s[4 * c + 2], s[4 * c + 3]));
-#pragma unroll
-        for (int k = 8; k > 0; k >>= 1)
-#pragma unroll
-          for (int c = 0; c < k; ++c) mx[c] = fmaxf(mx[c], mx[c + k]);
         float* rbuf = red + sb * 4 * HC;
-        rbuf[kq * HC + i] = mx[0];
+        rbuf[kq * HC + i] = own;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_TMAX + rb));
         if (!wait_u(bar(B_TMAX + rb), js & 1)) { ok = false; break; }
@@ -555,32 +559,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           alpha = m == -INFINITY ? 0.f : ex2_approx((m - top) * c2);
           l *= alpha;
           m = top;
-        }
-        uint32_t pk[32];
-        if (m > -INFINITY) {
-          const uint64_t cc = f2_pack(c2, c2), off = f2_pack(-m * c2, -m * c2);
-          uint64_t acc[8];
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            float a0, a1;
-            f2_unpack(f2_fma(f2_pack(s[2 * c], s[2 * c + 1]), cc, off), a0, a1);
-            const float e0 = ex2_approx(a0), e1 = ex2_approx(a1);
-            // P in bf16 for the MMA (2^-8 of each weight); the sum takes the unrounded weights
-            pk[c] = pack_bf16(e0, e1);
-            const uint64_t le = f2_pack(e0, e1);
-            if (c < 8) acc[c] = le;
-            else acc[c & 7] = f2_add(acc[c & 7], le);
-          }
-#pragma unroll
-          for (int k = 4; k > 0; k >>= 1)
-#pragma unroll
-            for (int c = 0; c < k; ++c) acc[c] = f2_add(acc[c], acc[c + k]);
-          float l0, l1;
-          f2_unpack(acc[0], l0, l1);
-          l += l0 + l1;
-        } else {
-#pragma unroll
-          for (int c = 0; c < 32; ++c) pk[c] = 0u;
         }
         // P.V of the step before is done: P may be overwritten and O rescaled
         if (js > 0 && !wait_u(bar(B_PVD), (js - 1) & 1)) { ok = false; break; }
@@ -598,11 +576,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tmem_wait_st();
           tc_fence_before();
         }
+        // P = 2^((s - m) c2) in bf16 for the MMA (2^-8 of each weight); the sum takes the unrounded weights
+        const float moff = m > -INFINITY ? -m * c2 : 0.f;       // (no finite score: all weights are 2^-inf)
+        const uint64_t cc = f2_pack(c2, c2), off = f2_pack(moff, moff);
         uint8_t* prow = smem + OFF_P + kq * BOX + i * 128;
+        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          float s[32];
+          load(h, s);
+          uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4*>(prow + ((c ^ (i & 7)) << 4)) =
-              make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+          for (int c = 0; c < 16; ++c) {
+            float a0, a1;
+            f2_unpack(f2_fma(f2_pack(s[2 * c], s[2 * c + 1]), cc, off), a0, a1);
+            const float e0 = ex2_approx(a0), e1 = ex2_approx(a1);
+            pk[c] = pack_bf16(e0, e1);
+            acc[c & 3] = f2_add(acc[c & 3], f2_pack(e0, e1));
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint4*>(prow + (((4 * h + c) ^ (i & 7)) << 4)) =
+                make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        }
+        {
+          float l0, l1;
+          f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), l0, l1);
+          l += l0 + l1;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_pair(sfree + 8 * sb);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) arrive_pair(prdy);
