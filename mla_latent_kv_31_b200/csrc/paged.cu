@@ -154,27 +154,32 @@ __device__ __forceinline__ int code_of(float x, float s) {
   return r >= 127.f ? 127 : r <= -127.f ? -127 : (int)r;
 }
 
-// Summaries of the pages that the new tokens complete. Block i looks at `group` tokens; a token that is its page's last
-// row stands for the page. The lookups come before the wait for the append's rows. Four groups of threads take a
-// quarter of the rows each (page sizes are multiples of 16), 16 of them in flight; their sums meet in shared memory.
-// The sums are in double: of bf16 values they are exact, so the summary does not depend on the order.
+// Summaries of the pages that the new tokens complete. Block i looks at `group` <= 32 tokens, a lane each; a token that is
+// its page's last row stands for the page. The lookups come before the wait for the append's rows. Four groups of
+// threads take a quarter of the rows each (page sizes are multiples of 16), 16 of them in flight; their sums meet in
+// shared memory. The sums are in double: of bf16 values they are exact, so the summary does not depend on the order.
 constexpr int SUM_GROUPS = 4;
 template <typename T>
 __global__ void __launch_bounds__(512) summarise_kernel(PagedView v, int group, uint8_t* summaries, int64_t pitch) {
   extern __shared__ double part[];    // [SUM_GROUPS][W]
   __shared__ float red[32];
   const int tid = threadIdx.x, W = v.d_c + v.d_r;
-  bool waited = false;
-  for (int k = 0; k < group; ++k) {
-    const int64_t t = (int64_t)blockIdx.x * group + k;
-    if (t >= v.total_q) break;
-    const PagedToken tok = paged_token(v, t);
-    if (tok.seq < 0) break;
-    if (tok.pos < 0 || tok.pos % v.page != v.page - 1) continue;
-    const int32_t p = v.table[(int64_t)tok.seq * v.stride + tok.pos / v.page];
-    if (p < 0 || p >= v.num_pages) continue;      // flagged by the append
-    if (!waited) wait_for_previous();
-    waited = true;
+  int32_t own = -1;                   // the page that this lane's token completes
+  {
+    const int64_t t = (int64_t)blockIdx.x * group + (tid & 31);
+    if ((tid & 31) < group && t < v.total_q && t < v.cu_q[v.B]) {
+      const int64_t b = seq_of_token(v.cu_q, v.B, t), q0 = v.cu_q[b], n = v.cu_q[b + 1] - q0, len = v.kv_lens[b];
+      const int64_t pos = len - n + (t - q0);
+      if (t >= q0 && t - q0 < n && n <= len && len <= v.max_pages * v.page && (pos + 1) % v.page == 0) {
+        own = v.table[b * v.stride + pos / v.page];
+        if (own >= v.num_pages) own = -1;                     // flagged by the append
+      }
+    }
+  }
+  uint32_t pages = __ballot_sync(0xffffffffu, own >= 0);      // the same in every warp
+  wait_for_previous();
+  for (; pages; pages &= pages - 1) {
+    const int32_t p = __shfl_sync(0xffffffffu, own, __ffs(pages) - 1);
     const T* rows = reinterpret_cast<const T*>(v.cache) + (int64_t)p * v.page * W;
     constexpr int E = sizeof(T) == 2 ? 8 : 1;     // columns per thread: 16 bytes of bf16 (W is a multiple of 8 there)
     const int cols = W / E, per = v.page / SUM_GROUPS;
@@ -224,7 +229,6 @@ __global__ void __launch_bounds__(512) summarise_kernel(PagedView v, int group, 
     if (tid == 0) *reinterpret_cast<float*>(out + W) = s;
     __syncthreads();
   }
-  if (!waited) wait_for_previous();   // this kernel must not be complete before the append is
 }
 
 // ---- attention by CUDA cores --------------------------------------------------------------------------------
@@ -525,8 +529,8 @@ cudaError_t paged_append(const PagedView& v, bool bf16, const void* kv, int64_t 
   note_launch();
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !summaries) return e;
-  // enough blocks for every page to be on its own where tokens are few; else each looks at several tokens
-  const int group = (int)((v.total_q + 2047) / 2048);
+  // a token a block where they are few (each may complete a page), else about two blocks an SM
+  const int group = (int)(v.total_q <= 296 ? 1 : v.total_q >= 32 * 296 ? 32 : (v.total_q + 295) / 296);
   const dim3 grid((unsigned)((v.total_q + group - 1) / group));
   const size_t smem = (size_t)SUM_GROUPS * (v.d_c + v.d_r) * sizeof(double);
   const int64_t pitch = (int64_t)summary_pitch(v.d_c, v.d_r);

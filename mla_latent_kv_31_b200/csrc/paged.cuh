@@ -27,12 +27,28 @@ struct PagedToken {
   int64_t pos;
 };
 
+// (Called by whole warps with one t: the lanes look at 32 entries of cu_q at a time, one trip to L2 where a bisection
+// takes log2(B) one after the other; it only narrows long lists down.)
 __device__ __forceinline__ PagedToken paged_token(const PagedView& v, int64_t t) {
   PagedToken r;
   r.seq = -1;
   r.pos = -1;
-  if (t >= v.cu_q[v.B]) return r;
-  const int64_t b = seq_of_token(v.cu_q, v.B, t);
+  const int lane = threadIdx.x & 31;
+  int64_t lo = 0, hi = v.B;           // the last entry <= t is in [lo, hi]
+  while (hi - lo >= 256) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (v.cu_q[mid] <= t) lo = mid; else hi = mid;
+  }
+  const int64_t end = v.cu_q[v.B];
+  int64_t b = lo;
+#pragma unroll 4
+  for (int64_t i = lo; i <= hi; i += 32) {
+    const bool in = i + lane <= hi && v.cu_q[min(i + lane, hi)] <= t;
+    const uint32_t m = __ballot_sync(0xffffffffu, in);
+    if (m) b = i + 31 - __clz(m);
+  }
+  if (t >= end) return r;
+  b = min(b, v.B - 1);
   const int64_t q0 = v.cu_q[b], n = v.cu_q[b + 1] - q0, len = v.kv_lens[b];
   r.seq = (int32_t)b;
   if (t >= q0 && t - q0 < n && n <= len && len <= v.max_pages * v.page) r.pos = len - n + (t - q0);
