@@ -370,6 +370,7 @@ __global__ void __launch_bounds__(32 * SCORE_WARPS)
     score_kernel(PagedView v, const int8_t* codes, const float* scales, const uint8_t* summaries, int64_t pitch,
                  int32_t top_k, float* scores, uint32_t* err) {
   extern __shared__ int32_t ksh[];    // [32][W / 4 | 1]
+  let_next_start();
   __shared__ float best[SCORE_WARPS][32];
   const int64_t t = blockIdx.y;
   const PagedToken tok = paged_token(v, t);
@@ -423,6 +424,7 @@ __global__ void __launch_bounds__(kSelectThreads)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int NW = kSelectThreads / 32;
   const PagedToken tok = paged_token(v, t);
+  wait_for_previous();
   if (tok.seq < 0) return;
   int32_t* out = blocks + t * top_k;
   const int nb = tok.pos < 0 ? 0 : (int)(tok.pos / v.page) + 1;
@@ -576,9 +578,8 @@ cudaError_t paged_select(const PagedView& v, bool bf16, const void* q_abs, const
     note_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  select_kernel<<<(unsigned)v.total_q, kSelectThreads, 0, st>>>(v, scores, top_k, n_first, n_last, blocks);
-  note_launch();
-  return cudaGetLastError();
+  return launch_next(select_kernel, dim3((unsigned)v.total_q), kSelectThreads, 0, st, v, (const float*)scores, top_k,
+                     n_first, n_last, blocks);
 }
 
 }  // namespace mla

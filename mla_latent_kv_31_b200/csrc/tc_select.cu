@@ -2,12 +2,13 @@
 // block g, max_i s_i (x_i . y_g) with int8 codes x_i of the 128 query rows [q~_i | q^R_i] and y_g of the block's
 // summary, times the summary's scale. The products are whole numbers (kind::i8, int32 accumulation): exact.
 //
-// A CTA takes one token and every gridDim.x-th tile of 128 blocks. It quantises the token's queries into shared memory
-// once (they are read from HBM once per CTA), then per tile gathers 128 summary rows (cp.async, the rows of a tile
-// lie anywhere) and multiplies: M = 128 blocks, N = 128 heads, K = 576, 18 MMAs of K = 32. With the blocks on the
-// lanes the maximum over the heads stays in a thread. Two buffers of summaries and two accumulators, so that the
-// next tile is fetched and multiplied while a tile's maxima are taken.
-// Bounds: the queries' bytes (147 KB a token) for chunks; the chain of latencies for a few tokens.
+// A CTA takes tokens t, t + gridDim.y, ... and of each every gridDim.x-th tile of 128 blocks. Half of its warps take the
+// token's tiles: they gather 128 summary rows (cp.async; the rows of a tile lie anywhere) and multiply, M = 128 blocks,
+// N = 128 heads, K = 576 in 18 MMAs of K = 32; with the blocks on the lanes the maximum over the heads stays in a
+// thread, and it is taken while the next tile is fetched. The other half quantise the next token's queries into
+// the other of two buffers meanwhile (the first token's by all), so queries are read from HBM once per CTA.
+// Bounds: a tile takes about 2.3 us, of which the gather's latency is 1.6; a token's codes take 5 us. With one token
+// a CTA the chain lookup - queries - codes - tile - score.
 #include <cuda_bf16.h>
 
 #include "paged.cuh"
@@ -21,21 +22,20 @@ using namespace sm100;
 
 constexpr int H = 128, DC = 512, DR = 64, W = DC + DR;
 constexpr int TILE = 128;                       // blocks per tile
-constexpr int kThreads = 512;
+constexpr int kThreads = 512;                   // 8 warps for the tiles, 8 for the next token's codes
 constexpr uint32_t KBOX = 128 * 128;            // [128 rows x 128 codes], 128-byte swizzle
-// A row is 4.5 boxes wide: the two summary buffers share the ninth box (codes 512 .. 575 in its left or right half),
-// which leaves room for both beside the queries.
-constexpr uint32_t OFF_Q = 0;                                  // 5 boxes
-constexpr uint32_t OFF_Y = OFF_Q + 5 * KBOX;                   // 2 x 4 boxes, then the shared one
-constexpr uint32_t OFF_YH = OFF_Y + 8 * KBOX;
-constexpr uint32_t OFF_SQ = OFF_YH + KBOX;                     // [128] scales of the queries
-constexpr uint32_t OFF_BAR = OFF_SQ + H * 4;                   // 2 barriers, TMEM address
+// A row is 4.5 boxes wide: the two query buffers share a ninth box (codes 512 .. 575 in its left or right half).
+constexpr uint32_t OFF_Q = 0;                                  // 2 x 4 boxes, then the shared one
+constexpr uint32_t OFF_QH = OFF_Q + 8 * KBOX;
+constexpr uint32_t OFF_Y = OFF_QH + KBOX;                      // 5 boxes
+constexpr uint32_t OFF_SQ = OFF_Y + 5 * KBOX;                  // [2][128] scales of the queries
+constexpr uint32_t OFF_BAR = OFF_SQ + 2 * H * 4;               // a barrier, TMEM address
 constexpr uint32_t SMEM_BYTES = OFF_BAR + 32 + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
-// The right half of the queries' fifth box is free: chunk c (4 .. 7) of row r holds 16 bytes of what goes with
-// block r of a tile: the summaries' scales of the two buffers (4), the maxima of the column groups 1 .. 3 (5).
+// The right half of the summaries' fifth box is free: chunk c (4 .. 7) of row r holds 16 bytes of what goes with block r
+// of a tile: the summary's scale (4), the maximum over the upper 64 heads (5).
 __device__ __forceinline__ uint32_t row_chunk(int r, int c) {
-  return OFF_Q + 4 * KBOX + r * 128 + ((c ^ (r & 7)) << 4);
+  return OFF_Y + 4 * KBOX + r * 128 + ((c ^ (r & 7)) << 4);
 }
 
 // kind::i8: signed 8-bit A and B, 32-bit integer D, both K-major.
@@ -109,20 +109,12 @@ __device__ __forceinline__ uint32_t max_bits(__nv_bfloat162 m) {
   return __float_as_uint(fmaxf(fmaxf(__low2float(m), __high2float(m)), 0.f));
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
-    select_score_kernel(PagedView v, const __nv_bfloat16* q_abs, const __nv_bfloat16* q_rope, const uint8_t* summaries,
-                        int64_t pitch, int32_t top_k, float* scores, uint32_t* err) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t sbase = smem_addr(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t t = blockIdx.y;
-  // A warp quantises 8 query rows: all of their loads are in flight while the token is looked up. Lane: the chunks of 8
-  // elements lane and lane + 32 of each row, and q^R's chunk lane % 8 of rows lane / 8 and 4 + lane / 8.
-  constexpr int ROWS = H / (kThreads / 32);
-  const int i0 = ROWS * warp;
+// Quantises ROWS query rows, the warp's own, of token t into buffer b: loads, then codes. Lane: the chunks of 8 elements
+// lane and lane + 32 of each row, and q^R's chunk lane % 8 of rows lane / 8 and 4 + lane / 8.
+constexpr int ROWS = 8;
+struct QueryRows {
   uint4 u[ROWS][2], ur[2];
-  {
+  __device__ __forceinline__ void load(const __nv_bfloat16* q_abs, const __nv_bfloat16* q_rope, int64_t t, int i0, int lane) {
     const uint4* qa = reinterpret_cast<const uint4*>(q_abs + (t * H + i0) * DC) + lane;
     const uint4* qr = reinterpret_cast<const uint4*>(q_rope + (t * H + i0) * DR) + lane;
 #pragma unroll
@@ -133,160 +125,209 @@ __global__ void __launch_bounds__(kThreads, 1)
     ur[0] = qr[0];
     ur[1] = qr[32];
   }
-  if (blockIdx.x == 0 && t == 0) paged_check(v, err);
-  const PagedToken tok = paged_token(v, t);
-  if (tok.pos < 0) return;
-  const int nb = (int)(tok.pos / v.page) + 1;
-  const int stride = gridDim.x, first = blockIdx.x;
-  const int tiles = (nb + TILE - 1) / TILE;
-  if (nb <= top_k || first >= tiles) return;
-  const int n = (tiles - first + stride - 1) / stride;        // tiles of this CTA
-  auto bar = [&](int i) { return sbase + OFF_BAR + 8u * (uint32_t)i; };
+  __device__ __forceinline__ void codes(uint8_t* smem, int b, int i0, int lane) const {
+    float* sq = reinterpret_cast<float*>(smem + OFF_SQ) + b * H;
+    auto put = [&](int i, int c, uint2 x) {                   // 8-code chunk c (0 .. 71) of row i
+      const uint32_t dst = c < 64 ? OFF_Q + (4 * b + (c >> 4)) * KBOX + i * 128 + ((((c & 15) >> 1) ^ (i & 7)) << 4)
+                                  : OFF_QH + i * 128 + (((4 * b + ((c & 15) >> 1)) ^ (i & 7)) << 4);
+      *reinterpret_cast<uint2*>(smem + dst + (c & 1) * 8) = x;
+    };
+    float srow[2] = {0.f, 0.f};                               // scales of the rows of ur
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t mr = max_bits(max8(ur[h]));
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) mr = max(mr, __shfl_xor_sync(0xffffffffu, mr, o));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int j = 4 * h + k;
+        const uint32_t own = max(max_bits(max8(u[j][0])), max_bits(max8(u[j][1])));
+        const float amax = __uint_as_float(max(__reduce_max_sync(0xffffffffu, own), __shfl_sync(0xffffffffu, mr, 8 * k)));
+        float s = __fdiv_rn(amax, 127.f);
+        if (!(s > 0.f && s < INFINITY)) s = 0.f;
+        const float inv = 1.f / s;
+        put(i0 + j, lane, s == 0.f ? make_uint2(0u, 0u) : codes8(u[j][0], s, inv));
+        put(i0 + j, lane + 32, s == 0.f ? make_uint2(0u, 0u) : codes8(u[j][1], s, inv));
+        if (lane == 0) sq[i0 + j] = s;
+        if ((lane >> 3) == k) srow[h] = s;
+      }
+      put(i0 + 4 * h + (lane >> 3), 64 + (lane & 7),
+          srow[h] == 0.f ? make_uint2(0u, 0u) : codes8(ur[h], srow[h], 1.f / srow[h]));
+    }
+  }
+};
 
-  // The page of this thread's row (four threads a row) of the i-th tile, -1 for none.
-  auto page_of = [&](int i) -> int {
-    const int g = (first + i * stride) * TILE + (tid >> 2);
-    if (i >= n || g >= nb) return -1;
-    const int p = v.table[(int64_t)tok.seq * v.stride + g];
+__global__ void __launch_bounds__(kThreads, 1)
+    select_score_kernel(PagedView v, const __nv_bfloat16* q_abs, const __nv_bfloat16* q_rope, const uint8_t* summaries,
+                        int64_t pitch, int32_t top_k, float* scores, uint32_t* err) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_addr(smem), bar = sbase + OFF_BAR;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool tiles_half = warp < 8;
+  const int stride = gridDim.x, first = blockIdx.x;
+  int64_t t = blockIdx.y;
+  let_next_start();
+
+  // blocks of a token, 0 when there is nothing to score for this CTA
+  auto blocks_of = [&](const PagedToken& k) -> int {
+    const int nb = k.pos < 0 ? 0 : (int)(k.pos / v.page) + 1;
+    return nb > top_k && first * TILE < nb ? nb : 0;
+  };
+  {
+    // the first token: all loads are in flight while it is looked up
+    QueryRows q;
+    q.load(q_abs, q_rope, t, ROWS * warp, lane);
+    if (blockIdx.x == 0 && t == 0) paged_check(v, err);
+    if (tid == 0) {
+      mbar_init(bar, 1);
+      fence_mbar_init();
+    }
+    if (warp == 0) {
+      tmem_alloc(bar + 16, 128);
+      tmem_relinquish();
+    }
+    q.codes(smem, 0, ROWS * warp, lane);
+    fence_proxy_async_smem();
+  }
+  PagedToken tok = paged_token(v, t);
+  int nb = blocks_of(tok);
+  // The page of row 16 warp + lane % 16 of tile i of a token, -1 for none.
+  auto page_of = [&](const PagedToken& k, int n_blocks, int i) -> int {
+    const int g = (first + i * stride) * TILE + 16 * warp + (lane & 15);
+    if (g >= n_blocks) return -1;
+    const int p = v.table[(int64_t)k.seq * v.stride + g];
     if (p < 0 || p >= v.num_pages) {
       flag_error(err, DEVERR_PAGE);
       return -1;
     }
     return p;
   };
-  // Summary rows of the i-th tile into buffer i & 1: chunks (tid & 3) + 4 k of the thread's row.
-  auto fetch = [&](int i, int page) {
-    const int row = tid >> 2, b = i & 1;
-    const uint8_t* src = summaries + (int64_t)(page < 0 ? 0 : page) * pitch;
-    const uint32_t drow = row * 128;
+  // A tile's summary rows, 16 a warp: the first 512 bytes of a row by 32 lanes (contiguous: four times fewer L1 requests
+  // than a few lanes a row), then the last 64 of eight rows at a time, then the scales.
+  auto fetch = [&](int page) {
 #pragma unroll
-    for (int k = 0; k < 9; ++k) {
-      const int c = (tid & 3) + 4 * k;                        // 16-byte chunk 0 .. 35
-      const uint32_t dst = k < 8 ? OFF_Y + (4 * b + (c >> 3)) * KBOX + drow + (((c & 7) ^ (row & 7)) << 4)
-                                 : OFF_YH + drow + (((4 * b + (c & 3)) ^ (row & 7)) << 4);
-      copy16(sbase + dst, src + 16 * c, page < 0);
+    for (int j = 0; j < 16; ++j) {
+      const int p = __shfl_sync(0xffffffffu, page, j), r = 16 * warp + j;
+      copy16(sbase + OFF_Y + (lane >> 3) * KBOX + r * 128 + (((lane & 7) ^ (j & 7)) << 4),
+             summaries + (int64_t)(p < 0 ? 0 : p) * pitch + 16 * lane, p < 0);
     }
-    if ((tid & 3) == 0)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(sbase + row_chunk(row, 4) + 4 * b),
-                   "l"(src + W), "r"(page < 0 ? 0 : 4)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int j = 8 * h + (lane >> 2), p = __shfl_sync(0xffffffffu, page, j), r = 16 * warp + j, c = lane & 3;
+      copy16(sbase + OFF_Y + 4 * KBOX + r * 128 + ((c ^ (j & 7)) << 4),
+             summaries + (int64_t)(p < 0 ? 0 : p) * pitch + 512 + 16 * c, p < 0);
+    }
+    if (lane < 16)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(sbase + row_chunk(16 * warp + lane, 4)),
+                   "l"(summaries + (int64_t)(page < 0 ? 0 : page) * pitch + W), "r"(page < 0 ? 0 : 4)
                    : "memory");
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-
-  int page = page_of(0);
-  if (tid == 0) {
-    mbar_init(bar(0), 1);
-    mbar_init(bar(1), 1);
-    fence_mbar_init();
-  }
-  if (warp == 0) {
-    tmem_alloc(bar(2), 256);
-    tmem_relinquish();
-  }
-  fetch(0, page);
-  int page_next = page_of(1);
-  // ---- the queries' codes
-  float* sq = reinterpret_cast<float*>(smem + OFF_SQ);
-  auto put = [&](int i, int c, uint2 codes) {                 // 8-code chunk c (0 .. 71) of row i
-    const uint32_t dst = OFF_Q + (c >> 4) * KBOX + i * 128 + ((((c & 15) >> 1) ^ (i & 7)) << 4) + (c & 1) * 8;
-    *reinterpret_cast<uint2*>(smem + dst) = codes;
-  };
-  float srow[2] = {0.f, 0.f};                                 // scales of the rows of ur
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t mr = max_bits(max8(ur[h]));
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) mr = max(mr, __shfl_xor_sync(0xffffffffu, mr, o));
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int j = 4 * h + k;
-      const uint32_t own = max(max_bits(max8(u[j][0])), max_bits(max8(u[j][1])));
-      const float amax = __uint_as_float(max(__reduce_max_sync(0xffffffffu, own), __shfl_sync(0xffffffffu, mr, 8 * k)));
-      float s = __fdiv_rn(amax, 127.f);
-      if (!(s > 0.f && s < INFINITY)) s = 0.f;
-      const float inv = 1.f / s;
-      put(i0 + j, lane, s == 0.f ? make_uint2(0u, 0u) : codes8(u[j][0], s, inv));
-      put(i0 + j, lane + 32, s == 0.f ? make_uint2(0u, 0u) : codes8(u[j][1], s, inv));
-      if (lane == 0) sq[i0 + j] = s;
-      if ((lane >> 3) == k) srow[h] = s;
-    }
-    put(i0 + 4 * h + (lane >> 3), 64 + (lane & 7), srow[h] == 0.f ? make_uint2(0u, 0u) : codes8(ur[h], srow[h], 1.f / srow[h]));
-  }
-  fence_proxy_async_smem();
+  auto tiles_barrier = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+  if (tiles_half && nb > 0) fetch(page_of(tok, nb, 0));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<const uint32_t*>(smem + OFF_BAR + 16);
-  const int quarter = warp & 3, cg = warp >> 2;               // lanes 32 quarter .., heads 32 cg ..
+  const int quarter = warp & 3, cg = (warp >> 2) & 1;         // lanes 32 quarter .., heads 64 cg ..
+  const int row = 32 * quarter + lane;
   constexpr uint32_t idesc = idesc_i8(TILE, H);
+  uint32_t done = 0;                                          // tiles multiplied by this CTA
   bool ok = true;
-  for (int i = 0; i <= n; ++i) {
-    if (i < n) {
-      // every copy of tile i has landed (the only group in flight) and is visible to the MMAs
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncthreads();
-      if (tid == 0) {
-        tc_fence_after();
-        const int b = i & 1;
-        const uint32_t d = tmem + 128 * b;
-#pragma unroll
-        for (int k = 0; k < 18; ++k) {
-          const uint32_t ya = k < 16 ? OFF_Y + (4 * b + (k >> 2)) * KBOX : OFF_YH;
-          const int ko = k < 16 ? 2 * (k & 3) : 4 * b + 2 * (k - 16);
-          mma_i8(d, sw128_desc(sbase + ya, 0, 1024) + ko, sw128_desc(sbase + OFF_Q + (k >> 2) * KBOX, 0, 1024) + 2 * (k & 3),
-                 idesc, k > 0 ? 1u : 0u);
+  for (int b = 0; t < v.total_q; b ^= 1) {
+    const int64_t t_next = t + gridDim.y;
+    PagedToken tok_next;
+    tok_next.seq = -1;
+    tok_next.pos = -1;
+    int nb_next = 0;
+    if (!tiles_half) {
+      // ---- the next token's codes, 16 rows a warp
+      if (t_next < v.total_q) {
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          QueryRows q;
+          const int i0 = 2 * ROWS * (warp - 8) + ROWS * h;
+          q.load(q_abs, q_rope, t_next, i0, lane);
+          q.codes(smem, b ^ 1, i0, lane);
         }
-        mma_commit(bar(b));
+        fence_proxy_async_smem();
       }
-    }
-    float scale = 0.f;
-    const int row = 32 * quarter + lane;
-    if (i > 0) {
-      const int b = (i - 1) & 1;
-      if (cg == 0) scale = *reinterpret_cast<const float*>(smem + row_chunk(row, 4) + 4 * b);
-      // tile i - 1 multiplied: its buffer takes tile i + 1
-      ok = __syncthreads_and(mbar_wait(bar(b), ((i - 1) >> 1) & 1));
-      if (!ok) break;
-      tc_fence_after();
-    }
-    if (i + 1 < n) {
-      fetch(i + 1, page_next);
-      page_next = page_of(i + 2);
-    }
-    if (i > 0) {
-      const int b = (i - 1) & 1;
-      const int g = (first + (i - 1) * stride) * TILE + row;
-      uint32_t d[32];
-      tmem_ld32(tmem + ((uint32_t)(32 * quarter) << 16) + 128 * b + 32 * cg, d);
-      tmem_wait_ld();
-      float mx = -INFINITY;
+    } else {
+      const int n = nb > 0 ? ((nb + TILE - 1) / TILE - first + stride - 1) / stride : 0;
+      const float* sq = reinterpret_cast<const float*>(smem + OFF_SQ) + b * H + 64 * cg;
+      int page_next = n > 1 ? page_of(tok, nb, 1) : -1;
+      for (int i = 0; i < n && ok; ++i, ++done) {
+        // the tile has landed and is visible to the MMAs; the maxima of the tile before are taken
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        fence_proxy_async_smem();
+        tc_fence_before();
+        tiles_barrier();
+        if (tid == 0) {
+          tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < 32; c += 4) {
-        const float4 s4 = *reinterpret_cast<const float4*>(sq + 32 * cg + c);
-        mx = fmaxf(mx, fmaxf(fmaxf((float)(int)d[c] * s4.x, (float)(int)d[c + 1] * s4.y),
-                             fmaxf((float)(int)d[c + 2] * s4.z, (float)(int)d[c + 3] * s4.w)));
-      }
-      float* part = reinterpret_cast<float*>(smem + row_chunk(row, 5));
-      if (cg > 0) part[cg - 1] = mx;
-      tc_fence_before();
-      __syncthreads();
-      if (cg == 0 && g < nb) {
+          for (int k = 0; k < 18; ++k) {
+            const uint32_t q = k < 16 ? OFF_Q + (4 * b + (k >> 2)) * KBOX : OFF_QH;
+            const int qo = k < 16 ? 2 * (k & 3) : 4 * b + 2 * (k - 16);
+            mma_i8(tmem, sw128_desc(sbase + OFF_Y + (k >> 2) * KBOX, 0, 1024) + 2 * (k & 3),
+                   sw128_desc(sbase + q, 0, 1024) + qo, idesc, k > 0 ? 1u : 0u);
+          }
+          mma_commit(bar);
+        }
+        const float scale = *reinterpret_cast<const float*>(smem + row_chunk(row, 4));
+        if (i == 0 && t_next < v.total_q) {
+          tok_next = paged_token(v, t_next);
+          nb_next = blocks_of(tok_next);
+        }
+        const int page_after = i + 2 < n ? page_of(tok, nb, i + 2) : i + 1 == n && nb_next > 0 ? page_of(tok_next, nb_next, 0) : -1;
+        // multiplied, and the scales are read: the buffer takes the next tile (or a wait gave up, for all of them)
+        ok = !bar_sync_or(1, 256, !mbar_wait(bar, done & 1));
+        tc_fence_after();
+        if (!ok) break;
+        if (i + 1 < n) fetch(page_next);
+        else if (nb_next > 0) fetch(page_after);
+        page_next = page_after;
+        float mx = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < 3; ++k) mx = fmaxf(mx, part[k]);
-        scores[t * v.max_pages + g] = mx * scale + 0.f;       // + 0: a -0 ties with a 0
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x[32];
+          tmem_ld32(tmem + ((uint32_t)(32 * quarter) << 16) + 64 * cg + 32 * h, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            const float4 s4 = *reinterpret_cast<const float4*>(sq + 32 * h + c);
+            mx = fmaxf(mx, fmaxf(fmaxf((float)(int)x[c] * s4.x, (float)(int)x[c + 1] * s4.y),
+                                 fmaxf((float)(int)x[c + 2] * s4.z, (float)(int)x[c + 3] * s4.w)));
+          }
+        }
+        float* upper = reinterpret_cast<float*>(smem + row_chunk(row, 5));
+        if (cg == 1) *upper = mx;
+        tc_fence_before();
+        tiles_barrier();
+        const int g = (first + i * stride) * TILE + row;
+        if (cg == 0 && g < nb) scores[t * v.max_pages + g] = fmaxf(mx, *upper) * scale + 0.f;   // + 0: a -0 ties with a 0
+      }
+      if (n == 0 && t_next < v.total_q) {
+        tok_next = paged_token(v, t_next);
+        nb_next = blocks_of(tok_next);
+        if (nb_next > 0) fetch(page_of(tok_next, nb_next, 0));
       }
     }
+    // the codes are written, the tiles multiplied
+    if (!__syncthreads_and(ok)) {
+      if (tid == 0) flag_error(err, DEVERR_TIMEOUT);
+      break;
+    }
+    t = t_next;
+    tok = tok_next;
+    nb = nb_next;
   }
-  if (!ok) {
-    if (tid == 0) flag_error(err, DEVERR_TIMEOUT);
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  tc_fence_before();
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 128);
   }
 }
 
@@ -297,11 +338,12 @@ cudaError_t tc_select_scores(const PagedView& v, const void* q_abs, const void* 
   // per device, so set at every call
   cudaError_t e = cudaFuncSetAttribute(select_score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  // enough CTAs a token to fill the SMs (one CTA each), no more than it can have tiles
+  // one CTA an SM: a token's tiles are split over several where tokens are few, else a CTA takes several tokens
   const int64_t tiles = (v.max_pages + TILE - 1) / TILE;
   int64_t split = num_sms / v.total_q;
   split = split < 1 ? 1 : split > tiles ? tiles : split;
-  select_score_kernel<<<dim3((unsigned)split, (unsigned)v.total_q), kThreads, SMEM_BYTES, st>>>(
+  const int64_t rows = v.total_q < num_sms ? v.total_q : num_sms;
+  select_score_kernel<<<dim3((unsigned)split, (unsigned)rows), kThreads, SMEM_BYTES, st>>>(
       v, (const __nv_bfloat16*)q_abs, (const __nv_bfloat16*)q_rope, (const uint8_t*)summaries,
       (int64_t)summary_pitch(DC, DR), top_k, scores, err);
   note_launch();
