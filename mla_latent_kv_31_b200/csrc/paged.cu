@@ -142,16 +142,15 @@ __global__ void __launch_bounds__(128)
   }
 }
 
-// The scale and one code of a row whose largest magnitude is amax: x / scale to the nearest whole number.
-// A row whose scale is 0, infinite or NaN has scale 0 and codes 0; a NaN element has code 0.
-__device__ __forceinline__ float code_scale(float amax) {
-  const float s = __fdiv_rn(amax, 127.f);
+// The scale and one code of a row: x / scale to the nearest whole number. The largest magnitude is taken over the bits, so
+// that a NaN or an infinity wins: such a row, and one of zeros, has scale 0 and codes 0.
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+__device__ __forceinline__ float code_scale(uint32_t largest) {
+  const float s = __fdiv_rn(__uint_as_float(largest), 127.f);
   return s > 0.f && s < INFINITY ? s : 0.f;
 }
 __device__ __forceinline__ int code_of(float x, float s) {
-  if (!(s > 0.f)) return 0;
-  const float r = rintf(__fdiv_rn(x, s));
-  return r >= 127.f ? 127 : r <= -127.f ? -127 : (int)r;
+  return s > 0.f ? (int)fminf(fmaxf(rintf(__fdiv_rn(x, s)), -127.f), 127.f) : 0;
 }
 
 // Summaries of the pages that the new tokens complete. Block i looks at `group` <= 32 tokens, a lane each; a token that is
@@ -162,7 +161,7 @@ constexpr int SUM_GROUPS = 4;
 template <typename T>
 __global__ void __launch_bounds__(512) summarise_kernel(PagedView v, int group, uint8_t* summaries, int64_t pitch) {
   extern __shared__ double part[];    // [SUM_GROUPS][W]
-  __shared__ float red[32];
+  __shared__ uint32_t largest;
   const int tid = threadIdx.x, W = v.d_c + v.d_r;
   int32_t own = -1;                   // the page that this lane's token completes
   {
@@ -211,17 +210,21 @@ __global__ void __launch_bounds__(512) summarise_kernel(PagedView v, int group, 
 #pragma unroll
       for (int e = 0; e < E; ++e) part[g * W + c * E + e] = sum[e];
     }
+    if (tid == 0) largest = 0;
     __syncthreads();
-    float amax = 0.f;
+    uint32_t own_max = 0;
     for (int c = tid; c < W; c += blockDim.x) {
       double sum = 0.0;
 #pragma unroll
       for (int g = 0; g < SUM_GROUPS; ++g) sum += part[g * W + c];
       const float mean = (float)(sum / v.page);
       reinterpret_cast<float*>(part)[2 * c] = mean;          // in place of group 0's sum
-      amax = fmaxf(amax, fabsf(mean));
+      own_max = max(own_max, magnitude(mean));
     }
-    const float s = code_scale(block_max(amax, red));
+    own_max = __reduce_max_sync(0xffffffffu, own_max);
+    if ((tid & 31) == 0) atomicMax(&largest, own_max);
+    __syncthreads();
+    const float s = code_scale(largest);
     uint8_t* out = summaries + (int64_t)p * pitch;
     for (int c = tid; c < pitch; c += blockDim.x)
       if (c < W) out[c] = (uint8_t)(int8_t)code_of(reinterpret_cast<float*>(part)[2 * c], s);
@@ -357,9 +360,9 @@ __global__ void __launch_bounds__(256)
   const int lane = threadIdx.x & 31, W = v.d_c + v.d_r;
   if (r >= v.total_q * v.n_h || r / v.n_h >= v.cu_q[v.B]) return;
   auto at = [&](int c) { return c < v.d_c ? q_abs[r * v.d_c + c] : q_rope[r * v.d_r + c - v.d_c]; };
-  float amax = 0.f;
-  for (int c = lane; c < W; c += 32) amax = fmaxf(amax, fabsf(at(c)));
-  const float s = code_scale(warp_max(amax));
+  uint32_t largest = 0;
+  for (int c = lane; c < W; c += 32) largest = max(largest, magnitude(at(c)));
+  const float s = code_scale(__reduce_max_sync(0xffffffffu, largest));
   for (int c = lane; c < W; c += 32) codes[r * W + c] = (int8_t)code_of(at(c), s);
   if (lane == 0) scales[r] = s;
 }

@@ -55,31 +55,17 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool zero)
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(zero ? 0 : 16) : "memory");
 }
 
-// The elements of `near` (a bit each) of 8 again, by IEEE division.
-__device__ __noinline__ uint2 codes8_exact(uint4 u, float s, uint32_t near, uint2 codes) {
-  while (near) {
-    const int e = __ffs(near) - 1;
-    near &= near - 1;
-    const uint32_t w = (e >> 1) == 0 ? u.x : (e >> 1) == 1 ? u.y : (e >> 1) == 2 ? u.z : u.w;
-    const float n = rintf(__fdiv_rn(e & 1 ? bf16_hi(w) : bf16_lo(w), s));
-    const uint32_t code = n == n ? (uint32_t)(int)fminf(fmaxf(n, -127.f), 127.f) & 255u : 0u;
-    const int sh = 8 * (e & 3);
-    if (e < 4) codes.x = (codes.x & ~(255u << sh)) | (code << sh);
-    else codes.y = (codes.y & ~(255u << sh)) | (code << sh);
-  }
-  return codes;
-}
 // x / s to the nearest whole number (ties to even) for 8 elements, as an IEEE division gives it: x * (1 / s) is within
-// 3e-5 of the quotient for |x / s| <= 127, so only a value that near to a tie, a NaN or a scale whose reciprocal
-// overflows is divided. (Half of the row's largest magnitude, 63.5, is such a value, and about every second row of
-// bf16 numbers has one.) Adding 1.5 * 2^23 rounds to the nearest even whole number and leaves it, as two's
+// 3e-5 of the quotient for |x / s| <= 127, so only chunks with a value within 1e-4 of a tie (`rare`), or a scale whose
+// reciprocal overflows, are divided (about every second row of bf16 numbers has such a value, half of its
+// largest magnitude at 63.5). Adding 1.5 * 2^23 rounds to the nearest even whole number and leaves it, as two's
 // complement, in the low byte.
-__device__ __forceinline__ uint2 codes8(uint4 u, float s, float inv) {
+__device__ __forceinline__ uint2 codes8(uint4 u, float inv, bool* rare) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
   uint32_t t[8];
   const uint64_t inv2 = f2_pack(inv, inv), magic = f2_pack(12582912.f, 12582912.f), unmagic = f2_pack(-12582912.f, -12582912.f);
   const uint64_t minus = f2_pack(-1.f, -1.f);
-  uint32_t near = inv < INFINITY ? 0u : 255u;
+  float off = 0.f;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const uint64_t r = f2_mul(f2_pack(bf16_lo(w[e]), bf16_hi(w[e])), inv2);
@@ -89,26 +75,28 @@ __device__ __forceinline__ uint2 codes8(uint4 u, float s, float inv) {
     f2_unpack(f2_fma(f2_add(m, unmagic), minus, r), d0, d1);
     t[2 * e] = __float_as_uint(m0);
     t[2 * e + 1] = __float_as_uint(m1);
-    if (!(fabsf(d0) <= 0.4999f)) near |= 1u << (2 * e);
-    if (!(fabsf(d1) <= 0.4999f)) near |= 2u << (2 * e);
+    off = fmaxf(off, fmaxf(fabsf(d0), fabsf(d1)));
   }
-  const uint2 codes = make_uint2(__byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410),
-                                 __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410));
-  return near ? codes8_exact(u, s, near, codes) : codes;
+  *rare = off > 0.4999f;
+  return make_uint2(__byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410));
 }
-// The largest magnitudes of the 8 elements, two at a time in bf16 (NaN is passed over).
-__device__ __forceinline__ __nv_bfloat162 max8(uint4 u) {
-  auto mag = [](uint32_t w) {
-    w &= 0x7fff7fffu;
-    return *reinterpret_cast<__nv_bfloat162*>(&w);
-  };
-  return __hmax2(__hmax2(mag(u.x), mag(u.y)), __hmax2(mag(u.z), mag(u.w)));
+// One code by IEEE division.
+__device__ __forceinline__ uint8_t code_exact(float x, float s) {
+  return (uint8_t)(int)fminf(fmaxf(rintf(__fdiv_rn(x, s)), -127.f), 127.f);
 }
-// ... as the bits of one fp32 value, which order like it; a NaN is 0.
-__device__ __forceinline__ uint32_t max_bits(__nv_bfloat162 m) {
-  return __float_as_uint(fmaxf(fmaxf(__low2float(m), __high2float(m)), 0.f));
+// The largest magnitude of 8 elements as the bits of a bf16, which order like the magnitudes, a NaN above all: the scale
+// of a row with a NaN or an infinity is not finite, and its codes are zeros.
+__device__ __forceinline__ uint32_t max8(uint4 u) {
+  const uint32_t m = __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+  return max(m & 0xffffu, m >> 16);
 }
 
+// Where the 8 codes of chunk c (0 .. 71) of query row i go in buffer b.
+__device__ __forceinline__ uint32_t place(int b, int i, int c) {
+  return (c < 64 ? OFF_Q + (4 * b + (c >> 4)) * KBOX + i * 128 + ((((c & 15) >> 1) ^ (i & 7)) << 4)
+                 : OFF_QH + i * 128 + (((4 * b + ((c & 15) >> 1)) ^ (i & 7)) << 4)) + (c & 1) * 8;
+}
 // Quantises ROWS query rows, the warp's own, of token t into buffer b: loads, then codes. Lane: the chunks of 8 elements
 // lane and lane + 32 of each row, and q^R's chunk lane % 8 of rows lane / 8 and 4 + lane / 8.
 constexpr int ROWS = 8;
@@ -125,34 +113,72 @@ struct QueryRows {
     ur[0] = qr[0];
     ur[1] = qr[32];
   }
-  __device__ __forceinline__ void codes(uint8_t* smem, int b, int i0, int lane) const {
+  __device__ __forceinline__ void codes(uint8_t* smem, const __nv_bfloat16* q_abs, const __nv_bfloat16* q_rope, int64_t t,
+                                        int b, int i0, int lane) const {
     float* sq = reinterpret_cast<float*>(smem + OFF_SQ) + b * H;
-    auto put = [&](int i, int c, uint2 x) {                   // 8-code chunk c (0 .. 71) of row i
-      const uint32_t dst = c < 64 ? OFF_Q + (4 * b + (c >> 4)) * KBOX + i * 128 + ((((c & 15) >> 1) ^ (i & 7)) << 4)
-                                  : OFF_QH + i * 128 + (((4 * b + ((c & 15) >> 1)) ^ (i & 7)) << 4);
-      *reinterpret_cast<uint2*>(smem + dst + (c & 1) * 8) = x;
-    };
-    float srow[2] = {0.f, 0.f};                               // scales of the rows of ur
+    auto put = [&](int i, int c, uint2 x) { *reinterpret_cast<uint2*>(smem + place(b, i, c)) = x; };
+    // the rows' largest magnitudes, all at once
+    uint32_t big[ROWS];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t mr = max_bits(max8(ur[h]));
+      uint32_t mr = max8(ur[h]);
 #pragma unroll
       for (int o = 1; o < 8; o <<= 1) mr = max(mr, __shfl_xor_sync(0xffffffffu, mr, o));
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int j = 4 * h + k;
-        const uint32_t own = max(max_bits(max8(u[j][0])), max_bits(max8(u[j][1])));
-        const float amax = __uint_as_float(max(__reduce_max_sync(0xffffffffu, own), __shfl_sync(0xffffffffu, mr, 8 * k)));
-        float s = __fdiv_rn(amax, 127.f);
-        if (!(s > 0.f && s < INFINITY)) s = 0.f;
-        const float inv = 1.f / s;
-        put(i0 + j, lane, s == 0.f ? make_uint2(0u, 0u) : codes8(u[j][0], s, inv));
-        put(i0 + j, lane + 32, s == 0.f ? make_uint2(0u, 0u) : codes8(u[j][1], s, inv));
-        if (lane == 0) sq[i0 + j] = s;
-        if ((lane >> 3) == k) srow[h] = s;
+        big[j] = max(__reduce_max_sync(0xffffffffu, max(max8(u[j][0]), max8(u[j][1]))), __shfl_sync(0xffffffffu, mr, 8 * k));
       }
-      put(i0 + 4 * h + (lane >> 3), 64 + (lane & 7),
-          srow[h] == 0.f ? make_uint2(0u, 0u) : codes8(ur[h], srow[h], 1.f / srow[h]));
+    }
+    float s[ROWS], inv[ROWS];
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      s[j] = __fdiv_rn(__uint_as_float(big[j] << 16), 127.f);
+      if (!(s[j] > 0.f && s[j] < INFINITY)) s[j] = 0.f;
+      inv[j] = 1.f / s[j];
+      if (lane == 0) sq[i0 + j] = s[j];
+    }
+    // chunk k of row j: bit 2 j + k; q^R's chunk of half h: bit 16 + h
+    uint32_t again = 0;
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        bool rare;
+        const uint2 x = codes8(u[j][k], inv[j], &rare);
+        put(i0 + j, lane + 32 * k, s[j] == 0.f ? make_uint2(0u, 0u) : x);
+        if (rare || !(inv[j] < INFINITY)) again |= 1u << (2 * j + k);
+      }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float sr = s[4 * h], ir = inv[4 * h];
+#pragma unroll
+      for (int k = 1; k < 4; ++k) {
+        sr = (lane >> 3) == k ? s[4 * h + k] : sr;
+        ir = (lane >> 3) == k ? inv[4 * h + k] : ir;
+      }
+      bool rare;
+      const uint2 x = codes8(ur[h], ir, &rare);
+      put(i0 + 4 * h + (lane >> 3), 64 + (lane & 7), sr == 0.f ? make_uint2(0u, 0u) : x);
+      if (rare || !(ir < INFINITY)) again |= 1u << (16 + h);
+    }
+    __syncwarp();
+    // the rare chunks: their elements near a tie once more, from the loads' cache
+    while (again) {
+      const int bit = __ffs(again) - 1;
+      again &= again - 1;
+      const int i = bit < 16 ? i0 + (bit >> 1) : i0 + 4 * (bit - 16) + (lane >> 3), c = bit < 16 ? lane + 32 * (bit & 1) : 64 + (lane & 7);
+      const float si = sq[i];
+      if (si == 0.f) continue;
+      const __nv_bfloat16* src = c < 64 ? q_abs + (t * H + i) * DC + 8 * c : q_rope + (t * H + i) * DR + 8 * (c - 64);
+      const uint4 v4 = *reinterpret_cast<const uint4*>(src);
+      const uint32_t w[4] = {v4.x, v4.y, v4.z, v4.w};
+      uint8_t* dst = smem + place(b, i, c);
+#pragma unroll 1
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t we = e < 4 ? (e < 2 ? w[0] : w[1]) : (e < 6 ? w[2] : w[3]);
+        dst[e] = code_exact(e & 1 ? bf16_hi(we) : bf16_lo(we), si);
+      }
     }
   }
 };
@@ -187,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_alloc(bar + 16, 128);
       tmem_relinquish();
     }
-    q.codes(smem, 0, ROWS * warp, lane);
+    q.codes(smem, q_abs, q_rope, t, 0, ROWS * warp, lane);
     fence_proxy_async_smem();
   }
   PagedToken tok = paged_token(v, t);
@@ -249,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           QueryRows q;
           const int i0 = 2 * ROWS * (warp - 8) + ROWS * h;
           q.load(q_abs, q_rope, t_next, i0, lane);
-          q.codes(smem, b ^ 1, i0, lane);
+          q.codes(smem, q_abs, q_rope, t_next, b ^ 1, i0, lane);
         }
         fence_proxy_async_smem();
       }

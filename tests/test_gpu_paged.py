@@ -343,6 +343,43 @@ def test_select_ties_and_empty_summaries(mods, dtype):
     assert torch.equal(got.cpu(), c.select(means, 20, 1, 2))
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_select_queries_out_of_range(mods, dtype):
+    """Heads of zeros, of tiny and huge values, with an infinity and with a NaN: scale 0 where none is finite."""
+    m = mods[dtype]
+    c = Case(dtype, 16, [16 * 200], [1], seed=31)
+    means = c.normal(c.num_pages, c.W) * 0.3
+    d = c.dims
+    c.q *= 1e-3
+    c.q[0, 0] *= 1e33
+    c.q[0, 1] = float("inf")
+    c.q[0, 2, 5] = float("nan")
+    c.q[0, 3] = 0
+    c.q[0, 0, 7] = -float("inf") if d.n_h > 100 else c.q[0, 0, 7]
+    c.q = c.q.to(DT[dtype]).double()
+    for tiny in (1.0, 1e-37):
+        c.q = (c.q * tiny).to(DT[dtype]).double()
+        got = m.paged_select(c.batch(), c.q_abs, c.q_rope, c.summaries(means).cuda(), 20, 1, 2)
+        ok(m)
+        assert torch.equal(got.cpu(), c.select(means, 20, 1, 2)), tiny
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_select_half_of_the_largest(mods, dtype):
+    """Elements at every half step of the scale: the ties of the rounding, one way or the other by the scale's own."""
+    m = mods[dtype]
+    c = Case(dtype, 16, [16 * 300], [2], seed=32)
+    top = torch.rand(2, c.dims.n_h, 1, generator=c.g, dtype=torch.float64) + 0.5
+    c.q = (top * (torch.randint(-127, 128, c.q.shape, generator=c.g) + 0.5) / 127).to(DT[dtype]).double()
+    c.q[..., 0] = top[..., 0].to(DT[dtype]).double()
+    c.q[..., 1] = -c.q[..., 0] / 2
+    c.q[..., -1] = c.q[..., 0] / 2
+    means = c.normal(c.num_pages, c.W)
+    got = m.paged_select(c.batch(), c.q_abs, c.q_rope, c.summaries(means).cuda(), 33, 0, 1)
+    ok(m)
+    assert torch.equal(got.cpu(), c.select(means, 33, 0, 1))
+
+
 # ---- together -----------------------------------------------------------------------------------------------
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_a_prompt_in_chunks_then_decode_steps(mods, dtype):
