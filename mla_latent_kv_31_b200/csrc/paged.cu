@@ -557,7 +557,7 @@ cudaError_t paged_attention_simt(const PagedView& v, const void* q_abs, const vo
 
 size_t paged_select_bytes(bool bf16, int32_t n_h, int32_t d_c, int32_t d_r, int64_t total_q, int64_t max_pages) {
   const size_t rows = (size_t)total_q * n_h, scores = align1k((size_t)total_q * max_pages * 4);
-  return bf16 ? scores : scores + align1k(rows * (d_c + d_r)) + align1k(rows * 4);
+  return bf16 ? tc_select_bytes(total_q, max_pages) : scores + align1k(rows * (d_c + d_r)) + align1k(rows * 4);
 }
 
 cudaError_t paged_select(const PagedView& v, bool bf16, const void* q_abs, const void* q_rope, const void* summaries,
@@ -566,7 +566,7 @@ cudaError_t paged_select(const PagedView& v, bool bf16, const void* q_abs, const
   float* scores = (float*)ws;
   cudaError_t e;
   if (bf16) {
-    if ((e = tc_select_scores(v, q_abs, q_rope, summaries, top_k, scores, num_sms, err, st)) != cudaSuccess) return e;
+    if ((e = tc_select_scores(v, q_abs, q_rope, summaries, top_k, ws, num_sms, err, st)) != cudaSuccess) return e;
   } else {
     const size_t rows = (size_t)v.total_q * v.n_h, W = (size_t)v.d_c + v.d_r;
     int8_t* codes = (int8_t*)ws + align1k((size_t)v.total_q * v.max_pages * 4);

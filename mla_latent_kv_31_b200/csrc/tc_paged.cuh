@@ -14,8 +14,10 @@ cudaError_t tc_paged_attention(const PagedView& v, const void* q_abs, const void
                                int32_t top_k, float scale, void* o_lat, float* lse, void* ws, int num_sms, uint32_t* err,
                                cudaStream_t st);
 
-// Scores [T, max_pages] of the blocks that each new token sees, for the tokens with more than top_k of them.
+// Scores [T, max_pages] fp32 (at the start of ws) of the blocks that each new token sees, for the tokens with more than
+// top_k of them; ws: tc_select_bytes().
+size_t tc_select_bytes(int64_t total_q, int64_t max_pages);
 cudaError_t tc_select_scores(const PagedView& v, const void* q_abs, const void* q_rope, const void* summaries,
-                             int32_t top_k, float* scores, int num_sms, uint32_t* err, cudaStream_t st);
+                             int32_t top_k, void* ws, int num_sms, uint32_t* err, cudaStream_t st);
 
 }  // namespace mla

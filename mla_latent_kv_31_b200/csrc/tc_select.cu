@@ -2,17 +2,21 @@
 // block g, max_i s_i (x_i . y_g) with int8 codes x_i of the 128 query rows [q~_i | q^R_i] and y_g of the block's
 // summary, times the summary's scale. The products are whole numbers (kind::i8, int32 accumulation): exact.
 //
-// A CTA takes tokens t, t + gridDim.y, ... and of each every gridDim.x-th tile of 128 blocks. Half of its warps take the
-// token's tiles: they gather 128 summary rows (cp.async; the rows of a tile lie anywhere) and multiply, M = 128 blocks,
-// N = 128 heads, K = 576 in 18 MMAs of K = 32; with the blocks on the lanes the maximum over the heads stays in a
-// thread, and it is taken while the next tile is fetched. The other half quantise the next token's queries into
-// the other of two buffers meanwhile (the first token's by all), so queries are read from HBM once per CTA.
-// Bounds: a tile takes about 2.3 us, of which the gather's latency is 1.6; a token's codes take 5 us. With one token
-// a CTA the chain lookup - queries - codes - tile - score.
+// Two kernels. select_codes_kernel quantises the query rows, a warp eight rows (their bytes bound it). In
+// select_score_kernel a CTA keeps one tile of 128 blocks of a sequence in shared memory (gathered by cp.async: its rows lie
+// anywhere) and runs over the sequence's tokens, whose codes stream in by TMA (80 KB each): M = 128 blocks, N = 128
+// heads, K = 576 in 18 MMAs of K = 32. With the blocks on the lanes the maximum over the heads stays in a thread.
+// The products bound it: kind::i8 runs an M128 N128 K32 MMA in 128 cycles (half of the rate of fp8), 2304 a token and
+// tile; 512 tokens over 2048 blocks take 100 us, 74 % of the tensor pipe's time (70 us), the conversions of the sums to
+// fp32 61 % of the XU's. 512 tokens over 512 blocks: codes 20-30 us (110 MB), scores 35, choice 16; 80 in one call.
+// (Quantising inside the scoring kernel, a token's codes kept and the tiles streamed past, took 94 us there and 172
+// against 134 for four chunks of 512 tokens: 5 us of arithmetic a token, and a gather's latency for every tile.)
 #include <cuda_bf16.h>
+#include <string.h>
 
 #include "paged.cuh"
 #include "sm100.cuh"
+#include "tc_gemm.cuh"
 #include "tc_paged.cuh"
 
 namespace mla {
@@ -22,21 +26,19 @@ using namespace sm100;
 
 constexpr int H = 128, DC = 512, DR = 64, W = DC + DR;
 constexpr int TILE = 128;                       // blocks per tile
-constexpr int kThreads = 512;                   // 8 warps for the tiles, 8 for the next token's codes
-constexpr uint32_t KBOX = 128 * 128;            // [128 rows x 128 codes], 128-byte swizzle
-// A row is 4.5 boxes wide: the two query buffers share a ninth box (codes 512 .. 575 in its left or right half).
-constexpr uint32_t OFF_Q = 0;                                  // 2 x 4 boxes, then the shared one
-constexpr uint32_t OFF_QH = OFF_Q + 8 * KBOX;
-constexpr uint32_t OFF_Y = OFF_QH + KBOX;                      // 5 boxes
-constexpr uint32_t OFF_SQ = OFF_Y + 5 * KBOX;                  // [2][128] scales of the queries
-constexpr uint32_t OFF_BAR = OFF_SQ + 2 * H * 4;               // a barrier, TMEM address
-constexpr uint32_t SMEM_BYTES = OFF_BAR + 32 + 1024;
+constexpr int kThreads = 384;                   // warp 0: TMA, warp 1: MMAs, warps 4-11: maxima; all: the gather
+constexpr int kBoxes = 5;                       // [128 rows x 128 codes] boxes of a row (the last one half full)
+constexpr int RING = 8;                         // boxes of query codes in flight
+constexpr uint32_t KBOX = 128 * 128;            // 128-byte swizzle
+constexpr uint32_t OFF_Y = 0;
+constexpr uint32_t OFF_RING = OFF_Y + kBoxes * KBOX;
+constexpr uint32_t OFF_SY = OFF_RING + RING * KBOX;            // [128] scales of the summaries
+constexpr uint32_t OFF_SQ = OFF_SY + TILE * 4;                 // [2][128] scales of the queries
+constexpr uint32_t OFF_PART = OFF_SQ + 2 * H * 4;              // [128] maxima over the upper 64 heads
+constexpr uint32_t OFF_BAR = OFF_PART + TILE * 4;
+enum : int { B_FULL = 0, B_EMPTY = B_FULL + RING, B_DFULL = B_EMPTY + RING, B_DFREE = B_DFULL + 2, NBAR = B_DFREE + 2 };
+constexpr uint32_t SMEM_BYTES = OFF_BAR + 8 * NBAR + 16 + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
-// The right half of the summaries' fifth box is free: chunk c (4 .. 7) of row r holds 16 bytes of what goes with block r
-// of a tile: the summary's scale (4), the maximum over the upper 64 heads (5).
-__device__ __forceinline__ uint32_t row_chunk(int r, int c) {
-  return OFF_Y + 4 * KBOX + r * 128 + ((c ^ (r & 7)) << 4);
-}
 
 // kind::i8: signed 8-bit A and B, 32-bit integer D, both K-major.
 constexpr uint32_t idesc_i8(int M, int N) {
@@ -92,288 +94,314 @@ __device__ __forceinline__ uint32_t max8(uint4 u) {
   return max(m & 0xffffu, m >> 16);
 }
 
-// Where the 8 codes of chunk c (0 .. 71) of query row i go in buffer b.
-__device__ __forceinline__ uint32_t place(int b, int i, int c) {
-  return (c < 64 ? OFF_Q + (4 * b + (c >> 4)) * KBOX + i * 128 + ((((c & 15) >> 1) ^ (i & 7)) << 4)
-                 : OFF_QH + i * 128 + (((4 * b + ((c & 15) >> 1)) ^ (i & 7)) << 4)) + (c & 1) * 8;
-}
-// Quantises ROWS query rows, the warp's own, of token t into buffer b: loads, then codes. Lane: the chunks of 8 elements
-// lane and lane + 32 of each row, and q^R's chunk lane % 8 of rows lane / 8 and 4 + lane / 8.
-constexpr int ROWS = 8;
-struct QueryRows {
+// Codes [T * 128][576] and scales [T * 128] of the query rows, 8 rows a warp, of the tokens with more than top_k blocks
+// (2048 tokens with fewer: 26 us where quantising them all took 134). Four CTAs an SM hide the look at the token (3 us
+// of 80 against three CTAs; the 8 bytes that spill cost less). Lane: the chunks of 8 elements lane and
+// lane + 32 of each row, and q^R's chunk lane % 8 of rows lane / 8 and 4 + lane / 8.
+constexpr int ROWS = 8, CODE_WARPS = 4;
+__global__ void __launch_bounds__(32 * CODE_WARPS, 4)
+    select_codes_kernel(PagedView v, const __nv_bfloat16* q_abs, const __nv_bfloat16* q_rope, int32_t top_k, int8_t* codes,
+                        float* scales, uint32_t* err) {
+  const int lane = threadIdx.x & 31;
+  const int64_t r0 = ((int64_t)blockIdx.x * CODE_WARPS + (threadIdx.x >> 5)) * ROWS;
+  let_next_start();
+  if (blockIdx.x == 0) paged_check(v, err);
+  if (paged_token(v, r0 / H).pos < (int64_t)top_k * v.page) return;      // every block that it sees is chosen
   uint4 u[ROWS][2], ur[2];
-  __device__ __forceinline__ void load(const __nv_bfloat16* q_abs, const __nv_bfloat16* q_rope, int64_t t, int i0, int lane) {
-    const uint4* qa = reinterpret_cast<const uint4*>(q_abs + (t * H + i0) * DC) + lane;
-    const uint4* qr = reinterpret_cast<const uint4*>(q_rope + (t * H + i0) * DR) + lane;
+  const uint4* qa = reinterpret_cast<const uint4*>(q_abs + r0 * DC) + lane;
+  const uint4* qr = reinterpret_cast<const uint4*>(q_rope + r0 * DR) + lane;
 #pragma unroll
-    for (int j = 0; j < ROWS; ++j) {
-      u[j][0] = qa[j * (DC / 8)];
-      u[j][1] = qa[j * (DC / 8) + 32];
-    }
-    ur[0] = qr[0];
-    ur[1] = qr[32];
+  for (int j = 0; j < ROWS; ++j) {
+    u[j][0] = qa[j * (DC / 8)];
+    u[j][1] = qa[j * (DC / 8) + 32];
   }
-  __device__ __forceinline__ void codes(uint8_t* smem, const __nv_bfloat16* q_abs, const __nv_bfloat16* q_rope, int64_t t,
-                                        int b, int i0, int lane) const {
-    float* sq = reinterpret_cast<float*>(smem + OFF_SQ) + b * H;
-    auto put = [&](int i, int c, uint2 x) { *reinterpret_cast<uint2*>(smem + place(b, i, c)) = x; };
-    // the rows' largest magnitudes, all at once
-    uint32_t big[ROWS];
+  ur[0] = qr[0];
+  ur[1] = qr[32];
+  auto put = [&](int j, int c, uint2 x) { *reinterpret_cast<uint2*>(codes + (r0 + j) * W + 8 * c) = x; };
+  // the rows' largest magnitudes and scales, all at once
+  uint32_t big[ROWS];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t mr = max8(ur[h]);
+  for (int h = 0; h < 2; ++h) {
+    uint32_t mr = max8(ur[h]);
 #pragma unroll
-      for (int o = 1; o < 8; o <<= 1) mr = max(mr, __shfl_xor_sync(0xffffffffu, mr, o));
+    for (int o = 1; o < 8; o <<= 1) mr = max(mr, __shfl_xor_sync(0xffffffffu, mr, o));
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int j = 4 * h + k;
-        big[j] = max(__reduce_max_sync(0xffffffffu, max(max8(u[j][0]), max8(u[j][1]))), __shfl_sync(0xffffffffu, mr, 8 * k));
-      }
+    for (int k = 0; k < 4; ++k) {
+      const int j = 4 * h + k;
+      big[j] = max(__reduce_max_sync(0xffffffffu, max(max8(u[j][0]), max8(u[j][1]))), __shfl_sync(0xffffffffu, mr, 8 * k));
     }
-    float s[ROWS], inv[ROWS];
+  }
+  float s[ROWS], inv[ROWS];
 #pragma unroll
-    for (int j = 0; j < ROWS; ++j) {
-      s[j] = __fdiv_rn(__uint_as_float(big[j] << 16), 127.f);
-      if (!(s[j] > 0.f && s[j] < INFINITY)) s[j] = 0.f;
-      inv[j] = 1.f / s[j];
-      if (lane == 0) sq[i0 + j] = s[j];
-    }
-    // chunk k of row j: bit 2 j + k; q^R's chunk of half h: bit 16 + h
-    uint32_t again = 0;
+  for (int j = 0; j < ROWS; ++j) {
+    s[j] = __fdiv_rn(__uint_as_float(big[j] << 16), 127.f);
+    if (!(s[j] > 0.f && s[j] < INFINITY)) s[j] = 0.f;
+    inv[j] = 1.f / s[j];
+    if (lane == 0) scales[r0 + j] = s[j];
+  }
+  // chunk k of row j: bit 2 j + k; q^R's chunk of half h: bit 16 + h
+  uint32_t again = 0;
 #pragma unroll
-    for (int j = 0; j < ROWS; ++j)
+  for (int j = 0; j < ROWS; ++j)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        bool rare;
-        const uint2 x = codes8(u[j][k], inv[j], &rare);
-        put(i0 + j, lane + 32 * k, s[j] == 0.f ? make_uint2(0u, 0u) : x);
-        if (rare || !(inv[j] < INFINITY)) again |= 1u << (2 * j + k);
-      }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float sr = s[4 * h], ir = inv[4 * h];
-#pragma unroll
-      for (int k = 1; k < 4; ++k) {
-        sr = (lane >> 3) == k ? s[4 * h + k] : sr;
-        ir = (lane >> 3) == k ? inv[4 * h + k] : ir;
-      }
+    for (int k = 0; k < 2; ++k) {
       bool rare;
-      const uint2 x = codes8(ur[h], ir, &rare);
-      put(i0 + 4 * h + (lane >> 3), 64 + (lane & 7), sr == 0.f ? make_uint2(0u, 0u) : x);
-      if (rare || !(ir < INFINITY)) again |= 1u << (16 + h);
+      const uint2 x = codes8(u[j][k], inv[j], &rare);
+      put(j, lane + 32 * k, s[j] == 0.f ? make_uint2(0u, 0u) : x);
+      if (s[j] != 0.f && (rare || !(inv[j] < INFINITY))) again |= 1u << (2 * j + k);
     }
-    __syncwarp();
-    // the rare chunks: their elements near a tie once more, from the loads' cache
-    while (again) {
-      const int bit = __ffs(again) - 1;
-      again &= again - 1;
-      const int i = bit < 16 ? i0 + (bit >> 1) : i0 + 4 * (bit - 16) + (lane >> 3), c = bit < 16 ? lane + 32 * (bit & 1) : 64 + (lane & 7);
-      const float si = sq[i];
-      if (si == 0.f) continue;
-      const __nv_bfloat16* src = c < 64 ? q_abs + (t * H + i) * DC + 8 * c : q_rope + (t * H + i) * DR + 8 * (c - 64);
-      const uint4 v4 = *reinterpret_cast<const uint4*>(src);
-      const uint32_t w[4] = {v4.x, v4.y, v4.z, v4.w};
-      uint8_t* dst = smem + place(b, i, c);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float sr = s[4 * h], ir = inv[4 * h];
+#pragma unroll
+    for (int k = 1; k < 4; ++k) {
+      sr = (lane >> 3) == k ? s[4 * h + k] : sr;
+      ir = (lane >> 3) == k ? inv[4 * h + k] : ir;
+    }
+    bool rare;
+    const uint2 x = codes8(ur[h], ir, &rare);
+    put(4 * h + (lane >> 3), 64 + (lane & 7), sr == 0.f ? make_uint2(0u, 0u) : x);
+    if (sr != 0.f && (rare || !(ir < INFINITY))) again |= 1u << (16 + h);
+  }
+  // the rare chunks by division
+  while (again) {
+    const int bit = __ffs(again) - 1;
+    again &= again - 1;
+    const int j = bit < 16 ? bit >> 1 : 4 * (bit - 16) + (lane >> 3), c = bit < 16 ? lane + 32 * (bit & 1) : 64 + (lane & 7);
+    const __nv_bfloat16* src = c < 64 ? q_abs + (r0 + j) * DC + 8 * c : q_rope + (r0 + j) * DR + 8 * (c - 64);
+    const uint4 x = *reinterpret_cast<const uint4*>(src);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float sj = s[0];
+#pragma unroll
+    for (int k = 1; k < ROWS; ++k) sj = j == k ? s[k] : sj;
+    uint8_t* dst = reinterpret_cast<uint8_t*>(codes) + (r0 + j) * W + 8 * c;
 #pragma unroll 1
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t we = e < 4 ? (e < 2 ? w[0] : w[1]) : (e < 6 ? w[2] : w[3]);
-        dst[e] = code_exact(e & 1 ? bf16_hi(we) : bf16_lo(we), si);
-      }
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t we = e < 4 ? (e < 2 ? w[0] : w[1]) : (e < 6 ? w[2] : w[3]);
+      dst[e] = code_exact(e & 1 ? bf16_hi(we) : bf16_lo(we), sj);
     }
   }
+}
+
+struct ScoreParams {
+  CUtensorMap qmap;           // codes as [T * 128, 576] bytes, box {128, 128}
+  PagedView v;
+  const float* scales;        // [T * 128]
+  const uint8_t* summaries;
+  int64_t pitch;
+  int32_t top_k, group;       // tokens per CTA
+  float* scores;              // [T, max_pages]
+  uint32_t* err;
 };
 
-__global__ void __launch_bounds__(kThreads, 1)
-    select_score_kernel(PagedView v, const __nv_bfloat16* q_abs, const __nv_bfloat16* q_rope, const uint8_t* summaries,
-                        int64_t pitch, int32_t top_k, float* scores, uint32_t* err) {
+__global__ void __launch_bounds__(kThreads, 1) select_score_kernel(const __grid_constant__ ScoreParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t sbase = smem_addr(smem), bar = sbase + OFF_BAR;
+  const uint32_t sbase = smem_addr(smem);
+  const PagedView& v = p.v;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool tiles_half = warp < 8;
-  const int stride = gridDim.x, first = blockIdx.x;
-  int64_t t = blockIdx.y;
-  let_next_start();
-
-  // blocks of a token, 0 when there is nothing to score for this CTA
-  auto blocks_of = [&](const PagedToken& k) -> int {
-    const int nb = k.pos < 0 ? 0 : (int)(k.pos / v.page) + 1;
-    return nb > top_k && first * TILE < nb ? nb : 0;
-  };
-  {
-    // the first token: all loads are in flight while it is looked up
-    QueryRows q;
-    q.load(q_abs, q_rope, t, ROWS * warp, lane);
-    if (blockIdx.x == 0 && t == 0) paged_check(v, err);
-    if (tid == 0) {
-      mbar_init(bar, 1);
-      fence_mbar_init();
-    }
-    if (warp == 0) {
-      tmem_alloc(bar + 16, 128);
-      tmem_relinquish();
-    }
-    q.codes(smem, q_abs, q_rope, t, 0, ROWS * warp, lane);
-    fence_proxy_async_smem();
+  const int tile = blockIdx.x;
+  auto bar = [&](int i) { return sbase + OFF_BAR + 8u * (uint32_t)i; };
+  const uint32_t tmem_slot = bar(NBAR);
+  if (tid == 0) {
+    for (int i = 0; i < NBAR; ++i) mbar_init(bar(i), i >= B_DFREE ? 8 : 1);
+    fence_mbar_init();
+    prefetch_tmap(&p.qmap);
   }
-  PagedToken tok = paged_token(v, t);
-  int nb = blocks_of(tok);
-  // The page of row 16 warp + lane % 16 of tile i of a token, -1 for none.
-  auto page_of = [&](const PagedToken& k, int n_blocks, int i) -> int {
-    const int g = (first + i * stride) * TILE + 16 * warp + (lane & 15);
-    if (g >= n_blocks) return -1;
-    const int p = v.table[(int64_t)k.seq * v.stride + g];
-    if (p < 0 || p >= v.num_pages) {
-      flag_error(err, DEVERR_PAGE);
-      return -1;
-    }
-    return p;
-  };
-  // A tile's summary rows, 16 a warp: the first 512 bytes of a row by 32 lanes (contiguous: four times fewer L1 requests
-  // than a few lanes a row), then the last 64 of eight rows at a time, then the scales.
-  auto fetch = [&](int page) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int p = __shfl_sync(0xffffffffu, page, j), r = 16 * warp + j;
-      copy16(sbase + OFF_Y + (lane >> 3) * KBOX + r * 128 + (((lane & 7) ^ (j & 7)) << 4),
-             summaries + (int64_t)(p < 0 ? 0 : p) * pitch + 16 * lane, p < 0);
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int j = 8 * h + (lane >> 2), p = __shfl_sync(0xffffffffu, page, j), r = 16 * warp + j, c = lane & 3;
-      copy16(sbase + OFF_Y + 4 * KBOX + r * 128 + ((c ^ (j & 7)) << 4),
-             summaries + (int64_t)(p < 0 ? 0 : p) * pitch + 512 + 16 * c, p < 0);
-    }
-    if (lane < 16)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(sbase + row_chunk(16 * warp + lane, 4)),
-                   "l"(summaries + (int64_t)(page < 0 ? 0 : page) * pitch + W), "r"(page < 0 ? 0 : 4)
-                   : "memory");
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  auto tiles_barrier = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
-  if (tiles_half && nb > 0) fetch(page_of(tok, nb, 0));
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, 256);
+    tmem_relinquish();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<const uint32_t*>(smem + OFF_BAR + 16);
-  const int quarter = warp & 3, cg = (warp >> 2) & 1;         // lanes 32 quarter .., heads 64 cg ..
+  const uint32_t tmem = *reinterpret_cast<const uint32_t*>(smem + OFF_BAR + 8 * NBAR);
+  let_next_start();
+
+  float* sy = reinterpret_cast<float*>(smem + OFF_SY);
+  const int quarter = warp & 3, cg = warp >= 8 ? 1 : 0;       // lanes 32 quarter .., heads 64 cg .. (warps 4-11)
   const int row = 32 * quarter + lane;
-  constexpr uint32_t idesc = idesc_i8(TILE, H);
-  uint32_t done = 0;                                          // tiles multiplied by this CTA
-  bool ok = true;
-  for (int b = 0; t < v.total_q; b ^= 1) {
-    const int64_t t_next = t + gridDim.y;
-    PagedToken tok_next;
-    tok_next.seq = -1;
-    tok_next.pos = -1;
-    int nb_next = 0;
-    if (!tiles_half) {
-      // ---- the next token's codes, 16 rows a warp
-      if (t_next < v.total_q) {
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          QueryRows q;
-          const int i0 = 2 * ROWS * (warp - 8) + ROWS * h;
-          q.load(q_abs, q_rope, t_next, i0, lane);
-          q.codes(smem, q_abs, q_rope, t_next, b ^ 1, i0, lane);
+  bool ok = true, waited = false;
+  uint32_t n = 0, done = 0;                                   // ring boxes and tokens so far, the same in every role
+  const int64_t t_end = min((int64_t)(blockIdx.y + 1) * p.group, v.total_q);
+  for (int64_t t = (int64_t)blockIdx.y * p.group; t < t_end;) {
+    // a run: this CTA's tokens of one sequence, from the first with more than top_k blocks, some of them in this tile
+    const PagedToken tok = paged_token(v, t);
+    if (tok.seq < 0) break;
+    const int64_t stop = tok.pos < 0 ? t + 1 : min(t_end, min(v.cu_q[tok.seq + 1], v.total_q));
+    const int64_t need = (int64_t)max(p.top_k, tile * TILE) * v.page;      // the smallest position that is scored here
+    const int64_t from = tok.pos < 0 ? stop : t + max((int64_t)0, need - tok.pos);
+    const int64_t pos_from = tok.pos + (from - t);
+    t = stop;
+    if (from >= stop) continue;
+    const int nb = (int)((pos_from + (stop - 1 - from)) / v.page) + 1;     // blocks of the run's last token
+    // ---- the tile's summary rows: the first 512 bytes of a row by 32 lanes, then the last 64 of eight rows at a time,
+    // then the scales; rows behind the last block and of pages outside the pool are zeros
+    for (int r0 = 16 * warp; r0 < TILE; r0 += 16 * (kThreads / 32)) {
+      const int g = tile * TILE + r0 + (lane & 15);
+      int page = -1;
+      if (g < nb) {
+        page = v.table[(int64_t)tok.seq * v.stride + g];
+        if (page < 0 || page >= v.num_pages) {
+          flag_error(p.err, DEVERR_PAGE);
+          page = -1;
         }
-        fence_proxy_async_smem();
       }
-    } else {
-      const int n = nb > 0 ? ((nb + TILE - 1) / TILE - first + stride - 1) / stride : 0;
-      const float* sq = reinterpret_cast<const float*>(smem + OFF_SQ) + b * H + 64 * cg;
-      int page_next = n > 1 ? page_of(tok, nb, 1) : -1;
-      for (int i = 0; i < n && ok; ++i, ++done) {
-        // the tile has landed and is visible to the MMAs; the maxima of the tile before are taken
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        fence_proxy_async_smem();
-        tc_fence_before();
-        tiles_barrier();
-        if (tid == 0) {
-          tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < 18; ++k) {
-            const uint32_t q = k < 16 ? OFF_Q + (4 * b + (k >> 2)) * KBOX : OFF_QH;
-            const int qo = k < 16 ? 2 * (k & 3) : 4 * b + 2 * (k - 16);
-            mma_i8(tmem, sw128_desc(sbase + OFF_Y + (k >> 2) * KBOX, 0, 1024) + 2 * (k & 3),
-                   sw128_desc(sbase + q, 0, 1024) + qo, idesc, k > 0 ? 1u : 0u);
+      for (int j = 0; j < 16; ++j) {
+        const int q = __shfl_sync(0xffffffffu, page, j);
+        copy16(sbase + OFF_Y + (lane >> 3) * KBOX + (r0 + j) * 128 + (((lane & 7) ^ (j & 7)) << 4),
+               p.summaries + (int64_t)(q < 0 ? 0 : q) * p.pitch + 16 * lane, q < 0);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int j = 8 * h + (lane >> 2), q = __shfl_sync(0xffffffffu, page, j), c = lane & 3;
+        copy16(sbase + OFF_Y + 4 * KBOX + (r0 + j) * 128 + ((c ^ (j & 7)) << 4),
+               p.summaries + (int64_t)(q < 0 ? 0 : q) * p.pitch + 512 + 16 * c, q < 0);
+      }
+      if (lane < 16) sy[r0 + lane] = page < 0 ? 0.f : *reinterpret_cast<const float*>(p.summaries + (int64_t)page * p.pitch + W);
+    }
+    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+    fence_proxy_async_smem();
+    if (!waited) wait_for_previous();                         // the codes
+    waited = true;
+    __syncthreads();
+    const int cnt = (int)(stop - from);
+    if (warp == 0) {
+      // ---- codes
+      for (int k = 0; ok && k < cnt; ++k)
+        for (int e = 0; e < kBoxes; ++e, ++n) {
+          const uint32_t slot = n % RING;
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(B_EMPTY + slot), ((n / RING) & 1) ^ 1)) != 0;
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_expect_tx(bar(B_FULL + slot), KBOX);
+            tma_load_2d(sbase + OFF_RING + slot * KBOX, &p.qmap, 128 * e, (int32_t)((from + k) * H), bar(B_FULL + slot));
           }
-          mma_commit(bar);
+          __syncwarp();
         }
-        const float scale = *reinterpret_cast<const float*>(smem + row_chunk(row, 4));
-        if (i == 0 && t_next < v.total_q) {
-          tok_next = paged_token(v, t_next);
-          nb_next = blocks_of(tok_next);
+    } else if (warp == 1) {
+      // ---- products
+      constexpr uint32_t idesc = idesc_i8(TILE, H);
+      for (int k = 0; ok && k < cnt; ++k, ++done) {
+        const uint32_t d = tmem + 128 * (done & 1);
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(B_DFREE + (done & 1)), ((done >> 1) & 1) ^ 1)) != 0;
+        for (int e = 0; ok && e < kBoxes; ++e, ++n) {
+          const uint32_t slot = n % RING;
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(B_FULL + slot), (n / RING) & 1)) != 0;
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t a = sw128_desc(sbase + OFF_Y + e * KBOX, 0, 1024), b = sw128_desc(sbase + OFF_RING + slot * KBOX, 0, 1024);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (e < 4 || i < 2) mma_i8(d, a + 2 * i, b + 2 * i, idesc, (e | i) ? 1u : 0u);
+            mma_commit(bar(B_EMPTY + slot));
+            if (e == kBoxes - 1) mma_commit(bar(B_DFULL + (done & 1)));
+          }
+          __syncwarp();
         }
-        const int page_after = i + 2 < n ? page_of(tok, nb, i + 2) : i + 1 == n && nb_next > 0 ? page_of(tok_next, nb_next, 0) : -1;
-        // multiplied, and the scales are read: the buffer takes the next tile (or a wait gave up, for all of them)
-        ok = !bar_sync_or(1, 256, !mbar_wait(bar, done & 1));
-        tc_fence_after();
+      }
+    } else if (warp >= 4) {
+      // ---- maxima: thread = block, 64 heads
+      float* part = reinterpret_cast<float*>(smem + OFF_PART);
+      float* sq = reinterpret_cast<float*>(smem + OFF_SQ);
+      const float scale = sy[row];
+      const int et = tid - 128;
+      float s_next = et < H ? p.scales[from * H + et] : 0.f;
+      for (int k = 0; ok && k < cnt; ++k, ++done) {
+        float* sqb = sq + (done & 1) * H;
+        if (et < H) {
+          sqb[et] = s_next;
+          if (k + 1 < cnt) s_next = p.scales[(from + k + 1) * H + et];
+        }
+        // (also: the upper half's maxima of the token before are read)
+        ok = !bar_sync_or(1, 256, !mbar_wait(bar(B_DFULL + (done & 1)), (done >> 1) & 1));
         if (!ok) break;
-        if (i + 1 < n) fetch(page_next);
-        else if (nb_next > 0) fetch(page_after);
-        page_next = page_after;
+        tc_fence_after();
         float mx = -INFINITY;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t x[32];
-          tmem_ld32(tmem + ((uint32_t)(32 * quarter) << 16) + 64 * cg + 32 * h, x);
+          tmem_ld32(tmem + ((uint32_t)(32 * quarter) << 16) + 128 * (done & 1) + 64 * cg + 32 * h, x);
           tmem_wait_ld();
 #pragma unroll
           for (int c = 0; c < 32; c += 4) {
-            const float4 s4 = *reinterpret_cast<const float4*>(sq + 32 * h + c);
+            const float4 s4 = *reinterpret_cast<const float4*>(sqb + 64 * cg + 32 * h + c);
             mx = fmaxf(mx, fmaxf(fmaxf((float)(int)x[c] * s4.x, (float)(int)x[c + 1] * s4.y),
                                  fmaxf((float)(int)x[c + 2] * s4.z, (float)(int)x[c + 3] * s4.w)));
           }
         }
-        float* upper = reinterpret_cast<float*>(smem + row_chunk(row, 5));
-        if (cg == 1) *upper = mx;
         tc_fence_before();
-        tiles_barrier();
-        const int g = (first + i * stride) * TILE + row;
-        if (cg == 0 && g < nb) scores[t * v.max_pages + g] = fmaxf(mx, *upper) * scale + 0.f;   // + 0: a -0 ties with a 0
-      }
-      if (n == 0 && t_next < v.total_q) {
-        tok_next = paged_token(v, t_next);
-        nb_next = blocks_of(tok_next);
-        if (nb_next > 0) fetch(page_of(tok_next, nb_next, 0));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_DFREE + (done & 1)));
+        if (cg == 1) part[row] = mx;
+        asm volatile("bar.sync 2, 256;" ::: "memory");
+        const int64_t g = (int64_t)tile * TILE + row;
+        if (cg == 0 && g <= (pos_from + k) / v.page)
+          p.scores[(from + k) * v.max_pages + g] = fmaxf(mx, part[row]) * scale + 0.f;   // + 0: a -0 ties with a 0
       }
     }
-    // the codes are written, the tiles multiplied
+    // the roles agree on what went by; the tile's buffer takes the next run's
+    if (warp == 0) done += cnt;
+    if (warp >= 2) n += kBoxes * cnt;
+    if (warp == 2 || warp == 3) done += cnt;
     if (!__syncthreads_and(ok)) {
-      if (tid == 0) flag_error(err, DEVERR_TIMEOUT);
+      ok = false;
       break;
     }
-    t = t_next;
-    tok = tok_next;
-    nb = nb_next;
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (!waited) wait_for_previous();                           // not complete before the codes are
+  if (!ok && tid == 0) {
+    flag_error(p.err, DEVERR_TIMEOUT);
+    for (uint32_t i = n > RING ? n - RING : 0; i < n; ++i) mbar_wait(bar(B_FULL + i % RING), (i / RING) & 1);
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 128);
+    tmem_dealloc(tmem, 256);
   }
 }
 
+size_t align1k(size_t x) { return (x + 1023) / 1024 * 1024; }
+
 }  // namespace
 
+size_t tc_select_bytes(int64_t total_q, int64_t max_pages) {
+  return align1k((size_t)total_q * max_pages * 4) + align1k((size_t)total_q * H * W) + align1k((size_t)total_q * H * 4);
+}
+
 cudaError_t tc_select_scores(const PagedView& v, const void* q_abs, const void* q_rope, const void* summaries,
-                             int32_t top_k, float* scores, int num_sms, uint32_t* err, cudaStream_t st) {
-  // per device, so set at every call
-  cudaError_t e = cudaFuncSetAttribute(select_score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+                             int32_t top_k, void* ws, int num_sms, uint32_t* err, cudaStream_t st) {
+  ScoreParams p;
+  memset(&p, 0, sizeof(p));
+  p.scores = (float*)ws;
+  int8_t* codes = (int8_t*)ws + align1k((size_t)v.total_q * v.max_pages * 4);
+  float* scales = (float*)(codes + align1k((size_t)v.total_q * H * W));
+  cudaError_t e = make_tmap_u8(&p.qmap, codes, W, v.total_q * H, W, 128, 128);
   if (e != cudaSuccess) return e;
-  // one CTA an SM: a token's tiles are split over several where tokens are few, else a CTA takes several tokens
-  const int64_t tiles = (v.max_pages + TILE - 1) / TILE;
-  int64_t split = num_sms / v.total_q;
-  split = split < 1 ? 1 : split > tiles ? tiles : split;
-  const int64_t rows = v.total_q < num_sms ? v.total_q : num_sms;
-  select_score_kernel<<<dim3((unsigned)split, (unsigned)rows), kThreads, SMEM_BYTES, st>>>(
-      v, (const __nv_bfloat16*)q_abs, (const __nv_bfloat16*)q_rope, (const uint8_t*)summaries,
-      (int64_t)summary_pitch(DC, DR), top_k, scores, err);
+  // per device, so set at every call
+  e = cudaFuncSetAttribute(select_score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  select_codes_kernel<<<(unsigned)(v.total_q * H / (ROWS * CODE_WARPS)), 32 * CODE_WARPS, 0, st>>>(
+      v, (const __nv_bfloat16*)q_abs, (const __nv_bfloat16*)q_rope, top_k, codes, scales, err);
   note_launch();
-  return cudaGetLastError();
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  p.v = v;
+  p.scales = scales;
+  p.summaries = (const uint8_t*)summaries;
+  p.pitch = (int64_t)summary_pitch(DC, DR);
+  p.top_k = top_k;
+  p.err = err;
+  // one CTA an SM and about two rounds of them: more tokens a CTA gather a tile's summaries less often (512 tokens x 512
+  // blocks: 3 rounds 89 us, 2 rounds 80, 1 round 79), fewer balance tiles behind a sequence's end and single tokens of
+  // many sequences (64 x 1 over 512 blocks: 2 rounds 37, 1 round 41)
+  const int64_t tiles = (v.max_pages + TILE - 1) / TILE;
+  const int64_t group = (v.total_q * tiles + 2 * num_sms - 1) / (2 * num_sms);
+  p.group = (int32_t)(group < 1 ? 1 : group);
+  return launch_next(select_score_kernel, dim3((unsigned)tiles, (unsigned)((v.total_q + p.group - 1) / p.group)), kThreads,
+                     SMEM_BYTES, st, p);
 }
 
 }  // namespace mla

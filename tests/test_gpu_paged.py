@@ -380,6 +380,49 @@ def test_select_half_of_the_largest(mods, dtype):
     assert torch.equal(got.cpu(), c.select(means, 33, 0, 1))
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_select_over_many_sequences(mods, dtype):
+    """More sequences than one look at cu_q takes, empty ones and a flagged one among them; some see fewer blocks
+    than top_k."""
+    m = mods[dtype]
+    tq = [(3 * b) % 5 % 4 for b in range(300)]
+    c = Case(dtype, 16, [20 + (37 * b) % 150 for b in range(300)], tq, seed=33)
+    bad = 204
+    assert tq[bad] == 2
+    c.d_lens[bad] = 1                                                   # fewer rows than new tokens
+    means = c.normal(c.num_pages, c.W)
+    got = m.paged_select(c.batch(), c.q_abs, c.q_rope, c.summaries(means).cuda(), 5, 1, 2)
+    flagged(m, 1 << 1)
+    want = c.select(means, 5, 1, 2)
+    want[int(c.cu[bad]):int(c.cu[bad + 1])] = -1
+    assert torch.equal(got.cpu(), want)
+
+
+def test_select_runs_that_cross_sequences(mods):
+    """Several tokens and both tiles of 128 blocks in one CTA, with the ends of sequences between them."""
+    c = Case("bf16", 16, [3300, 40, 2500, 2200, 2060], [150, 1, 120, 0, 81], seed=34)
+    means = c.normal(c.num_pages, c.W) * 0.3
+    got = mods["bf16"].paged_select(c.batch(), c.q_abs, c.q_rope, c.summaries(means).cuda(), 9, 1, 2)
+    ok(mods["bf16"])
+    assert torch.equal(got.cpu(), c.select(means, 9, 1, 2))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("top_k", [50, 8300])
+def test_select_among_more_blocks_than_shared_memory_holds(mods, dtype, top_k):
+    """8391 blocks over 41 pages, so that scores tie in hundreds."""
+    m = mods[dtype]
+    c = Case(dtype, 16, [16 * 41], [2], seed=35, spare=0)
+    nb = 8391
+    c.table = c.table[:, torch.arange(nb) * 7 % 41].contiguous()
+    c.lens = [16 * nb]
+    c.d_table, c.d_lens = c.table.cuda(), torch.tensor(c.lens, device="cuda")
+    means = c.normal(c.num_pages, c.W)
+    got = m.paged_select(c.batch(), c.q_abs, c.q_rope, c.summaries(means).cuda(), top_k, 1, 2)
+    ok(m)
+    assert torch.equal(got.cpu(), c.select(means, top_k, 1, 2))
+
+
 # ---- together -----------------------------------------------------------------------------------------------
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_a_prompt_in_chunks_then_decode_steps(mods, dtype):
