@@ -9,8 +9,8 @@
 // The products bound it: kind::i8 runs an M128 N128 K32 MMA in 128 cycles (half of the rate of fp8), 2304 a token and
 // tile; 512 tokens over 2048 blocks take 100 us, 74 % of the tensor pipe's time (70 us), the conversions of the sums to
 // fp32 61 % of the XU's. 512 tokens over 512 blocks: codes 20-30 us (110 MB), scores 35, choice 16; 80 in one call.
-// (Quantising inside the scoring kernel, a token's codes kept and the tiles streamed past, took 94 us there and 172
-// against 134 for four chunks of 512 tokens: 5 us of arithmetic a token, and a gather's latency for every tile.)
+// (Quantising inside the scoring kernel, a token's codes kept and the tiles streamed past, took 94 us there: 5 us of
+// arithmetic a token, and a gather's latency for every tile.)
 #include <cuda_bf16.h>
 #include <string.h>
 

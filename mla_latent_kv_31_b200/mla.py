@@ -122,7 +122,7 @@ def _stream(stream, device: int):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
     import torch
-    return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device)      # the handle that current_stream() wraps, 2 us sooner
 
 
 def _check(status: int, what: str):
@@ -388,7 +388,6 @@ class MLA:
         if getattr(dims, "yarn_s", 1.0) > 1.0:
             mla_set_yarn(self.handle, dims.yarn_s, dims.yarn_alpha, dims.yarn_beta, dims.yarn_l0)
         self._ws = None
-        self._ws_captured, self._kept = False, []
 
     def close(self):
         if self.handle:
@@ -404,11 +403,7 @@ class MLA:
     def workspace(self, nbytes: int):
         torch = self.torch
         if self._ws is None or self._ws.numel() < nbytes:
-            if self._ws_captured:
-                self._kept.append(self._ws)     # a captured graph still writes to it when it is replayed
-                self._ws_captured = False
             self._ws = torch.empty(max(nbytes, 1024), dtype=torch.uint8, device=f"cuda:{self.device}")
-        self._ws_captured = self._ws_captured or torch.cuda.is_current_stream_capturing()
         return self._ws
 
     def region(self, op, which, shape, dtype, num_seqs=0, tq=1, total_tokens=0):
@@ -510,6 +505,11 @@ class MLA:
         return self.torch.zeros(num_pages, mla_paged_summary_bytes(self.handle), dtype=self.torch.uint8,
                                 device=f"cuda:{self.device}")
 
+    def _scratch(self, nbytes: int):
+        """A workspace of one call, from the current stream's allocations (in a capture, the graph's own): calls on
+        several streams or threads and graphs that replay side by side never share one."""
+        return self.torch.empty(max(nbytes, 1), dtype=self.torch.uint8, device=self.torch_device)
+
     def _expect_summaries(self, batch, summaries):
         d = self.dims
         shape = (batch.cache.shape[0], (d.d_c + d.d_r + 4 + 15) // 16 * 16)
@@ -561,7 +561,7 @@ class MLA:
             o_lat = torch.empty((T, d.n_h, d.d_c), dtype=self.tdtype, device=self.torch_device)
         if lse is None:
             lse = torch.empty((T, d.n_h), dtype=torch.float32, device=self.torch_device)
-        ws = self.workspace(mla_attn_paged_workspace(self.handle, batch.B, T))
+        ws = self._scratch(mla_attn_paged_workspace(self.handle, batch.B, T))
         if blocks is None:
             mla_attn_paged(self.handle, batch, q_abs, q_rope, o_lat, lse, ws, ws.numel(), device=self.device)
         else:
@@ -580,7 +580,7 @@ class MLA:
         self._expect_summaries(batch, summaries)
         if blocks is None:
             blocks = self.torch.empty((batch.total_q, top_k), dtype=self.torch.int32, device=self.torch_device)
-        ws = self.workspace(mla_paged_select_workspace(self.handle, batch.total_q, batch.max_pages))
+        ws = self._scratch(mla_paged_select_workspace(self.handle, batch.total_q, batch.max_pages))
         mla_paged_select(self.handle, batch, q_abs, q_rope, summaries, top_k, n_first, n_last, blocks, ws, ws.numel(),
                          device=self.device)
         return blocks

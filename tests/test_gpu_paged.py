@@ -502,3 +502,42 @@ def test_captured_steps_replay_on_new_lengths(mods, dtype):
             c.rows = [pool[c.table[s, torch.arange(n) // 32].long(), torch.arange(n) % 32] for s, n in enumerate(lens)]
             c.check_attention(o, lse, listed_rows(c, blocks.cpu()))
             assert (o[c.T:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_calls_and_graphs_side_by_side_on_two_streams(mods, dtype):
+    """The same calls of one handle on two streams at once, eager and as two graphs: as when they run alone."""
+    m = mods[dtype]
+    cases = [Case(dtype, 16, lens, tq, seed=60 + k) for k, (lens, tq) in enumerate((([900, 64, 33], [3, 1, 2]),
+                                                                                 ([16 * 200], [40])))]
+    jobs = []
+    for c in cases:
+        qa, qr, sums = c.q_abs, c.q_rope, c.summaries(c.normal(c.num_pages, c.W)).cuda()
+        blocks = torch.empty(c.T, 6, dtype=torch.int32, device="cuda")
+        outs = [torch.empty_like(qa), torch.empty(c.T, c.dims.n_h, device="cuda"),
+                torch.empty_like(qa), torch.empty(c.T, c.dims.n_h, device="cuda")]
+
+        def step(batch=c.batch(), qa=qa, qr=qr, sums=sums, blocks=blocks, outs=outs):
+            m.paged_select(batch, qa, qr, sums, 6, 1, 1, blocks)
+            m.attn_paged_sparse(batch, qa, qr, blocks, *outs[:2])
+            m.attn_paged(batch, qa, qr, *outs[2:])
+        step()
+        ok(m)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        torch.cuda.synchronize()
+        jobs.append((step, g, torch.cuda.Stream(), [blocks, *outs], [x.clone() for x in (blocks, *outs)]))
+    for graphs in (False, True):
+        for _, _, _, got, _ in jobs:
+            for x in got:
+                x.zero_()
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for step, g, s, _, _ in jobs:
+                with torch.cuda.stream(s):
+                    g.replay() if graphs else step()
+        torch.cuda.synchronize()
+        ok(m)
+        for _, _, _, got, want in jobs:
+            assert all(torch.equal(x, y) for x, y in zip(got, want))
