@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(512) summarise_kernel(PagedView v, int group, 
     if ((tid & 31) < group && t < v.total_q && t < v.cu_q[v.B]) {
       const int64_t b = seq_of_token(v.cu_q, v.B, t), q0 = v.cu_q[b], n = v.cu_q[b + 1] - q0, len = v.kv_lens[b];
       const int64_t pos = len - n + (t - q0);
-      if (t >= q0 && t - q0 < n && n <= len && len <= v.max_pages * v.page && (pos + 1) % v.page == 0) {
+      if (t >= q0 && t - q0 < n && n <= len && len <= v.max_pages * v.page && pos >= 0 && (pos + 1) % v.page == 0) {
         own = v.table[b * v.stride + pos / v.page];
         if (own >= v.num_pages) own = -1;                     // flagged by the append
       }

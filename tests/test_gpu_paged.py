@@ -505,6 +505,28 @@ def test_captured_steps_replay_on_new_lengths(mods, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("T", [1, 5, 100])
+def test_a_batch_without_new_tokens_leaves_everything_as_it_was(mods, dtype, T):
+    m = mods[dtype]
+    c = Case(dtype, 16, [100, 0, 33], [0, 0, 0], seed=61, pad=T)
+    d = c.dims
+    cache, kv = c.cache.clone(), c.on(c.normal(T, c.W))
+    sums = m.new_summaries(c.num_pages) + 5
+    q_out = torch.full((T, d.n_h, d.d_r), 7.0, dtype=DT[dtype], device="cuda")
+    blocks = torch.full((T, 4), -9, dtype=torch.int32, device="cuda")
+    o = torch.full((T, d.n_h, d.d_c), 7.0, dtype=DT[dtype], device="cuda")
+    lse = torch.full((T, d.n_h), 7.0, device="cuda")
+    m.paged_append(c.batch(), kv, q_rope=c.q_rope, q_out=q_out, summaries=sums)
+    m.paged_select(c.batch(), c.q_abs, c.q_rope, sums, 4, 1, 1, blocks)
+    m.attn_paged(c.batch(), c.q_abs, c.q_rope, o, lse)
+    m.attn_paged_sparse(c.batch(), c.q_abs, c.q_rope, blocks, o, lse)
+    ok(m)
+    i = torch.int16 if dtype == "bf16" else torch.int32
+    assert torch.equal(c.cache.view(i), cache.view(i)) and (sums == 5).all()
+    assert all((x == y).all() for x, y in ((q_out, 7), (blocks, -9), (o, 7), (lse, 7)))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_calls_and_graphs_side_by_side_on_two_streams(mods, dtype):
     """The same calls of one handle on two streams at once, eager and as two graphs: as when they run alone."""
     m = mods[dtype]
