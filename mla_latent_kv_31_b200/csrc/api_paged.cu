@@ -19,6 +19,7 @@ using mla::PagedView;
 using mla::tc_dims;
 
 constexpr int64_t kMaxRows = INT32_MAX;
+constexpr int64_t kMaxLen = 1 << 30;         // rows of a sequence: 32-bit key numbers with room for a step
 constexpr int64_t kMaxSelectTokens = 65535;  // a grid's second dimension
 
 // The host checks that every paged call shares; on MLA_OK *v describes the batch.
@@ -28,7 +29,7 @@ mla_status_t view_of(const mla_handle_t* h, const mla_paged_t* b, PagedView* v) 
   if (!b->cache || !b->block_table || !b->cu_q || !b->kv_lens || b->B <= 0 || b->total_q <= 0 || b->num_pages <= 0 ||
       b->max_pages <= 0 || b->table_stride < b->max_pages || b->page_size <= 0 || b->page_size % 16 != 0)
     return MLA_ERR_INVALID_ARG;
-  if (b->num_pages > kMaxRows / b->page_size || b->max_pages > kMaxRows / b->page_size || b->B > (1 << 20) ||
+  if (b->num_pages > kMaxRows / b->page_size || b->max_pages > kMaxLen / b->page_size || b->B > (1 << 20) ||
       b->total_q > kMaxRows / h->dims.n_h)
     return MLA_ERR_INVALID_ARG;
   if (!aligned16(b->cache) || !aligned16(b->block_table) || !aligned16(b->cu_q) || !aligned16(b->kv_lens))

@@ -12,8 +12,8 @@
 // 16 x 36 and 2 x 16 x 4 MMAs of N = 256. (An M = 128 pair MMA takes 78 cycles at N = 256 and 68 at N = 128,
 // measured: the 256-key step is what keeps the tensor cores near their rate.)
 //
-// Work split. Tokens are cut into units of 64 keys; all units of all tokens, plus a fixed cost per token,
-// are dealt to the pairs in equal contiguous ranges. A token that lies in one range is written by its pair; one
+// Work split. Tokens are cut into units of a step's 256 keys; all units of all tokens, plus a fixed cost per token,
+// are dealt to the pairs in equal contiguous ranges of at least kMinRange. A token that lies in one range is written by its pair; one
 // that crosses ranges leaves an unnormalised fp32 partial per range, merged exactly by combine_kernel.
 //
 // Pages. A step's 256 keys are 16 groups of 16 keys; each group's row in the pool comes from the block table (and
@@ -45,11 +45,12 @@ using namespace sm100;
 constexpr int H = 128, DC = 512, DR = 64;
 constexpr int HC = H / 2;                      // heads per CTA
 constexpr int NK = 256;                        // keys per step
-constexpr int UNIT = 64;                       // keys per unit of the work split
+constexpr int UNIT = NK;                       // keys per unit of the work split
 constexpr int GROUPS = NK / 16;                // a step's rows are looked up in groups of 16 keys
 constexpr int kThreads = 512;
 constexpr int kMaxPairs = 74;
-constexpr int kStartUnits = 4;                 // a token's fixed cost (query load, epilogue), in units
+constexpr int kStartUnits = 1;                 // a token's fixed cost (query load, epilogue), in units
+constexpr int kMinRange = 2;                   // a pair's smallest range, in units and start costs
 constexpr int64_t kPlanTokens = 64;            // tokens looked up in the plan's own launch
 constexpr float kRescaleLog2 = 8.f;            // keep the running maximum until it grows by 2^8
 constexpr int kEntriesK = 9, kEntriesV = 8;    // ring entries of a step: [128 keys x 64], 2 x [64 keys x 64]
@@ -711,7 +712,7 @@ struct PlanParams {
   int64_t* cost;
   int4* pinfo;
   int2* pfirst;
-  int32_t* splits;            // [pairs]: the pairs in whose range a token begins that goes on in the next, then -1
+  int4* splits;               // [pairs]: the tokens that cross ranges (token, first slot, first pair, last pair), then -1
   __nv_bfloat16* o_lat;
   float* lse;
   uint32_t* err;
@@ -760,14 +761,15 @@ __global__ void __launch_bounds__(256) paged_tokens_kernel(const __grid_constant
 }
 
 // Deals the tokens' units to the pairs (one block; with TOKENS it also looks the tokens up first). In cost, token t with u_t > 0 units is kStartUnits + u_t
-// long; pair pp's range begins at the first unit whose cost starts at or after pp * total / pairs. Each pair's
-// range is written as (first token, its first unit, last token, its end unit), (-1, ...) if empty.
+// long; of n = min(pairs, total / kMinRange) pairs, pair pp's range begins at the first unit whose cost starts at or
+// after pp * total / n. (A unit never starts two costs behind the one before, so no range of kMinRange is empty.) Each
+// pair's range is written as (first token, its first unit, last token, its end unit), (-1, ...) if it has none.
 template <bool TOKENS>
 __global__ void __launch_bounds__(1024) paged_plan_kernel(const __grid_constant__ PlanParams p) {
   __shared__ int64_t warp_tot[32];
   __shared__ int64_t total;
   __shared__ int32_t btok[kMaxPairs + 1], bunit[kMaxPairs + 1];
-  __shared__ bool begins[kMaxPairs];
+  __shared__ int4 begins[kMaxPairs];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t T = p.v.total_q;
   const int pairs = p.pairs;
@@ -813,24 +815,30 @@ __global__ void __launch_bounds__(1024) paged_plan_kernel(const __grid_constant_
   }
   __syncthreads();
   // the boundaries: the first token whose end lies behind the boundary's cost, and the unit in it
-  for (int pp = tid; pp <= pairs; pp += blockDim.x) {
-    const int64_t c = total * pp / pairs;
+  const int used = (int)max((int64_t)1, min((int64_t)pairs, total / kMinRange));
+  for (int pp = tid; pp <= used; pp += blockDim.x) {
+    const int64_t c = total * pp / used;
     int64_t a = 0, b = T;                     // the last token with cost <= c
     while (b - a > 1) {
       const int64_t mid = (a + b) >> 1;
       if (cost[mid] <= c) a = mid; else b = mid;
     }
     int u = (int)max((int64_t)0, c - cost[a] - kStartUnits);
-    if (pp == pairs || u >= units(a)) {       // behind its last unit: the next token
+    if (pp == used || u >= units(a)) {        // behind its last unit: the next token
       ++a;
       u = 0;
-      if (pp == pairs) a = T;
+      if (pp == used) a = T;
     }
     btok[pp] = (int32_t)a;
     bunit[pp] = u;
   }
   __syncthreads();
   for (int pp = tid; pp < pairs; pp += blockDim.x) {
+    begins[pp] = make_int4(-1, 0, 0, 0);
+    if (pp >= used) {
+      p.pinfo[pp] = make_int4(-1, 0, -2, 0);
+      continue;
+    }
     int a = btok[pp], e = btok[pp + 1], ue = bunit[pp + 1];
     int ua = bunit[pp];
     while (a < T && units(a) == 0) { ++a; ua = 0; }         // tokens without units
@@ -841,56 +849,45 @@ __global__ void __launch_bounds__(1024) paged_plan_kernel(const __grid_constant_
     const bool any = a < T && (a < e || (a == e && ua < ue));
     p.pinfo[pp] = any ? make_int4(a, ua, e, ue) : make_int4(-1, 0, -2, 0);
     if (any) p.pfirst[pp] = tinfo[a];
-    begins[pp] = any && ue < units(e) && !(a == e && ua > 0);
+    if (any && ue < units(e) && !(a == e && ua > 0)) {       // e begins here and goes on: to the pair of its last unit
+      const int64_t at_last = cost[e] + kStartUnits + units(e) - 1;
+      begins[pp] = make_int4(e, 2 * pp + (a == e ? 0 : 1), pp, (int)(((at_last + 1) * used - 1) / total));
+    }
   }
   __syncthreads();
   if (warp == 0) {
     int n = 0;
     for (int p0 = 0; p0 < pairs; p0 += 32) {
-      const bool is = p0 + lane < pairs && begins[p0 + lane];
-      const uint32_t m = __ballot_sync(0xffffffffu, is);
-      if (is) p.splits[n + __popc(m & ((1u << lane) - 1u))] = p0 + lane;
+      const int4 it = p0 + lane < pairs ? begins[p0 + lane] : make_int4(-1, 0, 0, 0);
+      const uint32_t m = __ballot_sync(0xffffffffu, it.x >= 0);
+      if (it.x >= 0) p.splits[n + __popc(m & ((1u << lane) - 1u))] = it;
       n += __popc(m);
     }
-    for (int k = n + lane; k < pairs; k += 32) p.splits[k] = -1;
+    for (int k = n + lane; k < pairs; k += 32) p.splits[k] = make_int4(-1, 0, 0, 0);
   }
 }
 
-// Exact merge of the tokens that cross ranges. Block (k, heads, columns) takes the k-th of them, the one that begins
-// in the range of pair splits[k] and goes on in the next: o = sum_s e^{m_s - M} O_s / sum_s e^{m_s - M} l_s over its
-// pieces, in order.
-constexpr int kCombHeads = 32, kCombCols = 32;
+// Exact merge of the tokens that cross ranges. Block (k, heads, columns) takes the k-th of them:
+// o = sum_s e^{m_s - M} O_s / sum_s e^{m_s - M} l_s over its pieces, in order: its first slot, then the first slots of
+// the pairs behind. The first kCombEarly pieces are loaded along with the maxima.
+constexpr int kCombHeads = 32, kCombCols = 32, kCombEarly = 8;
 __global__ void __launch_bounds__(256)
-    paged_combine_kernel(const int2* tinfo, const int4* pinfo, const int32_t* splits, int32_t pairs,
-                         const float4* part_o, const float2* part_ml, __nv_bfloat16* o_lat, float* lse) {
-  __shared__ int4 ranges[kMaxPairs];
-  __shared__ int32_t slots[kMaxPairs];
-  __shared__ int32_t ns_sh;
+    paged_combine_kernel(const int4* splits, const float4* part_o, const float2* part_ml, __nv_bfloat16* o_lat, float* lse) {
   __shared__ float2 ml[kMaxPairs][kCombHeads];     // maximum and sum of each piece, then its weight
   __shared__ __align__(16) float tile[kCombHeads][kCombCols + 4];   // written as float4
   const int tid = threadIdx.x, lane = tid & 31, grp = tid >> 5;
   wait_for_previous();
-  const int c = splits[blockIdx.x];
-  if (c < 0) return;
-  for (int d = tid; d < pairs; d += blockDim.x) ranges[d] = pinfo[d];
-  __syncthreads();
-  const int4 pc = ranges[c];
-  const int tok = pc.z;
-  if (tid == 0) {
-    const int units = (tinfo[tok].y + UNIT - 1) / UNIT;
-    int n = 0;
-    slots[n++] = 2 * c + (pc.x == tok ? 0 : 1);
-    for (int d = c + 1; d < pairs; ++d) {
-      const int4 pd = ranges[d];
-      if (pd.x < 0) continue;
-      slots[n++] = 2 * d;
-      if (pd.z != tok || pd.w >= units) break;
-    }
-    ns_sh = n;
-  }
-  __syncthreads();
-  const int ns = ns_sh, h0 = kCombHeads * blockIdx.y, c0 = kCombCols * blockIdx.z;
-  for (int s = grp; s < ns; s += 8) ml[s][lane] = part_ml[(int64_t)slots[s] * H + h0 + lane];
+  const int4 sp = splits[blockIdx.x];
+  const int tok = sp.x;
+  if (tok < 0) return;
+  const int ns = sp.w - sp.z + 1, h0 = kCombHeads * blockIdx.y, c0 = kCombCols * blockIdx.z;
+  auto slot = [&](int s) -> int64_t { return s == 0 ? sp.y : 2 * (sp.z + s); };
+  const float4* src = part_o + (int64_t)(c0 / 4 + grp) * H + h0 + lane;
+  float4 early[kCombEarly];
+#pragma unroll
+  for (int s = 0; s < kCombEarly; ++s)
+    if (s < ns) early[s] = src[slot(s) * (DC / 4) * H];
+  for (int s = grp; s < ns; s += 8) ml[s][lane] = part_ml[slot(s) * H + h0 + lane];
   __syncthreads();
   // weights e^{m_s - M} / L of the pieces (lane = head; the warps share the pieces, each finds M and L itself)
   float M = -INFINITY, L = 0.f;
@@ -904,13 +901,15 @@ __global__ void __launch_bounds__(256)
   __syncthreads();
   // thread (lane = head, grp): the column quad grp of this block's 8
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float4* src = part_o + (int64_t)(c0 / 4 + grp) * H + h0 + lane;
-#pragma unroll 8
-  for (int s = 0; s < ns; ++s) {
-    const float4 x = src[(int64_t)slots[s] * (DC / 4) * H];
+  auto add = [&](int s, float4 x) {
     const float e = ml[s][lane].x;
     acc.x += e * x.x; acc.y += e * x.y; acc.z += e * x.z; acc.w += e * x.w;
-  }
+  };
+#pragma unroll
+  for (int s = 0; s < kCombEarly; ++s)
+    if (s < ns) add(s, early[s]);
+#pragma unroll 8
+  for (int s = kCombEarly; s < ns; ++s) add(s, src[slot(s) * (DC / 4) * H]);
   *reinterpret_cast<float4*>(&tile[lane][4 * grp]) = acc;
   __syncthreads();
   // head tid / 8, 4 columns each
@@ -935,7 +934,7 @@ struct Scratch {
   int64_t* cost;
   int4* pinfo;
   int2* pfirst;
-  int32_t* splits;
+  int4* splits;
   float2* part_ml;
   float4* part_o;
   size_t bytes;
@@ -952,8 +951,8 @@ Scratch carve(void* ws, int64_t T) {
   p += align1k(kMaxPairs * sizeof(int4));
   s.pfirst = (int2*)p;
   p += align1k(kMaxPairs * sizeof(int2));
-  s.splits = (int32_t*)p;
-  p += align1k(kMaxPairs * sizeof(int32_t));
+  s.splits = (int4*)p;
+  p += align1k(kMaxPairs * sizeof(int4));
   s.part_ml = (float2*)p;
   p += align1k((size_t)2 * kMaxPairs * H * sizeof(float2));
   s.part_o = (float4*)p;
@@ -1023,8 +1022,7 @@ cudaError_t tc_paged_attention(const PagedView& v, const void* q_abs, const void
   const int64_t most = p.pairs - 1 < v.total_q ? p.pairs - 1 : v.total_q;
   if (most > 0)
     e = launch_next(paged_combine_kernel, dim3((unsigned)most, H / kCombHeads, DC / kCombCols), 256, 0, st,
-                    (const int2*)s.tinfo, (const int4*)s.pinfo, (const int32_t*)s.splits, p.pairs,
-                    (const float4*)s.part_o, (const float2*)s.part_ml, p.o_lat, lse);
+                    (const int4*)s.splits, (const float4*)s.part_o, (const float2*)s.part_ml, p.o_lat, lse);
   return e;
 }
 
