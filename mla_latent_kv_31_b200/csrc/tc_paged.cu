@@ -96,9 +96,9 @@ struct CoreParams {
   PagedView v;
   const int32_t* blocks;      // [T, top_k] chosen blocks; nullptr: all rows
   int32_t top_k, pairs;
-  const int2* tinfo;          // [T]: sequence, visible rows
+  const int4* tinfo;          // [T] in the order of the walk: sequence, visible rows, token
   const int4* pinfo;          // [pairs]: first token, its first unit, last token, its end unit
-  const int2* pfirst;         // [pairs]: the first token's tinfo
+  const int4* pfirst;         // [pairs]: the first token's tinfo
   __nv_bfloat16* o_lat;
   float* lse;
   float4* part_o;             // [2 * pairs][DC / 4][H]
@@ -198,18 +198,19 @@ __device__ __forceinline__ bool wait_own(uint32_t bar, uint32_t parity) {
 
 // The tokens of a pair's range, and of each the keys [k0, k1) that fall into it.
 struct Walk {
-  const int2* tinfo;
-  int tok, tok1, e1;
-  int seq, vis, k0, k1;
-  __device__ void set(int2 ti, int u) {
+  const int4* tinfo;
+  int tok, tok1, e1;          // in the order of the walk
+  int id, seq, vis, k0, k1;   // id: the token
+  __device__ void set(int4 ti, int u) {
     seq = ti.x;
     vis = ti.y;
+    id = ti.z;
     k0 = u * UNIT;
     k1 = tok == tok1 ? min(vis, e1 * UNIT) : vis;
   }
   __device__ void init(const CoreParams& p, int pair) {
     const int4 pi = p.pinfo[pair];
-    const int2 first = p.pfirst[pair];
+    const int4 first = p.pfirst[pair];
     tinfo = p.tinfo;
     tok = pi.x; tok1 = pi.z; e1 = pi.w;
     if (valid()) set(first, pi.y);
@@ -251,7 +252,7 @@ struct Rows {
     const int j = s2.k + 16 * g;
     if (s2.valid() && j < s2.w.k1) {
       const int i = j / p.v.page;
-      blk2 = p.blocks ? p.blocks[(int64_t)s2.w.tok * p.top_k + i] : i;
+      blk2 = p.blocks ? p.blocks[(int64_t)s2.w.id * p.top_k + i] : i;
     }
   }
   __device__ void entry(const CoreParams& p) {
@@ -340,7 +341,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, wait_own(bar(B_QEMPTY), (g & 1) ^ 1)) != 0;
       if (ok && elect_one()) {
         if (r == 0) mbar_expect_tx(bar(B_QFULL), 2 * Q_BYTES);
-        const int32_t y = w.tok * H + HC * (int)r;
+        const int32_t y = w.id * H + HC * (int)r;
         for (int c = 0; c < 8; ++c) pair_load(sbase + OFF_Q + c * BOX, &p.qmap, 64 * c, y, lead(B_QFULL));
         pair_load(sbase + OFF_Q + 8 * BOX, &p.qrmap, 0, y, lead(B_QFULL));
       }
@@ -656,7 +657,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!wait_u(bar(B_ODONE), gpc & 1)) { ok = false; break; }
       tc_fence_after();
       const bool whole = w.whole();
-      const int64_t row = (int64_t)w.tok * H + head;
+      const int64_t row = (int64_t)w.id * H + head;
       const int slot = 2 * pair + (gpc > 0 ? 1 : 0);
       if (quarter < 2) {
         if (whole) p.lse[row] = l == 0.f ? -INFINITY : m + logf(l);
@@ -708,18 +709,39 @@ struct PlanParams {
   PagedView v;
   const int32_t* blocks;
   int32_t top_k, pairs;
-  int2* tinfo;
+  bool gangs;                 // whether the tokens may be reordered (see gang_of)
+  int4* tinfo;
   int64_t* cost;
   int4* pinfo;
-  int2* pfirst;
+  int4* pfirst;
   int4* splits;               // [pairs]: the tokens that cross ranges (token, first slot, first pair, last pair), then -1
   __nv_bfloat16* o_lat;
   float* lse;
   uint32_t* err;
 };
 
+// Gangs. Pairs that run through the same rows at the same time read them from HBM once. Where every sequence has n new
+// tokens (draft-and-verify steps, even chunks), the order of the walk is changed: the n tokens of a sequence are cut into g
+// groups of n / g, and the walk takes the first group of every sequence, then the second of every sequence, and so on.
+// With a multiple of g pairs each group falls to as many pairs, and the i-th pairs of the g groups walk the same
+// sequences over the same keys, side by side. g: the largest divisor of n up to 12 that leaves at most 4 of 74 pairs
+// idle. Measured, the tokens' own order against gangs (B x n tokens, us): 64 x 2 behind 16896 rows 579 -> 521,
+// 64 x 4 1143 -> 993, 64 x 16 behind 4096 1340 -> 1135, 16 x 2 behind 4096 85 -> 75, 8 x 64 behind 16384 2270 -> 2010.
+// Returns n (0: no common one, the tokens' own order) and g, the same in all threads of the block.
+__device__ inline int2 gang_of(const PlanParams& p) {
+  if (!p.gangs) return make_int2(0, 1);
+  const PagedView& v = p.v;
+  const int64_t end = v.cu_q[v.B], n = end / v.B;
+  bool even = n >= 2 && end == n * v.B && end <= v.total_q;
+  for (int64_t b = threadIdx.x; b < v.B; b += blockDim.x) even = even && v.cu_q[b] == b * n;
+  if (!__syncthreads_and(even)) return make_int2(0, 1);
+  int g = (int)min(n, (int64_t)12);
+  while (g > 1 && (n % g != 0 || p.pairs % g > p.pairs / 18)) --g;
+  return make_int2((int)n, g);
+}
+
 // Sequence and visible rows of new token t, by one warp; an empty row is written here.
-__device__ __forceinline__ void plan_token(const PlanParams& p, int64_t t, int lane) {
+__device__ __forceinline__ void plan_token(const PlanParams& p, int64_t t, int2 gang, int lane) {
   const PagedView& v = p.v;
   const PagedToken tok = paged_token(v, t);
   int64_t vis = tok.pos + 1;
@@ -744,7 +766,14 @@ __device__ __forceinline__ void plan_token(const PlanParams& p, int64_t t, int l
     }
     vis = n == 0 ? 0 : (int64_t)(n - 1) * v.page + (at == own ? tok.pos % v.page + 1 : v.page);
   }
-  if (lane == 0) p.tinfo[t] = make_int2(tok.seq, (int32_t)(tok.seq < 0 ? 0 : vis));
+  if (lane == 0) {
+    int64_t at = t;
+    if (gang.y > 1 && tok.seq >= 0) {
+      const int per = gang.x / gang.y, k = (int)(t - (int64_t)tok.seq * gang.x);
+      at = ((int64_t)(k / per) * v.B + tok.seq) * per + k % per;
+    }
+    p.tinfo[at] = make_int4(tok.seq, (int32_t)(tok.seq < 0 ? 0 : vis), (int32_t)t, 0);
+  }
   if (tok.seq >= 0 && vis <= 0) {
     uint4* o = reinterpret_cast<uint4*>(p.o_lat + t * H * DC);
     for (int i = lane; i < H * DC / 8; i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -756,8 +785,9 @@ __device__ __forceinline__ void plan_token(const PlanParams& p, int64_t t, int l
 __global__ void __launch_bounds__(256) paged_tokens_kernel(const __grid_constant__ PlanParams p) {
   let_next_start();
   if (blockIdx.x == 0) paged_check(p.v, p.err);
+  const int2 gang = gang_of(p);
   const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (t < p.v.total_q) plan_token(p, t, threadIdx.x & 31);
+  if (t < p.v.total_q) plan_token(p, t, gang, threadIdx.x & 31);
 }
 
 // Deals the tokens' units to the pairs (one block; with TOKENS it also looks the tokens up first). In cost, token t with u_t > 0 units is kStartUnits + u_t
@@ -773,12 +803,13 @@ __global__ void __launch_bounds__(1024) paged_plan_kernel(const __grid_constant_
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t T = p.v.total_q;
   const int pairs = p.pairs;
-  int2* tinfo = p.tinfo;
+  int4* tinfo = p.tinfo;
   int64_t* cost = p.cost;
   let_next_start();
+  const int2 gang = gang_of(p);
   if (TOKENS) {
     paged_check(p.v, p.err);
-    for (int64_t t = warp; t < T; t += 32) plan_token(p, t, lane);
+    for (int64_t t = warp; t < T; t += 32) plan_token(p, t, gang, lane);
     __syncthreads();
   } else {
     wait_for_previous();
@@ -815,7 +846,8 @@ __global__ void __launch_bounds__(1024) paged_plan_kernel(const __grid_constant_
   }
   __syncthreads();
   // the boundaries: the first token whose end lies behind the boundary's cost, and the unit in it
-  const int used = (int)max((int64_t)1, min((int64_t)pairs, total / kMinRange));
+  int used = (int)max((int64_t)1, min((int64_t)pairs, total / kMinRange));
+  if (used >= gang.y) used -= used % gang.y;
   for (int pp = tid; pp <= used; pp += blockDim.x) {
     const int64_t c = total * pp / used;
     int64_t a = 0, b = T;                     // the last token with cost <= c
@@ -851,7 +883,7 @@ __global__ void __launch_bounds__(1024) paged_plan_kernel(const __grid_constant_
     if (any) p.pfirst[pp] = tinfo[a];
     if (any && ue < units(e) && !(a == e && ua > 0)) {       // e begins here and goes on: to the pair of its last unit
       const int64_t at_last = cost[e] + kStartUnits + units(e) - 1;
-      begins[pp] = make_int4(e, 2 * pp + (a == e ? 0 : 1), pp, (int)(((at_last + 1) * used - 1) / total));
+      begins[pp] = make_int4(tinfo[e].z, 2 * pp + (a == e ? 0 : 1), pp, (int)(((at_last + 1) * used - 1) / total));
     }
   }
   __syncthreads();
@@ -930,10 +962,10 @@ cudaError_t launch_core(const CoreParams& p, cudaStream_t st) {
 size_t align1k(size_t x) { return (x + 1023) / 1024 * 1024; }
 
 struct Scratch {
-  int2* tinfo;
+  int4* tinfo;
   int64_t* cost;
   int4* pinfo;
-  int2* pfirst;
+  int4* pfirst;
   int4* splits;
   float2* part_ml;
   float4* part_o;
@@ -943,14 +975,14 @@ struct Scratch {
 Scratch carve(void* ws, int64_t T) {
   Scratch s;
   char* p = (char*)ws;
-  s.tinfo = (int2*)p;
-  p += align1k((size_t)T * sizeof(int2));
+  s.tinfo = (int4*)p;
+  p += align1k((size_t)T * sizeof(int4));
   s.cost = (int64_t*)p;
   p += align1k((size_t)T * sizeof(int64_t));
   s.pinfo = (int4*)p;
   p += align1k(kMaxPairs * sizeof(int4));
-  s.pfirst = (int2*)p;
-  p += align1k(kMaxPairs * sizeof(int2));
+  s.pfirst = (int4*)p;
+  p += align1k(kMaxPairs * sizeof(int4));
   s.splits = (int4*)p;
   p += align1k(kMaxPairs * sizeof(int4));
   s.part_ml = (float2*)p;
@@ -996,6 +1028,9 @@ cudaError_t tc_paged_attention(const PagedView& v, const void* q_abs, const void
   pp.blocks = blocks;
   pp.top_k = top_k;
   pp.pairs = p.pairs;
+  // (one sequence: its pairs all walk it already, and 512 tokens behind 32768 rows lose 0-2 % to the idle pairs; lists of
+  // blocks differ from token to token; the look at every cu_q in every block is for batches, not for millions)
+  pp.gangs = !blocks && v.B > 1 && v.total_q > v.B && v.B <= 4096;
   pp.tinfo = s.tinfo;
   pp.cost = s.cost;
   pp.pinfo = s.pinfo;

@@ -48,6 +48,26 @@ def test_attention(mods, dtype, page, lens, tq):
     c.check_attention(o, lse, prefix(c))
 
 
+@pytest.mark.parametrize("B,n,hi,pad", [(2, 2, 700, 0), (9, 2, 2500, 3), (40, 2, 300, 0), (7, 3, 900, 1), (3, 5, 1300, 0),
+                                        (13, 7, 400, 2), (4, 16, 700, 0), (5, 14, 333, 0), (2, 11, 5000, 0)])
+def test_attention_even_batches(mods, B, n, hi, pad):
+    """The same number of new tokens everywhere, lengths from none behind them to hi: the walk's other orders."""
+    c = Case("bf16", 16, [n + (hi - n) * b // max(B - 1, 1) for b in range(B)], [n] * B, seed=62 + n, pad=pad)
+    o, lse = (torch.full((c.T + pad, 128, *w), 7.0, dtype=dt, device="cuda")
+              for w, dt in (((512,), torch.bfloat16), ((), torch.float32)))
+    mods["bf16"].attn_paged(c.batch(), c.q_abs, c.q_rope, o, lse)
+    ok(mods["bf16"])
+    c.check_attention(o, lse, prefix(c))
+    assert (o[c.T:] == 7).all() and (lse[c.T:] == 7).all()
+    c.d_lens[1] = n - 1                                    # fewer rows than new tokens
+    mods["bf16"].attn_paged(c.batch(), c.q_abs, c.q_rope, o, lse)
+    flagged(mods["bf16"], 1 << 1)
+    assert (o[n:2 * n] == 0).all() and torch.isneginf(lse[n:2 * n]).all()
+    tokens = c.tokens()
+    c.tokens = lambda: [x for x in tokens if x[1] != 1]
+    c.check_attention(o, lse, prefix(c))
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_attention_many_short_sequences(mods, dtype):
     c = Case(dtype, 16, [1 + 7 * i % 90 for i in range(200)], [1] * 200, seed=3)
