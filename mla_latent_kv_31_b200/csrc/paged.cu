@@ -22,7 +22,8 @@ __device__ __forceinline__ void rope_angle(const RopeTable& rt, const LayerOpts&
 // ---- append -----------------------------------------------------------------------------------------------
 // One block per new token: its row [c | R_pos k] into its page and, with q, its n_h rotated queries. The bytes bound it
 // for long chunks (a token's 2 x 1152 + 2 x 16384 at the DeepSeek-V3 sizes), the chain lookup - sine - store else,
-// so every load is issued before the lookup and the angles (in double) are taken by one warp.
+// so every load is issued before the lookup and the angles (in double) are taken by one warp. With the summaries, 16
+// tokens take 8.5 us; five chunks of 2703 tokens together 25 us (95 MB: 3.8 TB/s).
 __device__ __forceinline__ uint4 rotate8(uint4 u, const float2* cs, float mul) {       // 4 pairs of bf16
   uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -237,7 +238,8 @@ __global__ void __launch_bounds__(512) summarise_kernel(PagedView v, int group, 
 // ---- attention by CUDA cores --------------------------------------------------------------------------------
 // The fp32 configuration (tcgen05 has no fp32 product): one block per (token, head). Rows come through shared memory,
 // `chunk` at a time (what fits 64 KB), so that global reads are contiguous; two threads share a key's product, and
-// the 256 threads split into groups of d_c threads that share the chunk's keys in P.V.
+// the 256 threads split into groups of d_c threads that share the chunk's keys in P.V. Latency bounds it at small sizes:
+// 9 sequences of 33 to 700 rows, 1 to 5 tokens each, d_c = 64 and 4 heads take 25 us.
 constexpr int ATT = 256;
 constexpr int ATT_SMEM = 65536;
 __global__ void __launch_bounds__(ATT)

@@ -9,12 +9,22 @@
 // 256 columns for two score buffers of 64 heads x 256 keys. So softmax, P and O of a head stay in one SM
 // and nothing but the shared B operands crosses between the two: each CTA loads half of the keys for QK^T
 // (128 keys x 576) and half of the latent columns for P.V (256 keys x 256): 272 KB per 256 keys, against
-// 16 x 36 and 2 x 16 x 4 MMAs of N = 256. (An M = 128 pair MMA takes 78 cycles at N = 256 and 68 at N = 128,
-// measured: the 256-key step is what keeps the tensor cores near their rate.)
+// 36 and 32 MMAs of N = 256. (An M = 128 pair MMA of K = 16 takes 64 cycles at N = 256, 32 at N = 128, measured: 4357 a
+// step. The loads take about 4200 of 66 bytes a cycle and SM. With both under way a step takes 7000 to 8000.)
+//
+// What it reaches. 8 x 64 tokens behind 16384 rows: 1160 TFLOP/s, 2.0 ms; 64 x 4 behind 16896 rows 1210, 64 x 2 1160
+// (0.52 ms), its rows read once from HBM; 4 single tokens over 131072 rows 3.8 TB/s (161 us), 16 over 4096 rows 41 us:
+// there the chain plan - first rows - last partial - merge takes half of the time. No unit is at its limit (64 x 2 behind
+// 2048 rows: tensor pipe 52 %, HBM 30 %): a step is held by the hand-offs through a ring of 112 KB that cannot grow
+// (rings of 5 or 6 entries are 2 to 8 % slower), and by L2's latency (rows shared by all sequences: 1240 to 1290).
+// Measured and not kept: a ring and an issuing warp each for K and V (1184 -> 1041 TFLOP/s), unrolled MMA loops and waits
+// for several entries at once (0 to 8 % slower), the next step's rows prefetched to L2 by copies or loads (3 % slower and
+// more), 64 score columns a thread in registers (the same time, 128 registers instead of 94).
 //
 // Work split. Tokens are cut into units of a step's 256 keys; all units of all tokens, plus a fixed cost per token,
-// are dealt to the pairs in equal contiguous ranges of at least kMinRange. A token that lies in one range is written by its pair; one
-// that crosses ranges leaves an unnormalised fp32 partial per range, merged exactly by combine_kernel.
+// are dealt to the pairs in equal contiguous ranges of at least kMinRange. A token that lies in one range is written by
+// its pair; one that crosses ranges leaves an unnormalised fp32 partial per range, merged exactly by
+// paged_combine_kernel. (Gangs, below: the order in which the tokens are dealt.)
 //
 // Pages. A step's 256 keys are 16 groups of 16 keys; each group's row in the pool comes from the block table (and
 // the token's block list). TMA boxes are 64, 32 or 16 rows high, the largest that divides the page size, so a
@@ -26,8 +36,9 @@
 // MMAs take them (K of step j + 1 before V of step j; one thread issues a copy every 500 cycles or so, the copies
 // take 270), and warp 2 loads a token's queries; warp 1 of the leader CTA issues the MMAs;
 // these run warp-uniform code with one elected lane at each TMA, MMA and commit (a lane-0 branch around the
-// whole loop cost 650 cycles a ring entry, three times what the copies take); warps 4-11 are the softmax (thread = TMEM lane, two warps per lane quarter, 64 keys each) and rescale O when the running
-// maximum has grown by 2^8; warps 12-15 write O out while the next token's first step runs.
+// whole loop cost 650 cycles a ring entry, three times what the copies take); warps 4-11 are the softmax (thread = TMEM
+// lane, two warps per lane quarter, 64 keys each) and rescale O when the running maximum has grown by 2^8; warps 12-15
+// write O out while the next token's first step runs.
 // Every wait is bounded (a timeout sets the error word and the role returns).
 #include <cuda_bf16.h>
 #include <string.h>
@@ -50,7 +61,9 @@ constexpr int GROUPS = NK / 16;                // a step's rows are looked up in
 constexpr int kThreads = 512;
 constexpr int kMaxPairs = 74;
 constexpr int kStartUnits = 1;                 // a token's fixed cost (query load, epilogue), in units
-constexpr int kMinRange = 2;                   // a pair's smallest range, in units and start costs
+// A pair's smallest range, in units and start costs: one token over 4096 rows takes 25 us with 2, 28 with 3, 31 with 4
+// (49 when its 64-key quarters were dealt to 64 pairs); 16 over 512 rows take 22, 20 and 28.
+constexpr int kMinRange = 2;
 constexpr int64_t kPlanTokens = 64;            // tokens looked up in the plan's own launch
 constexpr float kRescaleLog2 = 8.f;            // keep the running maximum until it grows by 2^8
 constexpr int kEntriesK = 9, kEntriesV = 8;    // ring entries of a step: [128 keys x 64], 2 x [64 keys x 64]

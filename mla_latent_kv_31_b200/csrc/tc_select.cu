@@ -6,9 +6,10 @@
 // select_score_kernel a CTA keeps one tile of 128 blocks of a sequence in shared memory (gathered by cp.async: its rows lie
 // anywhere) and runs over the sequence's tokens, whose codes stream in by TMA (80 KB each): M = 128 blocks, N = 128
 // heads, K = 576 in 18 MMAs of K = 32. With the blocks on the lanes the maximum over the heads stays in a thread.
-// The products bound it: kind::i8 runs an M128 N128 K32 MMA in 128 cycles (half of the rate of fp8), 2304 a token and
+// The products bound it: kind::i8 runs an M128 N128 K32 MMA in 128 cycles (measured; half of fp8's nominal rate), 2304 a token and
 // tile; 512 tokens over 2048 blocks take 100 us, 74 % of the tensor pipe's time (70 us), the conversions of the sums to
-// fp32 61 % of the XU's. 512 tokens over 512 blocks: codes 20-30 us (110 MB), scores 35, choice 16; 80 in one call.
+// fp32 61 % of the XU's. 512 tokens over 512 blocks: codes 20-30 us (110 MB), scores 35, choice 14; 75 in one call.
+// 4 tokens over 2048 blocks: 19 us, the latency of the three launches.
 // (Quantising inside the scoring kernel, a token's codes kept and the tiles streamed past, took 94 us there: 5 us of
 // arithmetic a token, and a gather's latency for every tile.)
 #include <cuda_bf16.h>
