@@ -24,7 +24,7 @@
 // Work split. Tokens are cut into units of a step's 256 keys; all units of all tokens, plus a fixed cost per token,
 // are dealt to the pairs in equal contiguous ranges of at least kMinRange. A token that lies in one range is written by
 // its pair; one that crosses ranges leaves an unnormalised fp32 partial per range, merged exactly by
-// paged_combine_kernel. (Gangs, below: the order in which the tokens are dealt.)
+// paged_combine_kernel. (The order in which tokens are dealt: order_of().)
 //
 // Pages. A step's 256 keys are 16 groups of 16 keys; each group's row in the pool comes from the block table (and
 // the token's block list). TMA boxes are 64, 32 or 16 rows high, the largest that divides the page size, so a
@@ -209,6 +209,10 @@ __device__ __forceinline__ bool wait_own(uint32_t bar, uint32_t parity) {
   }
 }
 
+// The slow half of a wait that is unrolled many times: one copy, a call away.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity) { return wait_own(bar, parity); }
+__device__ __forceinline__ bool wait_short(uint32_t bar, uint32_t parity) { return test_bar(bar, parity) || wait_slow(bar, parity); }
+
 // The tokens of a pair's range, and of each the keys [k0, k1) that fall into it.
 struct Walk {
   const int4* tinfo;
@@ -301,7 +305,13 @@ struct Rows {
 };
 
 // GRAN: rows of a TMA box, the largest of 64, 32, 16 that divides the page size.
-template <int GRAN>
+// BURST: how the MMA warp goes through a step's entries. An entry at a time, all lanes wait for it and one issues: 380
+// cycles an entry, of which the MMAs take 256. With BURST one lane runs through all the entries of a product, unrolled:
+// a step takes 4600 cycles where the rows lie in L2 (512 tokens behind 16384 rows 1780 -> 1480 us, 1580 TFLOP/s), but where
+// they come from HBM the loads bunch up (64 x 2 behind 16896 rows 560 -> 606 us, 4 x 131072 162 -> 172). Between: 64 x 8
+// behind 8192 rows 970 -> 908, 16 x 8 behind 16384 560 -> 523, 64 x 4 behind 16896 the same. So: from 8 new tokens a
+// sequence on.
+template <int GRAN, bool BURST>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     paged_core_kernel(const __grid_constant__ CoreParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -461,46 +471,92 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       auto next_entry = [&]() {
         if (++slot == RING) { slot = 0; ph ^= 1; }
       };
+      auto advance = [&](int count) {         // 7 < count < 14
+        slot += count - RING;
+        ph ^= 1;
+        if (slot >= RING) { slot -= RING; ph ^= 1; }
+      };
+      auto qk_entry = [&](uint32_t d, int e, int s) {
+        const uint32_t a = q_lo + e * (BOX >> 4), b = k_lo + s * (ENTRY >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) pair_mma(d, a + 2 * kk, b + 2 * kk, id_qk, (e | kk) ? 1u : 0u);
+        pair_commit(bar(B_EMPTY + s));
+      };
+      auto pv_entry = [&](int e, int s, bool first) {
+        const uint32_t a = p_lo + (e >> 1) * (BOX >> 4), b = v_lo + s * (ENTRY >> 4);
+        const uint32_t keep = first && e < 2 ? 0u : 1u;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) pair_mma(tmem + 128 * (e & 1), a + 2 * kk, b + 128 * kk, id_pv, kk ? 1u : keep);
+        pair_commit(bar(B_EMPTY + s));
+      };
       auto qk = [&](int j) -> bool {
         const int sb = j & 1;
         if (!wait_all(bar(B_SFREE + sb), ((j >> 1) & 1) ^ 1)) return false;
+        tc_fence_after();
         const uint32_t d = tmem + 256 + 128 * sb;
-        for (int e = 0; e < kEntriesK; ++e) {
-          if (!wait_all(bar(B_FULL + slot), ph)) return false;
-          tc_fence_after();
-          const uint32_t a = q_lo + e * (BOX >> 4), b = k_lo + slot * (ENTRY >> 4);
+        if constexpr (BURST) {
+          if (!wait_all(bar(B_FULL + slot), ph)) return false;       // (all lanes: 4 % faster than in the loop)
+          bool good = true;
           if (elect_one()) {
+            int s = slot, par = ph;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) pair_mma(d, a + 2 * kk, b + 2 * kk, id_qk, (e | kk) ? 1u : 0u);
-            pair_commit(bar(B_EMPTY + slot));
-            if (e == kEntriesK - 1) pair_commit(bar(B_SFULL + sb));
+            for (int e = 0; e < kEntriesK; ++e) {
+              good = wait_short(bar(B_FULL + s), par);
+              if (!good) break;
+              qk_entry(d, e, s);
+              if (++s == RING) { s = 0; par ^= 1; }
+            }
+            if (good) pair_commit(bar(B_SFULL + sb));
           }
-          __syncwarp();
-          next_entry();
+          advance(kEntriesK);
+          return __all_sync(0xffffffffu, good) != 0;
+        } else {
+          for (int e = 0; e < kEntriesK; ++e) {
+            if (!wait_all(bar(B_FULL + slot), ph)) return false;
+            if (elect_one()) {
+              qk_entry(d, e, slot);
+              if (e == kEntriesK - 1) pair_commit(bar(B_SFULL + sb));
+            }
+            __syncwarp();
+            next_entry();
+          }
+          return true;
         }
-        return true;
       };
       auto pv = [&](int j, bool first, int tail_kq) -> bool {
         if (!wait_all(bar(B_PRDY), j & 1)) return false;
         if (first && !wait_all(bar(B_OFREE), (gpc & 1) ^ 1)) return false;
-        for (int e = 0; e < kEntriesV; ++e) {
-          const int kq = e >> 1;
-          if (!wait_all(bar(B_FULL + slot), ph)) return false;
-          if (kq == tail_kq && (e & 1) == 0 && !wait_all(bar(B_TRDY), tails++ & 1)) return false;
-          tc_fence_after();
-          const uint32_t a = p_lo + kq * (BOX >> 4), b = v_lo + slot * (ENTRY >> 4);
-          const uint32_t keep = first && kq == 0 ? 0u : 1u;
+        tc_fence_after();
+        if constexpr (BURST) {
+          bool good = true;
           if (elect_one()) {
+            int s = slot, par = ph;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              pair_mma(tmem + 128 * (e & 1), a + 2 * kk, b + 128 * kk, id_pv, kk ? 1u : keep);
-            pair_commit(bar(B_EMPTY + slot));
-            if (e == kEntriesV - 1) pair_commit(bar(B_PVD));
+            for (int e = 0; e < kEntriesV; ++e) {
+              good = wait_short(bar(B_FULL + s), par);
+              if (good && (e >> 1) == tail_kq && (e & 1) == 0) good = wait_short(bar(B_TRDY), tails & 1);
+              if (!good) break;
+              pv_entry(e, s, first);
+              if (++s == RING) { s = 0; par ^= 1; }
+            }
+            if (good) pair_commit(bar(B_PVD));
           }
-          __syncwarp();
-          next_entry();
+          if (tail_kq >= 0) ++tails;
+          advance(kEntriesV);
+          return __all_sync(0xffffffffu, good) != 0;
+        } else {
+          for (int e = 0; e < kEntriesV; ++e) {
+            if (!wait_all(bar(B_FULL + slot), ph)) return false;
+            if ((e >> 1) == tail_kq && (e & 1) == 0 && !wait_all(bar(B_TRDY), tails++ & 1)) return false;
+            if (elect_one()) {
+              pv_entry(e, slot, first);
+              if (e == kEntriesV - 1) pair_commit(bar(B_PVD));
+            }
+            __syncwarp();
+            next_entry();
+          }
+          return true;
         }
-        return true;
       };
       for (; ok && w.valid(); w.next(), ++gpc) {
         const int ns = w.steps(), rem = w.k1 - (w.k0 + (ns - 1) * NK);
@@ -722,7 +778,7 @@ struct PlanParams {
   PagedView v;
   const int32_t* blocks;
   int32_t top_k, pairs;
-  bool gangs;                 // whether the tokens may be reordered (see gang_of)
+  bool reorder;               // whether order_of() may change the order of the walk
   int4* tinfo;
   int64_t* cost;
   int4* pinfo;
@@ -733,28 +789,71 @@ struct PlanParams {
   uint32_t* err;
 };
 
-// Gangs. Pairs that run through the same rows at the same time read them from HBM once. Where every sequence has n new
-// tokens (draft-and-verify steps, even chunks), the order of the walk is changed: the n tokens of a sequence are cut into g
-// groups of n / g, and the walk takes the first group of every sequence, then the second of every sequence, and so on.
-// With a multiple of g pairs each group falls to as many pairs, and the i-th pairs of the g groups walk the same
-// sequences over the same keys, side by side. g: the largest divisor of n up to 12 that leaves at most 4 of 74 pairs
-// idle. Measured, the tokens' own order against gangs (B x n tokens, us): 64 x 2 behind 16896 rows 579 -> 521,
-// 64 x 4 1143 -> 993, 64 x 16 behind 4096 1340 -> 1135, 16 x 2 behind 4096 85 -> 75, 8 x 64 behind 16384 2270 -> 2010.
-// Returns n (0: no common one, the tokens' own order) and g, the same in all threads of the block.
-__device__ inline int2 gang_of(const PlanParams& p) {
-  if (!p.gangs) return make_int2(0, 1);
+// The order of the walk. Rows that several pairs read at the same time come from HBM once, so where sequences have several
+// new tokens each, these are not taken one after the other by one pair:
+// - Waves, from two tokens a pair on: pair i of n takes tokens i, n + i, 2 n + i, ..., so that all pairs are at the same
+//   few sequences at any time. For rows of two waves' sequences that L2 holds (kWaveRows). Measured, the tokens' own
+//   order or gangs against waves: 8 ragged chunks, 225 tokens, behind 15000 to 16300 rows 850 -> 803 us, 8 x 64 behind
+//   16384 1745 -> 1610 (gangs), 4 x 128 1880 -> 1680; with too many rows: 2 x 80 behind 65536 2400 -> 2680, 64 x 8 behind
+//   8192 1000 -> 1110, 16 x 16 behind 16384 the same.
+// - Gangs, where every sequence has n new tokens: these are cut into g groups of n / g, and the walk takes the first
+//   group of every sequence, then the second of every sequence, and so on. With a multiple of g pairs each group falls to
+//   as many pairs, and the i-th pairs of the g groups walk the same sequences over the same keys, side by side. g:
+//   the largest divisor of n up to 12 that leaves at most 4 of 74 pairs idle. Measured, the tokens' own order against
+//   gangs: 64 x 2 behind 16896 rows 579 -> 521 us, 64 x 4 1143 -> 993, 64 x 16 behind 4096 1340 -> 1135, 16 x 2
+//   behind 4096 85 -> 75.
+constexpr int64_t kWaveRows = 100000000 / ((DC + DR) * 2);
+struct Order {
+  int n, g;                   // g > 1: gangs
+  int64_t waves;              // > 0: waves of this many tokens in all
+};
+// The same in all threads of the block (and in all blocks).
+__device__ inline Order order_of(const PlanParams& p) {
+  __shared__ unsigned long long rows_sh;
+  Order o = {0, 1, 0};
   const PagedView& v = p.v;
-  const int64_t end = v.cu_q[v.B], n = end / v.B;
-  bool even = n >= 2 && end == n * v.B && end <= v.total_q;
-  for (int64_t b = threadIdx.x; b < v.B; b += blockDim.x) even = even && v.cu_q[b] == b * n;
-  if (!__syncthreads_and(even)) return make_int2(0, 1);
-  int g = (int)min(n, (int64_t)12);
-  while (g > 1 && (n % g != 0 || p.pairs % g > p.pairs / 18)) --g;
-  return make_int2((int)n, g);
+  if (!p.reorder) return o;
+  const int64_t T = v.cu_q[v.B], n = T / v.B;
+  if (T <= v.B || T > v.total_q) return o;
+  if (threadIdx.x == 0) rows_sh = 0;
+  bool even = n * v.B == T;
+  unsigned long long rows = 0;
+  for (int64_t b = threadIdx.x; b < v.B; b += blockDim.x) {
+    const int64_t q0 = v.cu_q[b];
+    even = even && q0 == b * n;
+    if (v.cu_q[b + 1] > q0) rows += (unsigned long long)min(max(v.kv_lens[b], (int64_t)0), v.max_pages * v.page);
+  }
+  even = __syncthreads_and(even);
+  if (rows) atomicAdd(&rows_sh, rows);
+  __syncthreads();
+  const int64_t all = (int64_t)rows_sh;
+  if (T >= 2 * p.pairs && all / T * (2 * p.pairs) <= kWaveRows) {
+    o.waves = T;
+  } else if (even) {
+    o.n = (int)n;
+    o.g = (int)min(n, (int64_t)12);
+    while (o.g > 1 && (n % o.g != 0 || p.pairs % o.g > p.pairs / 18)) --o.g;
+  }
+  return o;
+}
+// Where token t of sequence seq stands in it: a permutation of [0, T) for any contents of cu_q.
+__device__ inline int64_t place_of(const PlanParams& p, const Order& o, int64_t t, int64_t seq) {
+  if (o.waves > t) {
+    // pair i's column begins at i T / pairs and holds T / pairs tokens or one more; those come last
+    const int64_t T = o.waves, n = p.pairs, depth = T / n, rest = T % n, i = t % n;
+    if (t < n * depth) return i * T / n + t / n;
+    const int64_t c = ((t - n * depth + 1) * n + rest - 1) / rest - 1;
+    return c * T / n + depth;
+  }
+  if (o.g > 1 && t < (int64_t)o.n * p.v.B) {
+    const int64_t per = o.n / o.g, k = t - seq * o.n;
+    return (k / per * p.v.B + seq) * per + k % per;
+  }
+  return t;
 }
 
 // Sequence and visible rows of new token t, by one warp; an empty row is written here.
-__device__ __forceinline__ void plan_token(const PlanParams& p, int64_t t, int2 gang, int lane) {
+__device__ __forceinline__ void plan_token(const PlanParams& p, int64_t t, const Order& order, int lane) {
   const PagedView& v = p.v;
   const PagedToken tok = paged_token(v, t);
   int64_t vis = tok.pos + 1;
@@ -779,14 +878,8 @@ __device__ __forceinline__ void plan_token(const PlanParams& p, int64_t t, int2 
     }
     vis = n == 0 ? 0 : (int64_t)(n - 1) * v.page + (at == own ? tok.pos % v.page + 1 : v.page);
   }
-  if (lane == 0) {
-    int64_t at = t;
-    if (gang.y > 1 && tok.seq >= 0) {
-      const int per = gang.x / gang.y, k = (int)(t - (int64_t)tok.seq * gang.x);
-      at = ((int64_t)(k / per) * v.B + tok.seq) * per + k % per;
-    }
-    p.tinfo[at] = make_int4(tok.seq, (int32_t)(tok.seq < 0 ? 0 : vis), (int32_t)t, 0);
-  }
+  if (lane == 0)
+    p.tinfo[place_of(p, order, t, tok.seq)] = make_int4(tok.seq, (int32_t)(tok.seq < 0 ? 0 : vis), (int32_t)t, 0);
   if (tok.seq >= 0 && vis <= 0) {
     uint4* o = reinterpret_cast<uint4*>(p.o_lat + t * H * DC);
     for (int i = lane; i < H * DC / 8; i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -798,13 +891,14 @@ __device__ __forceinline__ void plan_token(const PlanParams& p, int64_t t, int2 
 __global__ void __launch_bounds__(256) paged_tokens_kernel(const __grid_constant__ PlanParams p) {
   let_next_start();
   if (blockIdx.x == 0) paged_check(p.v, p.err);
-  const int2 gang = gang_of(p);
+  const Order order = order_of(p);
   const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (t < p.v.total_q) plan_token(p, t, gang, threadIdx.x & 31);
+  if (t < p.v.total_q) plan_token(p, t, order, threadIdx.x & 31);
 }
 
-// Deals the tokens' units to the pairs (one block; with TOKENS it also looks the tokens up first). In cost, token t with u_t > 0 units is kStartUnits + u_t
-// long; of n = min(pairs, total / kMinRange) pairs, pair pp's range begins at the first unit whose cost starts at or
+// Deals the tokens' units to the pairs (one block; with TOKENS it also looks the tokens up first). In cost, token t with
+// u_t > 0 units is kStartUnits + u_t long; of n = min(pairs, total / kMinRange) pairs, pair pp's range begins at the
+// first unit whose cost starts at or
 // after pp * total / n. (A unit never starts two costs behind the one before, so no range of kMinRange is empty.) Each
 // pair's range is written as (first token, its first unit, last token, its end unit), (-1, ...) if it has none.
 template <bool TOKENS>
@@ -819,10 +913,10 @@ __global__ void __launch_bounds__(1024) paged_plan_kernel(const __grid_constant_
   int4* tinfo = p.tinfo;
   int64_t* cost = p.cost;
   let_next_start();
-  const int2 gang = gang_of(p);
+  const Order order = order_of(p);
   if (TOKENS) {
     paged_check(p.v, p.err);
-    for (int64_t t = warp; t < T; t += 32) plan_token(p, t, gang, lane);
+    for (int64_t t = warp; t < T; t += 32) plan_token(p, t, order, lane);
     __syncthreads();
   } else {
     wait_for_previous();
@@ -860,7 +954,7 @@ __global__ void __launch_bounds__(1024) paged_plan_kernel(const __grid_constant_
   __syncthreads();
   // the boundaries: the first token whose end lies behind the boundary's cost, and the unit in it
   int used = (int)max((int64_t)1, min((int64_t)pairs, total / kMinRange));
-  if (used >= gang.y) used -= used % gang.y;
+  if (used >= order.g) used -= used % order.g;
   for (int pp = tid; pp <= used; pp += blockDim.x) {
     const int64_t c = total * pp / used;
     int64_t a = 0, b = T;                     // the last token with cost <= c
@@ -964,12 +1058,16 @@ __global__ void __launch_bounds__(256)
       make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
 }
 
-template <int GRAN>
+template <int GRAN, bool BURST>
 cudaError_t launch_core(const CoreParams& p, cudaStream_t st) {
   // per device, so set at every call
-  cudaError_t e = cudaFuncSetAttribute(paged_core_kernel<GRAN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+  cudaError_t e = cudaFuncSetAttribute(paged_core_kernel<GRAN, BURST>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  return launch_next(paged_core_kernel<GRAN>, dim3(2 * p.pairs), kThreads, SMEM_BYTES, st, p);
+  return launch_next(paged_core_kernel<GRAN, BURST>, dim3(2 * p.pairs), kThreads, SMEM_BYTES, st, p);
+}
+template <int GRAN>
+cudaError_t launch_core(const CoreParams& p, bool burst, cudaStream_t st) {
+  return burst ? launch_core<GRAN, true>(p, st) : launch_core<GRAN, false>(p, st);
 }
 
 size_t align1k(size_t x) { return (x + 1023) / 1024 * 1024; }
@@ -1043,7 +1141,7 @@ cudaError_t tc_paged_attention(const PagedView& v, const void* q_abs, const void
   pp.pairs = p.pairs;
   // (one sequence: its pairs all walk it already, and 512 tokens behind 32768 rows lose 0-2 % to the idle pairs; lists of
   // blocks differ from token to token; the look at every cu_q in every block is for batches, not for millions)
-  pp.gangs = !blocks && v.B > 1 && v.total_q > v.B && v.B <= 4096;
+  pp.reorder = !blocks && v.B > 1 && v.total_q > v.B && v.B <= 4096;
   pp.tinfo = s.tinfo;
   pp.cost = s.cost;
   pp.pinfo = s.pinfo;
@@ -1064,7 +1162,8 @@ cudaError_t tc_paged_attention(const PagedView& v, const void* q_abs, const void
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if ((e = launch_next(paged_plan_kernel<false>, dim3(1), 1024, 0, st, pp)) != cudaSuccess) return e;
   }
-  e = gran == 64 ? launch_core<64>(p, st) : gran == 32 ? launch_core<32>(p, st) : launch_core<16>(p, st);
+  const bool burst = v.total_q >= 8 * v.B;
+  e = gran == 64 ? launch_core<64>(p, burst, st) : gran == 32 ? launch_core<32>(p, burst, st) : launch_core<16>(p, burst, st);
   if (e != cudaSuccess) return e;
   // at most one token per boundary, and no more than there are, goes on in the next pair's range
   const int64_t most = p.pairs - 1 < v.total_q ? p.pairs - 1 : v.total_q;

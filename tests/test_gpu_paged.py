@@ -49,7 +49,8 @@ def test_attention(mods, dtype, page, lens, tq):
 
 
 @pytest.mark.parametrize("B,n,hi,pad", [(2, 2, 700, 0), (9, 2, 2500, 3), (40, 2, 300, 0), (7, 3, 900, 1), (3, 5, 1300, 0),
-                                        (13, 7, 400, 2), (4, 16, 700, 0), (5, 14, 333, 0), (2, 11, 5000, 0)])
+                                        (13, 7, 400, 2), (4, 16, 700, 0), (5, 14, 333, 0), (2, 11, 5000, 0),
+                                        (3, 64, 300, 5), (2, 74, 200, 0)])
 def test_attention_even_batches(mods, B, n, hi, pad):
     """The same number of new tokens everywhere, lengths from none behind them to hi: the walk's other orders."""
     c = Case("bf16", 16, [n + (hi - n) * b // max(B - 1, 1) for b in range(B)], [n] * B, seed=62 + n, pad=pad)
@@ -65,6 +66,20 @@ def test_attention_even_batches(mods, B, n, hi, pad):
     assert (o[n:2 * n] == 0).all() and torch.isneginf(lse[n:2 * n]).all()
     tokens = c.tokens()
     c.tokens = lambda: [x for x in tokens if x[1] != 1]
+    c.check_attention(o, lse, prefix(c))
+
+
+def test_attention_uneven_chunks_of_many_tokens(mods):
+    """Two to four tokens a pair of CTAs, sequences of 0 to 64 new tokens, one of them flagged."""
+    tq = [50, 0, 64, 1, 33, 7, 40, 20]
+    c = Case("bf16", 32, [300, 40, 64, 500, 33, 600, 41, 290], tq, seed=63, pad=2)
+    c.d_lens[6] = 39                                       # fewer rows than new tokens
+    o, lse = mods["bf16"].attn_paged(c.batch(), c.q_abs, c.q_rope)
+    flagged(mods["bf16"], 1 << 1)
+    a, b = int(c.cu[6]), int(c.cu[7])
+    assert (o[a:b] == 0).all() and torch.isneginf(lse[a:b]).all()
+    tokens = [x for x in c.tokens() if x[1] != 6]
+    c.tokens = lambda: tokens
     c.check_attention(o, lse, prefix(c))
 
 
