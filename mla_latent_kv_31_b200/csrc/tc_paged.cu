@@ -12,14 +12,16 @@
 // 36 and 32 MMAs of N = 256. (An M = 128 pair MMA of K = 16 takes 64 cycles at N = 256, 32 at N = 128, measured: 4357 a
 // step. The loads take about 4200 of 66 bytes a cycle and SM. With both under way a step takes 7000 to 8000.)
 //
-// What it reaches. 8 x 64 tokens behind 16384 rows: 1160 TFLOP/s, 2.0 ms; 64 x 4 behind 16896 rows 1210, 64 x 2 1160
-// (0.52 ms), its rows read once from HBM; 4 single tokens over 131072 rows 3.8 TB/s (161 us), 16 over 4096 rows 41 us:
-// there the chain plan - first rows - last partial - merge takes half of the time. No unit is at its limit (64 x 2 behind
-// 2048 rows: tensor pipe 52 %, HBM 30 %): a step is held by the hand-offs through a ring of 112 KB that cannot grow
-// (rings of 5 or 6 entries are 2 to 8 % slower), and by L2's latency (rows shared by all sequences: 1240 to 1290).
-// Measured and not kept: a ring and an issuing warp each for K and V (1184 -> 1041 TFLOP/s), unrolled MMA loops and waits
-// for several entries at once (0 to 8 % slower), the next step's rows prefetched to L2 by copies or loads (3 % slower and
-// more), 64 score columns a thread in registers (the same time, 128 registers instead of 94).
+// What it reaches. 512 tokens of one sequence behind 32768 rows: 1490 TFLOP/s; 8 x 64 behind 16384 rows 1300 to 1450 (1.6
+// to 1.75 ms), 64 x 4 behind 16896 rows 1190, 64 x 2 1140 (0.53 ms), the rows read once from HBM; 4 single tokens over
+// 131072 rows 3.8 TB/s (160 us), 16 over 4096 rows 41 us: there the chain plan - first rows - last partial - merge takes
+// half of the time. Where rows come from L2 a step takes 4600 cycles, MMAs and loads both near their rates; where they
+// come from HBM 7000 to 8500 and no unit is at its limit (64 x 2 behind 2048 rows: tensor pipe 52 %, HBM 30 %): the
+// ring of 112 KB, which cannot grow, holds what is on its way for 2 us or so.
+// Measured and not kept: a ring and an issuing warp each for K and V (1184 -> 1041 TFLOP/s), waits for several entries at
+// once (0 to 8 % slower), P handed over 64 keys at a time (5 % slower: each wait and commit of the MMA warp counts), the
+// next step's rows prefetched to L2 by copies or loads (3 % slower and more), 64 score columns a thread in registers
+// (the same time, 128 registers instead of 94).
 //
 // Work split. Tokens are cut into units of a step's 256 keys; all units of all tokens, plus a fixed cost per token,
 // are dealt to the pairs in equal contiguous ranges of at least kMinRange. A token that lies in one range is written by
@@ -898,9 +900,9 @@ __global__ void __launch_bounds__(256) paged_tokens_kernel(const __grid_constant
 
 // Deals the tokens' units to the pairs (one block; with TOKENS it also looks the tokens up first). In cost, token t with
 // u_t > 0 units is kStartUnits + u_t long; of n = min(pairs, total / kMinRange) pairs, pair pp's range begins at the
-// first unit whose cost starts at or
-// after pp * total / n. (A unit never starts two costs behind the one before, so no range of kMinRange is empty.) Each
-// pair's range is written as (first token, its first unit, last token, its end unit), (-1, ...) if it has none.
+// first unit whose cost starts at or after pp * total / n. (A unit never starts two costs behind the one before, so no
+// range of kMinRange is empty.) Each pair's range is written as (first token, its first unit, last token, its end unit),
+// (-1, ...) if it has none.
 template <bool TOKENS>
 __global__ void __launch_bounds__(1024) paged_plan_kernel(const __grid_constant__ PlanParams p) {
   __shared__ int64_t warp_tot[32];
