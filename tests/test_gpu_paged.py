@@ -562,6 +562,50 @@ def test_a_batch_without_new_tokens_leaves_everything_as_it_was(mods, dtype, T):
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_pages_far_into_a_large_pool(mods, dtype):
+    """Rows whose element offsets pass 2^32: every call at the end of a pool of 9 GB."""
+    m = mods[dtype]
+    c = Case(dtype, 64, [300, 64, 190], [3, 1, 62], seed=64)
+    d, far = c.dims, 9 * 2 ** 30 // (64 * c.W * c.cache.element_size())
+    assert far * 64 * c.W > 2 ** 31
+    small, c.cache = c.cache, torch.empty(far + c.num_pages, 64, c.W, dtype=DT[dtype], device="cuda")
+    c.cache[far:] = small
+    c.d_table = c.d_table + far * (c.d_table >= 0).int()
+    kv, sums = c.on(c.normal(c.T, c.W)), m.new_summaries(far + c.num_pages)
+    q_rope = m.paged_append(c.batch(), kv, q_rope=c.q_rope, summaries=sums)
+    c.q[..., d.d_c:] = q_rope.double().cpu()
+    blocks = m.paged_select(c.batch(), c.q_abs, q_rope, sums, 3, 0, 1)
+    o, lse = m.attn_paged(c.batch(), c.q_abs, q_rope)
+    o2, lse2 = m.attn_paged_sparse(c.batch(), c.q_abs, q_rope, blocks)
+    ok(m)
+    pool = c.cache[far:].double().cpu()
+    c.rows = [pool[c.table[b, torch.arange(n) // 64].long(), torch.arange(n) % 64] for b, n in enumerate(c.lens)]
+    c.check_attention(o, lse, prefix(c))
+    c.check_attention(o2, lse2, listed_rows(c, blocks.cpu()))
+    done = sorted({int(c.table[b, pos // 64]) for _, b, pos in c.tokens() if pos % 64 == 63})
+    assert torch.equal(sums[far:].cpu()[done], c.summaries((pool[done].sum(1) / 64).float().double()))
+    assert not sums[:far].any()
+
+
+@pytest.mark.parametrize("dtype,times", [("fp32", 16), ("bf16", 1024)])
+def test_attention_over_a_long_table_of_the_same_pages(mods, dtype, times):
+    """The same 1024 rows over and over: the same weighted mean, ln(times) more in the logarithm of the sum."""
+    m = mods[dtype]
+    c = Case(dtype, 64, [1024], [1], seed=65, spare=0)
+    n = 1024 * times
+    b = mla.PagedBatch(c.cache, c.d_table[:, :16].repeat(1, times), c.d_cu, torch.tensor([n], device="cuda"), 1)
+    o, lse = m.attn_paged(b, c.q_abs, c.q_rope)
+    ok(m)
+    ro, rl, A, gamma = c.attend(0, c.rows[0])
+    # as in check_attention; bf16 sums 4096 steps of 256 rows in 74 ranges, then the 74 partials
+    terms = n if dtype == "fp32" else 56 * 256 + 74
+    rel = 2 * gamma + 2.0 ** -18 + terms * 2.0 ** -23 + (HALF["bf16"] if dtype == "bf16" else 0.0)
+    assert ((o[0].double().cpu() - ro).abs() <= rel[:, None] * A + HALF[dtype] * ro.abs() * (1 + rel[:, None])).all()
+    want = rl + torch.tensor(float(times), dtype=torch.float64).log()
+    assert ((lse[0].double().cpu() - want).abs() <= gamma + 2.0 ** -18 + terms * 2.0 ** -23 + 2.0 ** -23 * want.abs()).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_calls_and_graphs_side_by_side_on_two_streams(mods, dtype):
     """The same calls of one handle on two streams at once, eager and as two graphs: as when they run alone."""
     m = mods[dtype]

@@ -38,7 +38,8 @@ def calls(h, b):
                                   dict(B=0), dict(total_q=0), dict(num_pages=0), dict(max_pages=0),
                                   dict(table_stride=19), dict(page_size=0), dict(page_size=-16), dict(page_size=24),
                                   dict(page_size=8), dict(num_pages=1 << 31), dict(num_pages=(1 << 31) // 64),
-                                  dict(total_q=1 << 40), dict(B=1 << 30)])
+                                  dict(total_q=1 << 40), dict(B=1 << 30),
+                                  dict(max_pages=(1 << 24) + 1, table_stride=1 << 25)])    # more than 2^30 rows
 def test_bad_batches_are_refused(over):
     h = mla.mla_create(synth.V3)
     try:
