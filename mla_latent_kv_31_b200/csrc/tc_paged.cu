@@ -855,7 +855,7 @@ __device__ inline int64_t place_of(const PlanParams& p, const Order& o, int64_t 
 }
 
 // Sequence and visible rows of new token t, by one warp; an empty row is written here.
-__device__ __forceinline__ void plan_token(const PlanParams& p, int64_t t, const Order& order, int lane) {
+__device__ __forceinline__ void plan_token(const PlanParams& p, int64_t t, const Order& order, int lane, int4* also = nullptr) {
   const PagedView& v = p.v;
   const PagedToken tok = paged_token(v, t);
   int64_t vis = tok.pos + 1;
@@ -880,8 +880,12 @@ __device__ __forceinline__ void plan_token(const PlanParams& p, int64_t t, const
     }
     vis = n == 0 ? 0 : (int64_t)(n - 1) * v.page + (at == own ? tok.pos % v.page + 1 : v.page);
   }
-  if (lane == 0)
-    p.tinfo[place_of(p, order, t, tok.seq)] = make_int4(tok.seq, (int32_t)(tok.seq < 0 ? 0 : vis), (int32_t)t, 0);
+  if (lane == 0) {
+    const int64_t at = place_of(p, order, t, tok.seq);
+    const int4 info = make_int4(tok.seq, (int32_t)(tok.seq < 0 ? 0 : vis), (int32_t)t, 0);
+    p.tinfo[at] = info;
+    if (also) also[at] = info;
+  }
   if (tok.seq >= 0 && vis <= 0) {
     uint4* o = reinterpret_cast<uint4*>(p.o_lat + t * H * DC);
     for (int i = lane; i < H * DC / 8; i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -898,12 +902,111 @@ __global__ void __launch_bounds__(256) paged_tokens_kernel(const __grid_constant
   if (t < p.v.total_q) plan_token(p, t, order, threadIdx.x & 31);
 }
 
-// Deals the tokens' units to the pairs (one block; with TOKENS it also looks the tokens up first). In cost, token t with
-// u_t > 0 units is kStartUnits + u_t long; of n = min(pairs, total / kMinRange) pairs, pair pp's range begins at the
-// first unit whose cost starts at or after pp * total / n. (A unit never starts two costs behind the one before, so no
-// range of kMinRange is empty.) Each pair's range is written as (first token, its first unit, last token, its end unit),
-// (-1, ...) if it has none.
-template <bool TOKENS>
+// Dealing the tokens' units to the pairs. In cost, token t with u_t > 0 units is kStartUnits + u_t long; of
+// n = min(pairs, total / kMinRange) pairs, pair pp's range begins at the first unit whose cost starts at or after
+// pp * total / n. (A unit never starts two costs behind the one before, so no range of kMinRange is empty.) Each pair's
+// range is written as (first token, its first unit, last token, its end unit), (-1, ...) if it has none.
+__device__ __forceinline__ int units_of(const int4& info) { return (max(info.y, 0) + UNIT - 1) / UNIT; }
+__device__ __forceinline__ int weight_of(int units) { return units > 0 ? units + kStartUnits : 0; }
+__device__ __forceinline__ int pairs_used(const PlanParams& p, const Order& order, int64_t total) {
+  const int used = (int)max((int64_t)1, min((int64_t)p.pairs, total / kMinRange));
+  return used >= order.g ? used - used % order.g : used;
+}
+// Boundary pp: the first token whose end lies behind the boundary's cost, and the unit in it.
+template <typename Cost>
+__device__ __forceinline__ void deal_boundary(int pp, int used, int64_t total, int64_t T, const int4* tinfo, const Cost* cost,
+                                              int32_t* tok, int32_t* unit) {
+  const int64_t q = total / used, c = q * pp + (int)(total - q * used) * pp / used;      // total * pp / used
+  int64_t a = 0, b = T;                     // the last token with cost <= c
+  while (b - a > 1) {
+    const int64_t mid = (a + b) >> 1;
+    if (cost[mid] <= c) a = mid; else b = mid;
+  }
+  int u = (int)max((int64_t)0, c - cost[a] - kStartUnits);
+  if (pp == used || u >= units_of(tinfo[a])) {   // behind its last unit: the next token
+    ++a;
+    u = 0;
+    if (pp == used) a = T;
+  }
+  *tok = (int32_t)a;
+  *unit = u;
+}
+// Pair pp's range from the boundaries; returns its entry of splits, (-1, ...) if no token that goes on begins in it.
+template <typename Cost>
+__device__ __forceinline__ int4 deal_pair(const PlanParams& p, int pp, int used, int64_t total, int64_t T, const int4* tinfo,
+                                          const Cost* cost, const int32_t* btok, const int32_t* bunit) {
+  int4 split = make_int4(-1, 0, 0, 0), info = make_int4(-1, 0, -2, 0);
+  if (pp < used) {
+    int a = btok[pp], ua = bunit[pp], e = btok[pp + 1], ue = bunit[pp + 1];
+    while (a < T && units_of(tinfo[a]) == 0) { ++a; ua = 0; }       // tokens without units
+    if (ue == 0) {                                                  // ends with the token before
+      do --e; while (e >= 0 && units_of(tinfo[e]) == 0);
+      ue = e >= 0 ? units_of(tinfo[e]) : 0;
+    }
+    if (a < T && (a < e || (a == e && ua < ue))) {
+      info = make_int4(a, ua, e, ue);
+      p.pfirst[pp] = tinfo[a];
+      const int ne = units_of(tinfo[e]);
+      if (ue < ne && !(a == e && ua > 0))                           // e begins here and goes on: to its last unit's pair
+        split = make_int4(tinfo[e].z, 2 * pp + (a == e ? 0 : 1), pp,
+                          (int)(((int64_t)(cost[e] + kStartUnits + ne) * used - 1) / total));
+    }
+  }
+  p.pinfo[pp] = info;
+  return split;
+}
+// The pairs' entries to p.splits, the empty ones last, by one warp.
+__device__ __forceinline__ void write_splits(const PlanParams& p, int lane, const int4* begins) {
+  int n = 0;
+  for (int p0 = 0; p0 < p.pairs; p0 += 32) {
+    const int4 it = p0 + lane < p.pairs ? begins[p0 + lane] : make_int4(-1, 0, 0, 0);
+    const uint32_t m = __ballot_sync(0xffffffffu, it.x >= 0);
+    if (it.x >= 0) p.splits[n + __popc(m & ((1u << lane) - 1u))] = it;
+    n += __popc(m);
+  }
+  for (int k = n + lane; k < p.pairs; k += 32) p.splits[k] = make_int4(-1, 0, 0, 0);
+}
+
+// Few tokens: one block looks them up and deals them, from shared memory and without further trips to L2; a second block
+// checks the batch. (It stands in front of the whole chain. Through global memory, as below, it took 1.3 us more.)
+__global__ void __launch_bounds__(1024) paged_small_plan_kernel(const __grid_constant__ PlanParams p) {
+  __shared__ int4 tinfo[kPlanTokens];
+  __shared__ int32_t cost[kPlanTokens];
+  __shared__ int32_t btok[kMaxPairs + 1], bunit[kMaxPairs + 1];
+  __shared__ int4 begins[kMaxPairs];
+  constexpr int DEAL = (kMaxPairs + 1 + 31) / 32 * 32;          // threads that deal, a boundary or a pair each
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = (int)p.v.total_q;
+  let_next_start();
+  if (blockIdx.x == 1) {
+    paged_check(p.v, p.err);
+    return;
+  }
+  const Order order = order_of(p);
+  for (int t = warp; t < T; t += 32) plan_token(p, t, order, lane, tinfo);
+  __syncthreads();
+  if (tid >= DEAL) return;
+  int total = 0;                                                // (each of the warps finds the costs itself)
+  for (int t0 = 0; t0 < T; t0 += 32) {
+    const int w = t0 + lane < T ? weight_of(units_of(tinfo[t0 + lane])) : 0;
+    int x = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (warp == 0 && t0 + lane < T) cost[t0 + lane] = total + x - w;
+    total += __shfl_sync(0xffffffffu, x, 31);
+  }
+  const int used = pairs_used(p, order, total);
+  auto sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(DEAL) : "memory"); };
+  sync();
+  if (tid <= used) deal_boundary(tid, used, total, T, tinfo, cost, &btok[tid], &bunit[tid]);
+  sync();
+  if (tid < p.pairs) begins[tid] = deal_pair(p, tid, used, total, T, tinfo, cost, btok, bunit);
+  sync();
+  if (warp == 0) write_splits(p, lane, begins);
+}
+
 __global__ void __launch_bounds__(1024) paged_plan_kernel(const __grid_constant__ PlanParams p) {
   __shared__ int64_t warp_tot[32];
   __shared__ int64_t total;
@@ -911,24 +1014,15 @@ __global__ void __launch_bounds__(1024) paged_plan_kernel(const __grid_constant_
   __shared__ int4 begins[kMaxPairs];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t T = p.v.total_q;
-  const int pairs = p.pairs;
-  int4* tinfo = p.tinfo;
+  const int4* tinfo = p.tinfo;
   int64_t* cost = p.cost;
   let_next_start();
   const Order order = order_of(p);
-  if (TOKENS) {
-    paged_check(p.v, p.err);
-    for (int64_t t = warp; t < T; t += 32) plan_token(p, t, order, lane);
-    __syncthreads();
-  } else {
-    wait_for_previous();
-  }
-  auto units = [&](int64_t t) -> int { return (max(tinfo[t].y, 0) + UNIT - 1) / UNIT; };
-  auto weight = [&](int u) -> int { return u > 0 ? u + kStartUnits : 0; };
+  wait_for_previous();
   const int64_t per = (T + 1023) / 1024;
   const int64_t lo = min(T, tid * per), hi = min(T, lo + per);
   int64_t sum = 0;
-  for (int64_t t = lo; t < hi; ++t) sum += weight(units(t));
+  for (int64_t t = lo; t < hi; ++t) sum += weight_of(units_of(tinfo[t]));
   int64_t x = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -951,61 +1045,15 @@ __global__ void __launch_bounds__(1024) paged_plan_kernel(const __grid_constant_
   int64_t at = x - sum + (warp > 0 ? warp_tot[warp - 1] : 0);
   for (int64_t t = lo; t < hi; ++t) {
     cost[t] = at;
-    at += weight(units(t));
+    at += weight_of(units_of(tinfo[t]));
   }
   __syncthreads();
-  // the boundaries: the first token whose end lies behind the boundary's cost, and the unit in it
-  int used = (int)max((int64_t)1, min((int64_t)pairs, total / kMinRange));
-  if (used >= order.g) used -= used % order.g;
-  for (int pp = tid; pp <= used; pp += blockDim.x) {
-    const int64_t c = total * pp / used;
-    int64_t a = 0, b = T;                     // the last token with cost <= c
-    while (b - a > 1) {
-      const int64_t mid = (a + b) >> 1;
-      if (cost[mid] <= c) a = mid; else b = mid;
-    }
-    int u = (int)max((int64_t)0, c - cost[a] - kStartUnits);
-    if (pp == used || u >= units(a)) {        // behind its last unit: the next token
-      ++a;
-      u = 0;
-      if (pp == used) a = T;
-    }
-    btok[pp] = (int32_t)a;
-    bunit[pp] = u;
-  }
+  const int used = pairs_used(p, order, total);
+  for (int pp = tid; pp <= used; pp += blockDim.x) deal_boundary(pp, used, total, T, tinfo, cost, &btok[pp], &bunit[pp]);
   __syncthreads();
-  for (int pp = tid; pp < pairs; pp += blockDim.x) {
-    begins[pp] = make_int4(-1, 0, 0, 0);
-    if (pp >= used) {
-      p.pinfo[pp] = make_int4(-1, 0, -2, 0);
-      continue;
-    }
-    int a = btok[pp], e = btok[pp + 1], ue = bunit[pp + 1];
-    int ua = bunit[pp];
-    while (a < T && units(a) == 0) { ++a; ua = 0; }         // tokens without units
-    if (ue == 0) {                                         // ends with the token before
-      do --e; while (e >= 0 && units(e) == 0);
-      ue = e >= 0 ? units(e) : 0;
-    }
-    const bool any = a < T && (a < e || (a == e && ua < ue));
-    p.pinfo[pp] = any ? make_int4(a, ua, e, ue) : make_int4(-1, 0, -2, 0);
-    if (any) p.pfirst[pp] = tinfo[a];
-    if (any && ue < units(e) && !(a == e && ua > 0)) {       // e begins here and goes on: to the pair of its last unit
-      const int64_t at_last = cost[e] + kStartUnits + units(e) - 1;
-      begins[pp] = make_int4(tinfo[e].z, 2 * pp + (a == e ? 0 : 1), pp, (int)(((at_last + 1) * used - 1) / total));
-    }
-  }
+  for (int pp = tid; pp < p.pairs; pp += blockDim.x) begins[pp] = deal_pair(p, pp, used, total, T, tinfo, cost, btok, bunit);
   __syncthreads();
-  if (warp == 0) {
-    int n = 0;
-    for (int p0 = 0; p0 < pairs; p0 += 32) {
-      const int4 it = p0 + lane < pairs ? begins[p0 + lane] : make_int4(-1, 0, 0, 0);
-      const uint32_t m = __ballot_sync(0xffffffffu, it.x >= 0);
-      if (it.x >= 0) p.splits[n + __popc(m & ((1u << lane) - 1u))] = it;
-      n += __popc(m);
-    }
-    for (int k = n + lane; k < pairs; k += 32) p.splits[k] = make_int4(-1, 0, 0, 0);
-  }
+  if (warp == 0) write_splits(p, lane, begins);
 }
 
 // Exact merge of the tokens that cross ranges. Block (k, heads, columns) takes the k-th of them:
@@ -1155,14 +1203,14 @@ cudaError_t tc_paged_attention(const PagedView& v, const void* q_abs, const void
   // One block looks up few tokens in the plan's own launch; each of its 32 warps takes a token in about 1 us (a list of
   // blocks is read for it), so more than kPlanTokens of them get a launch of their own.
   if (v.total_q <= kPlanTokens) {
-    paged_plan_kernel<true><<<1, 1024, 0, st>>>(pp);
+    paged_small_plan_kernel<<<2, 1024, 0, st>>>(pp);
     note_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   } else {
     paged_tokens_kernel<<<(unsigned)((v.total_q + 7) / 8), 256, 0, st>>>(pp);
     note_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if ((e = launch_next(paged_plan_kernel<false>, dim3(1), 1024, 0, st, pp)) != cudaSuccess) return e;
+    if ((e = launch_next(paged_plan_kernel, dim3(1), 1024, 0, st, pp)) != cudaSuccess) return e;
   }
   const bool burst = v.total_q >= 8 * v.B;
   e = gran == 64 ? launch_core<64>(p, burst, st) : gran == 32 ? launch_core<32>(p, burst, st) : launch_core<16>(p, burst, st);
