@@ -904,8 +904,9 @@ __global__ void __launch_bounds__(256) paged_tokens_kernel(const __grid_constant
 
 // Dealing the tokens' units to the pairs. In cost, token t with u_t > 0 units is kStartUnits + u_t long; of
 // n = min(pairs, total / kMinRange) pairs, pair pp's range begins at the first unit whose cost starts at or after
-// pp * total / n. (A unit never starts two costs behind the one before, so no range of kMinRange is empty.) Each pair's
-// range is written as (first token, its first unit, last token, its end unit), (-1, ...) if it has none.
+// pp * total / n, give or take a unit of a short token. (A unit never starts two costs behind the one before, so the
+// middle pieces of a token are not empty.) Each pair's range is written as (first token, its first unit, last token, its
+// end unit), (-1, ...) if it has none.
 __device__ __forceinline__ int units_of(const int4& info) { return (max(info.y, 0) + UNIT - 1) / UNIT; }
 __device__ __forceinline__ int weight_of(int units) { return units > 0 ? units + kStartUnits : 0; }
 __device__ __forceinline__ int pairs_used(const PlanParams& p, const Order& order, int64_t total) {
@@ -914,7 +915,7 @@ __device__ __forceinline__ int pairs_used(const PlanParams& p, const Order& orde
 }
 // Boundary pp: the first token whose end lies behind the boundary's cost, and the unit in it.
 template <typename Cost>
-__device__ __forceinline__ void deal_boundary(int pp, int used, int64_t total, int64_t T, const int4* tinfo, const Cost* cost,
+__device__ __forceinline__ void deal_boundary(int pp, int used, int pairs, int64_t total, int64_t T, const int4* tinfo, const Cost* cost,
                                               int32_t* tok, int32_t* unit) {
   const int64_t q = total / used, c = q * pp + (int)(total - q * used) * pp / used;      // total * pp / used
   int64_t a = 0, b = T;                     // the last token with cost <= c
@@ -923,7 +924,12 @@ __device__ __forceinline__ void deal_boundary(int pp, int used, int64_t total, i
     if (cost[mid] <= c) a = mid; else b = mid;
   }
   int u = (int)max((int64_t)0, c - cost[a] - kStartUnits);
-  if (pp == used || u >= units_of(tinfo[a])) {   // behind its last unit: the next token
+  // Short tokens are not cut for the sake of one unit: those of two units never (16 x 1 over 512 rows 21.6 -> 19.4 us), of
+  // up to four not when all pairs have work (64 x 1 over 300 rows 33 -> 25, 40 x 1 over 700 34 -> 26; but one token over
+  // 600 rows takes 20.0 in two ranges and 22.5 in one, and 16 over 4096, of 16 units, 40 and 43).
+  const int n = units_of(tinfo[a]);
+  if (n <= (used == pairs ? 4 : 2)) u = u < 2 ? 0 : u + 1 >= n ? n : u;
+  if (pp == used || u >= n) {               // behind its last unit: the next token
     ++a;
     u = 0;
     if (pp == used) a = T;
@@ -947,9 +953,11 @@ __device__ __forceinline__ int4 deal_pair(const PlanParams& p, int pp, int used,
       info = make_int4(a, ua, e, ue);
       p.pfirst[pp] = tinfo[a];
       const int ne = units_of(tinfo[e]);
-      if (ue < ne && !(a == e && ua > 0))                           // e begins here and goes on: to its last unit's pair
-        split = make_int4(tinfo[e].z, 2 * pp + (a == e ? 0 : 1), pp,
-                          (int)(((int64_t)(cost[e] + kStartUnits + ne) * used - 1) / total));
+      if (ue < ne && !(a == e && ua > 0)) {                         // e begins here and goes on: to its last unit's pair
+        int last = (int)(((int64_t)(cost[e] + kStartUnits + ne) * used - 1) / total);
+        while (btok[last] > e) --last;                              // (whose first unit went to the pair before)
+        split = make_int4(tinfo[e].z, 2 * pp + (a == e ? 0 : 1), pp, last);
+      }
     }
   }
   p.pinfo[pp] = info;
@@ -1000,7 +1008,7 @@ __global__ void __launch_bounds__(1024) paged_small_plan_kernel(const __grid_con
   const int used = pairs_used(p, order, total);
   auto sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(DEAL) : "memory"); };
   sync();
-  if (tid <= used) deal_boundary(tid, used, total, T, tinfo, cost, &btok[tid], &bunit[tid]);
+  if (tid <= used) deal_boundary(tid, used, p.pairs, total, T, tinfo, cost, &btok[tid], &bunit[tid]);
   sync();
   if (tid < p.pairs) begins[tid] = deal_pair(p, tid, used, total, T, tinfo, cost, btok, bunit);
   sync();
@@ -1049,7 +1057,7 @@ __global__ void __launch_bounds__(1024) paged_plan_kernel(const __grid_constant_
   }
   __syncthreads();
   const int used = pairs_used(p, order, total);
-  for (int pp = tid; pp <= used; pp += blockDim.x) deal_boundary(pp, used, total, T, tinfo, cost, &btok[pp], &bunit[pp]);
+  for (int pp = tid; pp <= used; pp += blockDim.x) deal_boundary(pp, used, p.pairs, total, T, tinfo, cost, &btok[pp], &bunit[pp]);
   __syncthreads();
   for (int pp = tid; pp < p.pairs; pp += blockDim.x) begins[pp] = deal_pair(p, pp, used, total, T, tinfo, cost, btok, bunit);
   __syncthreads();

@@ -40,7 +40,8 @@ LENS = [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 255, 257, 1000]
     ("bf16", 48, [200, 1000, 47], [3, 2, 1]), ("bf16", 80, [321, 79, 81, 400], [2, 2, 2, 2]),
     ("bf16", 128, [1025, 128, 5], [1, 8, 5]), ("bf16", 192, [700, 191], [1, 4]),
     ("bf16", 64, [4097], [1]), ("bf16", 64, [9000, 77], [1, 1]), ("bf16", 64, [300], [300]),
-    ("bf16", 1024, [1500, 2049], [2, 1])])
+    ("bf16", 1024, [1500, 2049], [2, 1]), ("bf16", 64, [300, 700, 512, 513, 1000] * 11, [1] * 55),
+    ("bf16", 64, [257, 900, 600, 5, 1025] * 3, [1, 0, 1, 1, 1] * 3)])
 def test_attention(mods, dtype, page, lens, tq):
     c = Case(dtype, page, lens, tq, seed=len(lens) + page)
     o, lse = mods[dtype].attn_paged(c.batch(), c.q_abs, c.q_rope)
