@@ -14,7 +14,7 @@
 //
 // What it reaches. 512 tokens of one sequence behind 32768 rows: 1490 TFLOP/s; 8 x 64 behind 16384 rows 1300 to 1450 (1.6
 // to 1.75 ms), 64 x 4 behind 16896 rows 1190, 64 x 2 1140 (0.53 ms), the rows read once from HBM; 4 single tokens over
-// 131072 rows 3.8 TB/s (160 us), 16 over 4096 rows 41 us: there the chain plan - first rows - last partial - merge takes
+// 131072 rows 3.8 TB/s (160 us), 16 over 4096 rows 40 us: there the chain plan - first rows - last partial - merge takes
 // half of the time. Where rows come from L2 a step takes 4600 cycles, MMAs and loads both near their rates; where they
 // come from HBM 7000 to 8500 and no unit is at its limit (64 x 2 behind 2048 rows: tensor pipe 52 %, HBM 30 %): the
 // ring of 112 KB, which cannot grow, holds what is on its way for 2 us or so.

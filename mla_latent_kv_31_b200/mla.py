@@ -388,6 +388,7 @@ class MLA:
         if getattr(dims, "yarn_s", 1.0) > 1.0:
             mla_set_yarn(self.handle, dims.yarn_s, dims.yarn_alpha, dims.yarn_beta, dims.yarn_l0)
         self._ws = None
+        self._ws_bytes = {}                     # of the paged calls, by call and sizes
 
     def close(self):
         if self.handle:
@@ -505,10 +506,15 @@ class MLA:
         return self.torch.zeros(num_pages, mla_paged_summary_bytes(self.handle), dtype=self.torch.uint8,
                                 device=f"cuda:{self.device}")
 
-    def _scratch(self, nbytes: int):
-        """A workspace of one call, from the current stream's allocations (in a capture, the graph's own): calls on
-        several streams or threads and graphs that replay side by side never share one."""
-        return self.torch.empty(max(nbytes, 1), dtype=self.torch.uint8, device=self.torch_device)
+    def _scratch(self, query, a: int, b: int):
+        """A workspace of query(handle, a, b) bytes for one call, from the current stream's allocations (in a capture,
+        the graph's own): calls on several streams or threads and graphs that replay side by side never share one."""
+        n = self._ws_bytes.get((query, a, b))
+        if n is None:
+            if len(self._ws_bytes) >= 1024:
+                self._ws_bytes.clear()
+            n = self._ws_bytes[query, a, b] = max(query(self.handle, a, b), 1)
+        return self.torch.empty(n, dtype=self.torch.uint8, device=self.torch_device)
 
     def _expect_summaries(self, batch, summaries):
         d = self.dims
@@ -558,10 +564,10 @@ class MLA:
             rows.append(("lse", lse, (d.n_h,), torch.float32))
         self._expect_rows(batch, rows)
         if o_lat is None:
-            o_lat = torch.empty((T, d.n_h, d.d_c), dtype=self.tdtype, device=self.torch_device)
+            o_lat = torch.empty_like(q_abs)
         if lse is None:
-            lse = torch.empty((T, d.n_h), dtype=torch.float32, device=self.torch_device)
-        ws = self._scratch(mla_attn_paged_workspace(self.handle, batch.B, T))
+            lse = q_abs.new_empty((T, d.n_h), dtype=torch.float32)
+        ws = self._scratch(mla_attn_paged_workspace, batch.B, T)
         if blocks is None:
             mla_attn_paged(self.handle, batch, q_abs, q_rope, o_lat, lse, ws, ws.numel(), device=self.device)
         else:
@@ -579,8 +585,8 @@ class MLA:
         self._expect_rows(batch, rows)
         self._expect_summaries(batch, summaries)
         if blocks is None:
-            blocks = self.torch.empty((batch.total_q, top_k), dtype=self.torch.int32, device=self.torch_device)
-        ws = self._scratch(mla_paged_select_workspace(self.handle, batch.total_q, batch.max_pages))
+            blocks = q_abs.new_empty((batch.total_q, top_k), dtype=self.torch.int32)
+        ws = self._scratch(mla_paged_select_workspace, batch.total_q, batch.max_pages)
         mla_paged_select(self.handle, batch, q_abs, q_rope, summaries, top_k, n_first, n_last, blocks, ws, ws.numel(),
                          device=self.device)
         return blocks
