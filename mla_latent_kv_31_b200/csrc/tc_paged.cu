@@ -12,16 +12,15 @@
 // 36 and 32 MMAs of N = 256. (An M = 128 pair MMA of K = 16 takes 64 cycles at N = 256, 32 at N = 128, measured: 4357 a
 // step. The loads take about 4200 of 66 bytes a cycle and SM. With both under way a step takes 7000 to 8000.)
 //
-// What it reaches. 512 tokens of one sequence behind 32768 rows: 1490 TFLOP/s; 8 x 64 behind 16384 rows 1300 to 1450 (1.6
-// to 1.75 ms), 64 x 4 behind 16896 rows 1190, 64 x 2 1140 (0.53 ms), the rows read once from HBM; 4 single tokens over
-// 131072 rows 3.8 TB/s (160 us), 16 over 4096 rows 40 us: there the chain plan - first rows - last partial - merge takes
-// half of the time. Where rows come from L2 a step takes 4600 cycles, MMAs and loads both near their rates; where they
-// come from HBM 7000 to 8500 and no unit is at its limit (64 x 2 behind 2048 rows: tensor pipe 52 %, HBM 30 %): the
-// ring of 112 KB, which cannot grow, holds what is on its way for 2 us or so.
+// What it reaches. 512 tokens of one sequence behind 32768 rows: 1540 TFLOP/s; 8 x 64 behind 16384 rows 1270 to 1400 (1.65
+// to 1.8 ms), 64 x 4 behind 8192 rows 1230, 64 x 2 behind 16896 1190 (0.51 ms), the rows read once from HBM; 4 single
+// tokens over 131072 rows 4.0 TB/s (150 us), 16 over 4096 rows 39 us: there the chain plan - first rows - last partial -
+// merge takes half of the time. Where rows come from L2 a step takes 4600 cycles, MMAs and loads both near their rates;
+// where they come from HBM 6500 to 8000 and no unit is at its limit: the ring of 112 KB, which cannot grow, holds what is
+// on its way for 2 us or so.
 // Measured and not kept: a ring and an issuing warp each for K and V (1184 -> 1041 TFLOP/s), waits for several entries at
-// once (0 to 8 % slower), P handed over 64 keys at a time (5 % slower: each wait and commit of the MMA warp counts), the
-// next step's rows prefetched to L2 by copies or loads (3 % slower and more), 64 score columns a thread in registers
-// (the same time, 128 registers instead of 94).
+// once (0 to 8 % slower), P handed over 64 keys at a time (5 % slower: each wait and commit of the MMA warp counts),
+// 64 score columns a thread in registers (the same time, 128 registers instead of 94).
 //
 // Work split. Tokens are cut into units of a step's 256 keys; all units of all tokens, plus a fixed cost per token,
 // are dealt to the pairs in equal contiguous ranges of at least kMinRange. A token that lies in one range is written by
@@ -163,6 +162,10 @@ __device__ __forceinline__ void pair_commit(uint32_t bar) {
       "h"((uint16_t)3)
       : "memory");
 }
+// Contiguous bytes on their way to L2 (a multiple of 16).
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
 // A TMA load into this CTA that counts its bytes on `bar`, a barrier of either CTA (cluster address).
 __device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
   asm volatile(
@@ -289,6 +292,10 @@ struct Rows {
     if (s2.valid()) s2.next();
     block(p);
   }
+  // The first of this lane's rows of step s1, -1 if there are none.
+  __device__ int ahead(const CoreParams& p) const {
+    return off1 < 0 || raw1 < 0 || raw1 >= p.v.num_pages ? -1 : raw1 * p.v.page + off1;
+  }
   // The rows of step s1 (this lane's group), and on to the next: a group behind the last visible key, or in a page
   // outside the pool (flagged), is read out of range, which gives zeros.
   __device__ int take(const CoreParams& p) {
@@ -307,13 +314,7 @@ struct Rows {
 };
 
 // GRAN: rows of a TMA box, the largest of 64, 32, 16 that divides the page size.
-// BURST: how the MMA warp goes through a step's entries. An entry at a time, all lanes wait for it and one issues: 380
-// cycles an entry, of which the MMAs take 256. With BURST one lane runs through all the entries of a product, unrolled:
-// a step takes 4600 cycles where the rows lie in L2 (512 tokens behind 16384 rows 1780 -> 1480 us, 1580 TFLOP/s), but where
-// they come from HBM the loads bunch up (64 x 2 behind 16896 rows 560 -> 606 us, 4 x 131072 162 -> 172). Between: 64 x 8
-// behind 8192 rows 970 -> 908, 16 x 8 behind 16384 560 -> 523, 64 x 4 behind 16896 the same. So: from 8 new tokens a
-// sequence on.
-template <int GRAN, bool BURST>
+template <int GRAN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     paged_core_kernel(const __grid_constant__ CoreParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -411,6 +412,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       leave(kEntriesK);
     };
     auto values_of = [&](int row, int tail_kq) {   // V of a step: 64 keys x 128 of this CTA's columns an entry
+      // ... and the next step's keys on their way to L2, 16 rows an entry: 4 x 131072 rows 164 -> 151 us, 64 x 2 behind
+      // 16896 542 -> 521. (All at once, or alongside the keys, they hold the keys' own copies up: 3 to 5 % slower than
+      // without. Rows that L2 has already cost 0 to 4 %: 8 x 64 behind 16384.)
+      const int later = rows.ahead(p);
       for (int e = turn, slot; e < kEntriesV && ready(e, &slot); e += 3) {
         const int kq = e >> 1;
         int y[64 / GRAN];
@@ -434,6 +439,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (GRAN < 64) pair_load_3d(dst + BOX + s * GRAN * 128, &p.vmap, 0, y[s], z + 1, b);
           }
         }
+        const int to_l2 = __shfl_sync(0xffffffffu, later, 8 * (int)r + e);
+        if (to_l2 >= 0 && elect_one())
+          prefetch_l2(reinterpret_cast<const __nv_bfloat16*>(p.v.cache) + (int64_t)to_l2 * (DC + DR), 16 * (DC + DR) * 2);
         __syncwarp();
         last = n + e;
       }
@@ -470,95 +478,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       auto wait_all = [&](uint32_t b, uint32_t par) { return __all_sync(0xffffffffu, wait_own(b, par)) != 0; };
       int js = 0, gpc = 0, tails = 0;         // step, token, tokens that end inside 64 keys
       int slot = 0, ph = 0;
-      auto next_entry = [&]() {
-        if (++slot == RING) { slot = 0; ph ^= 1; }
-      };
       auto advance = [&](int count) {         // 7 < count < 14
         slot += count - RING;
         ph ^= 1;
         if (slot >= RING) { slot -= RING; ph ^= 1; }
       };
-      auto qk_entry = [&](uint32_t d, int e, int s) {
-        const uint32_t a = q_lo + e * (BOX >> 4), b = k_lo + s * (ENTRY >> 4);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) pair_mma(d, a + 2 * kk, b + 2 * kk, id_qk, (e | kk) ? 1u : 0u);
-        pair_commit(bar(B_EMPTY + s));
-      };
-      auto pv_entry = [&](int e, int s, bool first) {
-        const uint32_t a = p_lo + (e >> 1) * (BOX >> 4), b = v_lo + s * (ENTRY >> 4);
-        const uint32_t keep = first && e < 2 ? 0u : 1u;
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) pair_mma(tmem + 128 * (e & 1), a + 2 * kk, b + 128 * kk, id_pv, kk ? 1u : keep);
-        pair_commit(bar(B_EMPTY + s));
-      };
+      // One lane runs through the entries of a product, unrolled: with a wait of all lanes and an elected lane for each entry
+      // a step took 6900 cycles instead of 4600 where the rows lie in L2. (The warp's own path bounds it then, 380 cycles
+      // an entry of which the MMAs take 256: each instruction more adds to the step.)
       auto qk = [&](int j) -> bool {
         const int sb = j & 1;
         if (!wait_all(bar(B_SFREE + sb), ((j >> 1) & 1) ^ 1)) return false;
+        if (!wait_all(bar(B_FULL + slot), ph)) return false;       // (by all lanes: 4 % faster than in the loop)
         tc_fence_after();
         const uint32_t d = tmem + 256 + 128 * sb;
-        if constexpr (BURST) {
-          if (!wait_all(bar(B_FULL + slot), ph)) return false;       // (all lanes: 4 % faster than in the loop)
-          bool good = true;
-          if (elect_one()) {
-            int s = slot, par = ph;
+        bool good = true;
+        if (elect_one()) {
+          int s = slot, par = ph;
 #pragma unroll
-            for (int e = 0; e < kEntriesK; ++e) {
-              good = wait_short(bar(B_FULL + s), par);
-              if (!good) break;
-              qk_entry(d, e, s);
-              if (++s == RING) { s = 0; par ^= 1; }
-            }
-            if (good) pair_commit(bar(B_SFULL + sb));
-          }
-          advance(kEntriesK);
-          return __all_sync(0xffffffffu, good) != 0;
-        } else {
           for (int e = 0; e < kEntriesK; ++e) {
-            if (!wait_all(bar(B_FULL + slot), ph)) return false;
-            if (elect_one()) {
-              qk_entry(d, e, slot);
-              if (e == kEntriesK - 1) pair_commit(bar(B_SFULL + sb));
-            }
-            __syncwarp();
-            next_entry();
+            good = wait_short(bar(B_FULL + s), par);
+            if (!good) break;
+            const uint32_t a = q_lo + e * (BOX >> 4), b = k_lo + s * (ENTRY >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) pair_mma(d, a + 2 * kk, b + 2 * kk, id_qk, (e | kk) ? 1u : 0u);
+            pair_commit(bar(B_EMPTY + s));
+            if (++s == RING) { s = 0; par ^= 1; }
           }
-          return true;
+          if (good) pair_commit(bar(B_SFULL + sb));
         }
+        advance(kEntriesK);
+        return __all_sync(0xffffffffu, good) != 0;
       };
       auto pv = [&](int j, bool first, int tail_kq) -> bool {
         if (!wait_all(bar(B_PRDY), j & 1)) return false;
         if (first && !wait_all(bar(B_OFREE), (gpc & 1) ^ 1)) return false;
         tc_fence_after();
-        if constexpr (BURST) {
-          bool good = true;
-          if (elect_one()) {
-            int s = slot, par = ph;
+        bool good = true;
+        if (elect_one()) {
+          int s = slot, par = ph;
 #pragma unroll
-            for (int e = 0; e < kEntriesV; ++e) {
-              good = wait_short(bar(B_FULL + s), par);
-              if (good && (e >> 1) == tail_kq && (e & 1) == 0) good = wait_short(bar(B_TRDY), tails & 1);
-              if (!good) break;
-              pv_entry(e, s, first);
-              if (++s == RING) { s = 0; par ^= 1; }
-            }
-            if (good) pair_commit(bar(B_PVD));
-          }
-          if (tail_kq >= 0) ++tails;
-          advance(kEntriesV);
-          return __all_sync(0xffffffffu, good) != 0;
-        } else {
           for (int e = 0; e < kEntriesV; ++e) {
-            if (!wait_all(bar(B_FULL + slot), ph)) return false;
-            if ((e >> 1) == tail_kq && (e & 1) == 0 && !wait_all(bar(B_TRDY), tails++ & 1)) return false;
-            if (elect_one()) {
-              pv_entry(e, slot, first);
-              if (e == kEntriesV - 1) pair_commit(bar(B_PVD));
-            }
-            __syncwarp();
-            next_entry();
+            const int kq = e >> 1;
+            good = wait_short(bar(B_FULL + s), par);
+            if (good && kq == tail_kq && (e & 1) == 0) good = wait_short(bar(B_TRDY), tails & 1);
+            if (!good) break;
+            const uint32_t a = p_lo + kq * (BOX >> 4), b = v_lo + s * (ENTRY >> 4);
+            const uint32_t keep = first && kq == 0 ? 0u : 1u;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              pair_mma(tmem + 128 * (e & 1), a + 2 * kk, b + 128 * kk, id_pv, kk ? 1u : keep);
+            pair_commit(bar(B_EMPTY + s));
+            if (++s == RING) { s = 0; par ^= 1; }
           }
-          return true;
+          if (good) pair_commit(bar(B_PVD));
         }
+        if (tail_kq >= 0) ++tails;
+        advance(kEntriesV);
+        return __all_sync(0xffffffffu, good) != 0;
       };
       for (; ok && w.valid(); w.next(), ++gpc) {
         const int ns = w.steps(), rem = w.k1 - (w.k0 + (ns - 1) * NK);
@@ -1116,16 +1093,12 @@ __global__ void __launch_bounds__(256)
       make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
 }
 
-template <int GRAN, bool BURST>
+template <int GRAN>
 cudaError_t launch_core(const CoreParams& p, cudaStream_t st) {
   // per device, so set at every call
-  cudaError_t e = cudaFuncSetAttribute(paged_core_kernel<GRAN, BURST>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+  cudaError_t e = cudaFuncSetAttribute(paged_core_kernel<GRAN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  return launch_next(paged_core_kernel<GRAN, BURST>, dim3(2 * p.pairs), kThreads, SMEM_BYTES, st, p);
-}
-template <int GRAN>
-cudaError_t launch_core(const CoreParams& p, bool burst, cudaStream_t st) {
-  return burst ? launch_core<GRAN, true>(p, st) : launch_core<GRAN, false>(p, st);
+  return launch_next(paged_core_kernel<GRAN>, dim3(2 * p.pairs), kThreads, SMEM_BYTES, st, p);
 }
 
 size_t align1k(size_t x) { return (x + 1023) / 1024 * 1024; }
@@ -1220,8 +1193,7 @@ cudaError_t tc_paged_attention(const PagedView& v, const void* q_abs, const void
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if ((e = launch_next(paged_plan_kernel, dim3(1), 1024, 0, st, pp)) != cudaSuccess) return e;
   }
-  const bool burst = v.total_q >= 8 * v.B;
-  e = gran == 64 ? launch_core<64>(p, burst, st) : gran == 32 ? launch_core<32>(p, burst, st) : launch_core<16>(p, burst, st);
+  e = gran == 64 ? launch_core<64>(p, st) : gran == 32 ? launch_core<32>(p, st) : launch_core<16>(p, st);
   if (e != cudaSuccess) return e;
   // at most one token per boundary, and no more than there are, goes on in the next pair's range
   const int64_t most = p.pairs - 1 < v.total_q ? p.pairs - 1 : v.total_q;
