@@ -35,9 +35,9 @@
 //
 // Roles (512 threads): warps 0, 2 and 3 fill the ring of 16 KB entries, every third entry each, in the order the
 // MMAs take them (K of step j + 1 before V of step j; one thread issues a copy every 500 cycles or so, the copies
-// take 270), and warp 2 loads a token's queries; warp 1 of the leader CTA issues the MMAs;
-// these run warp-uniform code with one elected lane at each TMA, MMA and commit (a lane-0 branch around the
-// whole loop cost 650 cycles a ring entry, three times what the copies take); warps 4-11 are the softmax (thread = TMEM
+// take 270), and warp 2 loads a token's queries, in warp-uniform code with one elected lane at each copy; warp 1 of the
+// leader CTA issues the MMAs, one elected lane a product (a lane-0 branch around the whole loop cost 650 cycles a
+// ring entry, three times what the copies take); warps 4-11 are the softmax (thread = TMEM
 // lane, two warps per lane quarter, 64 keys each) and rescale O when the running maximum has grown by 2^8; warps 12-15
 // write O out while the next token's first step runs.
 // Every wait is bounded (a timeout sets the error word and the role returns).
