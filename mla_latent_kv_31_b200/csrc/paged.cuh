@@ -105,6 +105,13 @@ __device__ inline int64_t paged_list_rows(const int32_t* list, int32_t top_k, in
   return (int64_t)(n - 1) * page + (last == pos / page ? pos % page + 1 : page);
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // Programmatic dependent launch: the next kernel of the chain may start its prologue; this one waits for the kernel
 // before it (and with it all earlier ones) to be complete and visible.
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

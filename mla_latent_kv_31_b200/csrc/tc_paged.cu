@@ -132,12 +132,6 @@ __device__ __forceinline__ void pair_relinquish() {
 __device__ __forceinline__ void pair_dealloc(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
 // Low word of a 128-byte-swizzle descriptor (start address, distance of 64-wide MN blocks); the high word is the
 // same for every operand here (8-row atoms 1024 bytes apart).
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {

@@ -6,9 +6,10 @@
 // select_score_kernel a CTA keeps one tile of 128 blocks of a sequence in shared memory (gathered by cp.async: its rows lie
 // anywhere) and runs over the sequence's tokens, whose codes stream in by TMA (80 KB each): M = 128 blocks, N = 128
 // heads, K = 576 in 18 MMAs of K = 32. With the blocks on the lanes the maximum over the heads stays in a thread.
-// The products bound it: kind::i8 runs an M128 N128 K32 MMA in 128 cycles (measured; half of fp8's nominal rate), 2304 a token and
-// tile; 512 tokens over 2048 blocks take 100 us, 74 % of the tensor pipe's time (70 us), the conversions of the sums to
-// fp32 61 % of the XU's. 512 tokens over 512 blocks: codes 20-30 us (110 MB), scores 35, choice 14; 75 in one call.
+// A token and tile is 1152 cycles of MMAs (64 each, measured), 1300 of copies and 1024 of the XU's conversions of the
+// sums to fp32, of which no two overlap wholly: 512 tokens over 2048 blocks take 60 us, 36 of them MMAs. (100 us with an
+// elected lane and a wait of all lanes for each box of codes: 128 cycles an MMA.) 512 tokens over 512 blocks: codes 27 us
+// (110 MB), scores 25, choice 14; 66 in one call.
 // 4 tokens over 2048 blocks: 19 us, the latency of the three launches.
 // (Quantising inside the scoring kernel, a token's codes kept and the tiles streamed past, took 94 us there: 5 us of
 // arithmetic a token, and a gather's latency for every tile.)
@@ -34,9 +35,9 @@ constexpr uint32_t KBOX = 128 * 128;            // 128-byte swizzle
 constexpr uint32_t OFF_Y = 0;
 constexpr uint32_t OFF_RING = OFF_Y + kBoxes * KBOX;
 constexpr uint32_t OFF_SY = OFF_RING + RING * KBOX;            // [128] scales of the summaries
-constexpr uint32_t OFF_SQ = OFF_SY + TILE * 4;                 // [2][128] scales of the queries
-constexpr uint32_t OFF_PART = OFF_SQ + 2 * H * 4;              // [128] maxima over the upper 64 heads
-constexpr uint32_t OFF_BAR = OFF_PART + TILE * 4;
+constexpr uint32_t OFF_SQ = OFF_SY + TILE * 4;                 // [8 warps][2][64] scales of the queries
+constexpr uint32_t OFF_PART = OFF_SQ + 8 * 2 * 64 * 4;         // [2][128] maxima over the upper 64 heads
+constexpr uint32_t OFF_BAR = OFF_PART + 2 * TILE * 4;
 enum : int { B_FULL = 0, B_EMPTY = B_FULL + RING, B_DFULL = B_EMPTY + RING, B_DFREE = B_DFULL + 2, NBAR = B_DFREE + 2 };
 constexpr uint32_t SMEM_BYTES = OFF_BAR + 8 * NBAR + 16 + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_score_kernel(const __grid_
           const uint32_t slot = n % RING;
           ok = __all_sync(0xffffffffu, mbar_wait(bar(B_EMPTY + slot), ((n / RING) & 1) ^ 1)) != 0;
           if (!ok) break;
-          if (lane == 0) {
+          if (elect_one()) {
             mbar_expect_tx(bar(B_FULL + slot), KBOX);
             tma_load_2d(sbase + OFF_RING + slot * KBOX, &p.qmap, 128 * e, (int32_t)((from + k) * H), bar(B_FULL + slot));
           }
@@ -287,60 +288,64 @@ __global__ void __launch_bounds__(kThreads, 1) select_score_kernel(const __grid_
       for (int k = 0; ok && k < cnt; ++k, ++done) {
         const uint32_t d = tmem + 128 * (done & 1);
         ok = __all_sync(0xffffffffu, mbar_wait(bar(B_DFREE + (done & 1)), ((done >> 1) & 1) ^ 1)) != 0;
-        for (int e = 0; ok && e < kBoxes; ++e, ++n) {
-          const uint32_t slot = n % RING;
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(B_FULL + slot), (n / RING) & 1)) != 0;
-          if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint64_t a = sw128_desc(sbase + OFF_Y + e * KBOX, 0, 1024), b = sw128_desc(sbase + OFF_RING + slot * KBOX, 0, 1024);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (e < 4 || i < 2) mma_i8(d, a + 2 * i, b + 2 * i, idesc, (e | i) ? 1u : 0u);
-            mma_commit(bar(B_EMPTY + slot));
-            if (e == kBoxes - 1) mma_commit(bar(B_DFULL + (done & 1)));
-          }
-          __syncwarp();
-        }
-      }
-    } else if (warp >= 4) {
-      // ---- maxima: thread = block, 64 heads
-      float* part = reinterpret_cast<float*>(smem + OFF_PART);
-      float* sq = reinterpret_cast<float*>(smem + OFF_SQ);
-      const float scale = sy[row];
-      const int et = tid - 128;
-      float s_next = et < H ? p.scales[from * H + et] : 0.f;
-      for (int k = 0; ok && k < cnt; ++k, ++done) {
-        float* sqb = sq + (done & 1) * H;
-        if (et < H) {
-          sqb[et] = s_next;
-          if (k + 1 < cnt) s_next = p.scales[(from + k + 1) * H + et];
-        }
-        // (also: the upper half's maxima of the token before are read)
-        ok = !bar_sync_or(1, 256, !mbar_wait(bar(B_DFULL + (done & 1)), (done >> 1) & 1));
         if (!ok) break;
         tc_fence_after();
-        float mx = -INFINITY;
+        // one lane runs through the token's boxes, unrolled
+        bool good = true;
+        if (elect_one()) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t x[32];
-          tmem_ld32(tmem + ((uint32_t)(32 * quarter) << 16) + 128 * (done & 1) + 64 * cg + 32 * h, x);
-          tmem_wait_ld();
+          for (int e = 0; e < kBoxes; ++e) {
+            const uint32_t slot = (n + e) % RING;
+            good = mbar_wait(bar(B_FULL + slot), ((n + e) / RING) & 1);
+            if (!good) break;
+            const uint64_t a = sw128_desc(sbase + OFF_Y + e * KBOX, 0, 1024), b = sw128_desc(sbase + OFF_RING + slot * KBOX, 0, 1024);
 #pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            const float4 s4 = *reinterpret_cast<const float4*>(sqb + 64 * cg + 32 * h + c);
-            mx = fmaxf(mx, fmaxf(fmaxf((float)(int)x[c] * s4.x, (float)(int)x[c + 1] * s4.y),
-                                 fmaxf((float)(int)x[c + 2] * s4.z, (float)(int)x[c + 3] * s4.w)));
+            for (int i = 0; i < (e < 4 ? 4 : 2); ++i) mma_i8(d, a + 2 * i, b + 2 * i, idesc, (e | i) ? 1u : 0u);
+            mma_commit(bar(B_EMPTY + slot));
           }
+          if (good) mma_commit(bar(B_DFULL + (done & 1)));
         }
-        tc_fence_before();
+        n += kBoxes;
+        ok = __all_sync(0xffffffffu, good) != 0;
+      }
+    } else if (warp >= 4) {
+      // ---- maxima: thread = block, 64 heads; the two warps of a block of 32 lanes meet once a token
+      float* part = reinterpret_cast<float*>(smem + OFF_PART);
+      float* sq = reinterpret_cast<float*>(smem + OFF_SQ) + 128 * (warp - 4);
+      const float scale = sy[row];
+      const float2* src = reinterpret_cast<const float2*>(p.scales + from * H + 64 * cg) + lane;
+      float2 s_next = *src;
+      for (int k = 0; ok && k < cnt; ++k, ++done) {
+        float* sqb = sq + 64 * (done & 1);
+        reinterpret_cast<float2*>(sqb)[lane] = s_next;
+        if (k + 1 < cnt) s_next = src[(k + 1) * (H / 2)];
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_DFREE + (done & 1)));
-        if (cg == 1) part[row] = mx;
-        asm volatile("bar.sync 2, 256;" ::: "memory");
+        const bool full = __all_sync(0xffffffffu, mbar_wait(bar(B_DFULL + (done & 1)), (done >> 1) & 1)) != 0;
+        float mx = -INFINITY;
+        if (full) {
+          tc_fence_after();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t x[32];
+            tmem_ld32(tmem + ((uint32_t)(32 * quarter) << 16) + 128 * (done & 1) + 64 * cg + 32 * h, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+              const float4 s4 = *reinterpret_cast<const float4*>(sqb + 32 * h + c);
+              mx = fmaxf(mx, fmaxf(fmaxf((float)(int)x[c] * s4.x, (float)(int)x[c + 1] * s4.y),
+                                   fmaxf((float)(int)x[c + 2] * s4.z, (float)(int)x[c + 3] * s4.w)));
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_DFREE + (done & 1)));
+        }
+        float* pb = part + TILE * (done & 1);
+        if (cg == 1) pb[row] = mx;
+        ok = !bar_sync_or(1 + quarter, 64, !full);
         const int64_t g = (int64_t)tile * TILE + row;
-        if (cg == 0 && g <= (pos_from + k) / v.page)
-          p.scores[(from + k) * v.max_pages + g] = fmaxf(mx, part[row]) * scale + 0.f;   // + 0: a -0 ties with a 0
+        if (ok && cg == 0 && g <= (pos_from + k) / v.page)
+          p.scores[(from + k) * v.max_pages + g] = fmaxf(mx, pb[row]) * scale + 0.f;   // + 0: a -0 ties with a 0
       }
     }
     // the roles agree on what went by; the tile's buffer takes the next run's
