@@ -323,7 +323,9 @@ mla_status_t mla_attn_prefill(mla_handle_t *h, const void *q_c, const void *q_ro
  * page outside the pool is read as zero rows.
  * The handle's cache format must be MLA_CACHE_BF16 (MLA_ERR_UNSUPPORTED otherwise); page_size is a
  * multiple of 16, num_pages * page_size < 2^31 and max_pages * page_size <= 2^30. A handle without
- * weights serves these calls; its first call allocates the error word, so it must not be part of a stream capture. */
+ * weights serves these calls; its first call allocates the error word, so it must not be part of a
+ * stream capture. A workspace belongs to one call at a time: calls, and captured graphs, that may run
+ * at the same time need one each. */
 typedef struct {
   void *cache;                /* [num_pages, page_size, d_c + d_r] handle dtype, rows as elsewhere     */
   int64_t num_pages;
@@ -364,8 +366,7 @@ mla_status_t mla_paged_append(mla_handle_t *h, const mla_paged_t *batch, const v
  *   q_rope  [total_q, n_h, d_r]  handle dtype (rotated q^R)
  *   o_lat   [total_q, n_h, d_c]  handle dtype, sum_j p_j c_j (what W^UV is multiplied with)
  *   lse     [total_q, n_h]       fp32, natural log of sum_j exp(s_j)
- * Rows past pos may hold anything (NaN included). ws: mla_attn_paged_workspace() bytes; calls that
- * may overlap need workspaces of their own. */
+ * Rows past pos may hold anything (NaN included). ws: mla_attn_paged_workspace() bytes. */
 mla_status_t mla_attn_paged(mla_handle_t *h, const mla_paged_t *batch, const void *q_abs, const void *q_rope,
                             void *o_lat, float *lse, void *ws, size_t ws_bytes, mla_stream_t stream);
 
