@@ -56,7 +56,14 @@ __global__ void __launch_bounds__(AP_THREADS)
   if (has_row) uk = reinterpret_cast<const uint4*>(kv + t * kv_stride)[tid];
   if (t == 0) paged_check(v, err);
   const PagedToken tok = paged_token(v, t);
-  if (tok.pos < 0) return;
+  if (tok.pos < 0) {
+    if (q && tok.seq >= 0) {                                 // an empty row
+      uint4* qd = reinterpret_cast<uint4*>(q_out + t * AP_H * AP_DR);
+#pragma unroll
+      for (int k = 0; k < QC; ++k) qd[tid + k * AP_THREADS] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    return;
+  }
   const int64_t page = paged_page(v, tok.seq, tok.pos / v.page, err);
   if (tid < AP_DR / 2) rope_angle(rt, o, tok.pos, tid, AP_DR, &cs[tid].x, &cs[tid].y);
   float inv = 1.f;
@@ -112,7 +119,11 @@ __global__ void __launch_bounds__(128)
   const int64_t t = blockIdx.x;
   if (t == 0) paged_check(v, err);
   const PagedToken tok = paged_token(v, t);
-  if (tok.pos < 0) return;
+  if (tok.pos < 0) {
+    if (q && tok.seq >= 0)                                   // an empty row
+      for (int i = tid; i < v.n_h * v.d_r; i += blockDim.x) q_out[t * v.n_h * v.d_r + i] = 0.f;
+    return;
+  }
   const int64_t page = paged_page(v, tok.seq, tok.pos / v.page, err);
   for (int m = tid; m < v.d_r / 2; m += blockDim.x) rope_angle(rt, o, tok.pos, m, v.d_r, &cs[m].x, &cs[m].y);
   __syncthreads();

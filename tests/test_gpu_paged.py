@@ -345,6 +345,34 @@ def test_append_flags_bad_pages_and_writes_nothing_for_them(mods, dtype):
     assert changed == sorted([page2, int(c.table[1, 1])])
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_append_gives_flagged_tokens_empty_queries(mods, dtype, in_place):
+    """The middle sequence has fewer rows than new tokens, so its queries come back as zeros; the others are rotated,
+    the rows behind the last sequence stay as they were, and no page is complete."""
+    m = mods[dtype]
+    c = Case(dtype, 16, [40, 20, 9], [3, 2, 1], seed=23, pad=4)
+    c.d_lens[1] = 1
+    d, q = c.dims, c.q[..., c.dims.d_c:]
+    kv, qd, cache, sums = c.on(c.normal(c.T + 4, c.W)), c.q_rope, c.cache.clone(), m.new_summaries(c.num_pages) + 5
+    out = qd if in_place else torch.full_like(qd, 7.0)
+    kept = out[c.T:].clone()
+    assert m.paged_append(c.batch(), kv, q_rope=qd, q_out=out, summaries=sums) is out
+    flagged(m, 1 << 1)
+    got = out.double().cpu()
+    assert (got[3:5] == 0).all() and torch.equal(out[c.T:], kept) and (sums == 5).all()
+    rows = [(int(c.table[b, pos // 16]), pos % 16) for t, b, pos in c.tokens() if b != 1]
+    for t, b, pos in c.tokens():
+        if b != 1:
+            # as in check_append: one rounding of the result, two products and their sum in fp32
+            want = rope(q[t], pos, d)
+            pair = q[t].view(d.n_h, -1, 2).norm(dim=-1).repeat_interleave(2, dim=-1) * 1.5
+            assert ((got[t] - want).abs() <= HALF[dtype] * want.abs() + 8 * 2.0 ** -24 * pair).all(), (t, b, pos)
+    i = torch.int16 if dtype == "bf16" else torch.int32
+    changed = (c.cache.view(i) != cache.view(i)).any(-1).nonzero().tolist()
+    assert sorted(map(tuple, changed)) == sorted(rows)
+
+
 # ---- selection ----------------------------------------------------------------------------------------------
 @pytest.mark.parametrize("dtype,page,lens,tq,top_k,first,last", [
     ("fp32", 16, [700, 90, 16], [3, 2, 1], 8, 1, 2), ("bf16", 16, [700, 90, 16], [3, 2, 1], 8, 1, 2),
