@@ -334,8 +334,9 @@ __global__ void __launch_bounds__(ATT)
       if (j < cnt) s = d0 * scale;
     }
     const float m_new = fmaxf(m, block_max(s, red));
+    const float base = m_new == -INFINITY ? 0.f : m_new;        // (no score above -inf so far: weights of 0, a NaN stays)
     const float alpha = m == -INFINITY ? 0.f : __expf(m - m_new);
-    const float p = j < cnt ? __expf(s - m_new) : 0.f;
+    const float p = j < cnt ? __expf(s - base) : 0.f;
     if ((tid & 1) == 0 && j < cnt) ps[j] = p;
     l = l * alpha + block_sum((tid & 1) == 0 ? p : 0.f, red);
     acc[0] *= alpha;
@@ -352,7 +353,7 @@ __global__ void __launch_bounds__(ATT)
     m = m_new;
     __syncthreads();
   }
-  const float inv = n > 0 ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;                   // (l = 0: no rows, or every score -inf)
   acc_sh[tid] = acc[0];
   __syncthreads();
   if (kg == 0) {
@@ -361,7 +362,7 @@ __global__ void __launch_bounds__(ATT)
     o_lat[oq * v.d_c + col] = sum * inv;
     if (col + ATT < v.d_c) o_lat[oq * v.d_c + col + ATT] = acc[1] * inv;
   }
-  if (tid == 0) lse[oq] = n > 0 ? m + logf(l) : -INFINITY;
+  if (tid == 0) lse[oq] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
 // ---- selection ----------------------------------------------------------------------------------------------

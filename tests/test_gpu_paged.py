@@ -140,6 +140,27 @@ def test_attention_large_scores(mods):
     c.check_attention(o, lse, prefix(c))
 
 
+@pytest.mark.parametrize("dtype,page,lens,tq,low", [("fp32", 16, [300, 140, 139], [2, 1, 3], 140),
+                                                    ("bf16", 64, [700, 300, 256], [2, 1, 3], 300),
+                                                    ("bf16", 64, [5000, 20], [1, 1], 1500)])
+def test_attention_scores_of_minus_infinity(mods, dtype, page, lens, tq, low):
+    """The first `low` rows of each sequence score -inf: weights of 0; where no other row is seen, an empty row."""
+    c = Case(dtype, page, lens, tq, seed=67)
+    d = c.dims.d_c
+    c.q[..., d] = -c.q[..., d].abs() - 0.5
+    for b, n in enumerate(lens):
+        j = torch.arange(min(low, n))
+        c.cache[c.table[b, j // page].long().cuda(), (j % page).cuda(), d] = float("inf")
+    o, lse = mods[dtype].attn_paged(c.batch(), c.q_abs, c.q_rope)
+    blocks = torch.full((c.T, max(lens) // page + 1), -1, dtype=torch.int32)
+    for t, b, pos in c.tokens():
+        blocks[t, :pos // page + 1] = torch.arange(pos // page + 1, dtype=torch.int32)
+    o2, lse2 = mods[dtype].attn_paged_sparse(c.batch(), c.q_abs, c.q_rope, blocks.cuda())
+    ok(mods[dtype])
+    for x, y in ((o, lse), (o2, lse2)):
+        c.check_attention(x, y, lambda t, b, pos: c.rows[b][low:pos + 1])
+
+
 def test_attention_equals_the_contiguous_core(mods):
     c = Case("bf16", 64, [500, 1, 129], [1, 1, 1], seed=8)
     o, lse = mods["bf16"].attn_paged(c.batch(), c.q_abs, c.q_rope)
