@@ -703,7 +703,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int slot = 2 * pair + (gpc > 0 ? 1 : 0);
       if (quarter < 2) {
         if (whole) p.lse[row] = l == 0.f ? -INFINITY : m + logf(l);
-        else p.part_ml[(int64_t)slot * H + head] = make_float2(l == 0.f ? -INFINITY : m, l);
+        // (a maximum of -inf stands for a piece without weight; one of NaN scores alone, whose sum is NaN, gives it a 0)
+        else p.part_ml[(int64_t)slot * H + head] = make_float2(l == 0.f ? -INFINITY : m == -INFINITY ? 0.f : m, l);
       }
       const float inv = l == 0.f ? 0.f : 1.f / l;
       uint4* dst = reinterpret_cast<uint4*>(p.o_lat + row * DC + col0);

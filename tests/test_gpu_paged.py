@@ -161,6 +161,30 @@ def test_attention_scores_of_minus_infinity(mods, dtype, page, lens, tq, low):
         c.check_attention(x, y, lambda t, b, pos: c.rows[b][low:pos + 1])
 
 
+@pytest.mark.parametrize("dtype,lens", [("fp32", [700, 40]), ("bf16", [5000, 40]), ("bf16", [200, 40]),
+                                        ("bf16", [256 * 74 * 2, 300])])
+def test_attention_carries_nan_to_its_heads_and_tokens(mods, dtype, lens):
+    """A NaN in a query makes all scores of its head NaN, NaN rows those of a part of a token's keys: the output is NaN
+    there, in however many pieces the token is dealt, and the other heads and tokens keep their values bit for bit."""
+    m = mods[dtype]
+    c = Case(dtype, 16, lens, [1, 1], seed=68)
+    qa, qr, b = c.q_abs, c.q_rope, c.batch()
+    o, lse = m.attn_paged(b, qa, qr)
+    bad = qa.clone()
+    bad[0, 2, 3] = NAN
+    o2, lse2 = m.attn_paged(b, bad, qr)
+    ok(m)
+    assert torch.isnan(o2[0, 2]).all() and torch.isnan(lse2[0, 2])
+    o2[0, 2], lse2[0, 2] = o[0, 2], lse[0, 2]
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    j = torch.arange(lens[0] // 3)
+    c.cache[c.table[0, j // 16].long().cuda(), (j % 16).cuda()] = NAN
+    o2, lse2 = m.attn_paged(b, qa, qr)
+    ok(m)
+    assert torch.isnan(o2[0]).all() and torch.isnan(lse2[0]).all()
+    assert torch.equal(o[1], o2[1]) and torch.equal(lse[1], lse2[1])
+
+
 def test_attention_equals_the_contiguous_core(mods):
     c = Case("bf16", 64, [500, 1, 129], [1, 1, 1], seed=8)
     o, lse = mods["bf16"].attn_paged(c.batch(), c.q_abs, c.q_rope)
