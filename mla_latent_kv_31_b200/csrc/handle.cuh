@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "common.cuh"
 #include "mla.h"
 
@@ -59,15 +61,31 @@ inline mla_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MLA_O
     if (_e != cudaSuccess) return MLA_ERR_CUDA;    \
   } while (0)
 
-// Allocates the handle's error word on first use. The caller holds a DeviceGuard for h->device.
+// Makes the handle ready for launches on first use: the error word, zeroed and waited for (on a stream of its own, which
+// waits for no other work), and the SM count, published together. Calls of several threads may be the first ones; a
+// failure leaves the handle as it was. The caller holds a DeviceGuard for h->device.
 inline mla_status_t ensure_device(mla_handle* h) {
-  if (!h->d_err) {
-    MLA_TRY(cudaMalloc(&h->d_err, sizeof(uint32_t)));
-    MLA_TRY(cudaMemset(h->d_err, 0, sizeof(uint32_t)));
-    int sms = 0;
-    MLA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, h->device));
-    h->num_sms = sms;
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lock(mu);
+  if (h->d_err) return MLA_OK;
+  int sms = 0;
+  MLA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, h->device));
+  uint32_t* word = nullptr;
+  MLA_TRY(cudaMalloc(&word, sizeof(uint32_t)));
+  cudaStream_t st = nullptr;
+  cudaError_t e = cudaStreamCreateWithFlags(&st, cudaStreamNonBlocking);
+  if (e == cudaSuccess) {
+    e = cudaMemsetAsync(word, 0, sizeof(uint32_t), st);
+    const cudaError_t s = cudaStreamSynchronize(st);
+    if (e == cudaSuccess) e = s;
+    cudaStreamDestroy(st);
   }
+  if (e != cudaSuccess) {
+    cudaFree(word);
+    return MLA_ERR_CUDA;
+  }
+  h->num_sms = sms;
+  h->d_err = word;
   return MLA_OK;
 }
 

@@ -1,5 +1,7 @@
 """Host-side checks of the paged latent cache's calls: every refusal comes back before any launch (no GPU here)."""
 import ctypes
+import os
+import subprocess
 
 import pytest
 import torch
@@ -143,3 +145,13 @@ def test_the_tests_own_rotation_and_selection():
     means = torch.zeros(c.num_pages, c.W, dtype=torch.float64)
     means[c.table[0, 5].long()] = c.q[0, 2]             # one block looks like a query, the others score 0
     assert c.select(means, 4, 1, 1)[0].tolist() == [0, 1, 5, 8]
+
+
+def test_first_call_of_a_handle(tmp_path):
+    """tests/handle_init.cu: threads that are first at once, and each runtime call failing, over a stand-in runtime."""
+    exe = tmp_path / "handle_init"
+    here = os.path.dirname(os.path.abspath(__file__))
+    subprocess.run([mla_build.nvcc(), *mla_build.ARCH, *mla_build.FLAGS, "-cudart", "none",
+                    os.path.join(here, "handle_init.cu"), "-o", str(exe)], check=True, capture_output=True, text=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", (r.returncode, r.stdout, r.stderr)
