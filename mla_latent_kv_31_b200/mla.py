@@ -118,11 +118,11 @@ def _ptr(x) -> int | None:
     return x.data_ptr()
 
 
-def _stream(stream, device: int):
+def _stream(stream, device):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
     import torch
-    return torch._C._cuda_getCurrentRawStream(device)      # the handle that current_stream() wraps, 2 us sooner
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _check(status: int, what: str):

@@ -213,6 +213,22 @@ def test_attention_is_deterministic_and_runs_on_any_stream(mods, dtype):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+def test_calls_take_every_name_of_their_device(mods):
+    m = mods["bf16"]
+    c = Case("bf16", 64, [700, 64], [2, 1], seed=69)
+    b, qa, qr = c.batch(), c.q_abs, c.q_rope
+    o, lse = m.attn_paged(b, qa, qr)
+    n = mla.mla_attn_paged_workspace(m.handle, 2, 3)
+    torch.cuda.synchronize()
+    for device in (0, "cuda:0", torch.device("cuda", 0), torch.device("cuda"), None):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            o2, lse2, ws = torch.zeros_like(o), torch.zeros_like(lse), torch.empty(n, dtype=torch.uint8, device="cuda")
+            mla.mla_attn_paged(m.handle, b, qa, qr, o2, lse2, ws, n, device=device)
+        assert mla.mla_sync_status(m.handle, s, device=device) == 0
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_flagged_batches_give_empty_rows(mods, dtype):
     m = mods[dtype]

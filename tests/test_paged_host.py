@@ -95,6 +95,17 @@ def test_arguments_of_each_call():
         mla.mla_destroy(h)
 
 
+@pytest.mark.parametrize("device", [0, 1, "cuda:1", torch.device("cuda", 0), torch.device("cuda"), None])
+def test_default_stream_takes_every_name_of_a_device(monkeypatch, device):
+    """Without a stream, a call goes to torch's current stream of the device, named as torch.cuda names devices."""
+    class Stream:
+        cuda_stream = 77
+    asked = []
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: asked.append(d) or Stream)
+    assert mla._stream(None, device) == 77 and asked == [device]
+    assert mla._stream(5, device) == 5 and mla._stream(Stream, device) == 77 and asked == [device]
+
+
 def test_workspaces_and_summary_rows():
     h = mla.mla_create(synth.V3)
     t = mla.mla_create(synth.TINY, mla.MLA_FP32)
