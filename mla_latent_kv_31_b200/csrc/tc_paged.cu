@@ -40,7 +40,8 @@
 // ring entry, three times what the copies take); warps 4-11 are the softmax (thread = TMEM
 // lane, two warps per lane quarter, 64 keys each) and rescale O when the running maximum has grown by 2^8; warps 12-15
 // write O out while the next token's first step runs.
-// Every wait is bounded (a timeout sets the error word and the role returns).
+// Every wait is bounded (a timeout sets the error word and the role returns); that of the output warps, which lasts as
+// long as a token's steps, by the steps' progress.
 #include <cuda_bf16.h>
 #include <string.h>
 
@@ -75,11 +76,12 @@ constexpr uint32_t P_BYTES = HC * NK * 2;
 
 constexpr uint32_t OFF_RED = 512;                                  // [2][4][64] floats: maxima of the four key blocks
 constexpr uint32_t OFF_STAT = OFF_RED + 2 * 4 * HC * 4;            // [5][64] floats: sums of the four key blocks, maximum
+constexpr uint32_t OFF_STEPS = OFF_STAT + 5 * HC * 4;              // steps whose scores warp 4 has taken
 constexpr uint32_t OFF_Q = 4096;
 constexpr uint32_t OFF_P = OFF_Q + Q_BYTES;
 constexpr uint32_t OFF_RING = OFF_P + P_BYTES;
 constexpr uint32_t SMEM_BYTES = OFF_RING + RING * ENTRY + 1024;
-static_assert(OFF_STAT + 5 * HC * 4 <= OFF_Q, "statistics block");
+static_assert(OFF_STEPS + 4 <= OFF_Q, "statistics block");
 static_assert(OFF_Q % 1024 == 0 && OFF_P % 1024 == 0 && OFF_RING % 1024 == 0, "swizzle atom alignment");
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 
@@ -208,6 +210,26 @@ __device__ __forceinline__ bool wait_own(uint32_t bar, uint32_t parity) {
   }
 }
 
+// The same for a wait that lasts as long as many steps do: the limit counts from the last change of *steps, the count of
+// them that another warp keeps in shared memory.
+__device__ __forceinline__ bool wait_following(uint32_t bar, uint32_t parity, const volatile uint32_t* steps) {
+  uint32_t seen = *steps;
+  long long t0 = clock64();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63) == 0) {
+      const uint32_t now = *steps;
+      const long long t = clock64();
+      if (now != seen) {
+        seen = now;
+        t0 = t;
+      } else if (t - t0 > kWaitCycles) {
+        return false;
+      }
+    }
+  }
+}
+
 // The slow half of a wait that is unrolled many times: one copy, a call away.
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity) { return wait_own(bar, parity); }
 __device__ __forceinline__ bool wait_short(uint32_t bar, uint32_t parity) { return test_bar(bar, parity) || wait_slow(bar, parity); }
@@ -331,6 +353,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       else if (i == B_OFREE || i == B_LRDY) cnt = 8;
       mbar_init(bar(i), cnt);
     }
+    *reinterpret_cast<volatile uint32_t*>(smem + OFF_STEPS) = 0;
     fence_mbar_init();
     prefetch_tmap(&p.kmap);
     prefetch_tmap(&p.vmap);
@@ -568,6 +591,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int rem = w.k1 - (w.k0 + j * NK);              // visible keys from the step's first on
         if (!wait_u(bar(B_SFULL + sb), (js >> 1) & 1)) { ok = false; break; }
         tc_fence_after();
+        if (threadIdx.x == 128) *reinterpret_cast<volatile uint32_t*>(smem + OFF_STEPS) = (uint32_t)js + 1;
         // Two passes over the scores, 32 columns at a time from tensor memory (64 columns held in registers take the
         // same time, but 128 registers with spills instead of 94)
         const uint32_t scol = trow + 256 + 128 * sb + 64 * half;
@@ -687,11 +711,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int col0 = 128 * (quarter >> 1);
     const uint32_t trow = tmem + ((uint32_t)(32 * quarter) << 16);
     const float* stat = reinterpret_cast<const float*>(smem + OFF_STAT);
+    const volatile uint32_t* steps = reinterpret_cast<const volatile uint32_t*>(smem + OFF_STEPS);
     const uint32_t ofree = lead(B_OFREE);
     auto wait_u = [&](uint32_t b, uint32_t par) { return __all_sync(0xffffffffu, wait_own(b, par)) != 0; };
     int gpc = 0;
     for (; ok && w.valid(); w.next(), ++gpc) {
-      if (!wait_u(bar(B_LRDY), gpc & 1)) { ok = false; break; }
+      // (all steps of the token's piece: 2^22 of them at the most, more than 10 s)
+      if (!__all_sync(0xffffffffu, wait_following(bar(B_LRDY), gpc & 1, steps))) { ok = false; break; }
       const float l = (stat[i] + stat[HC + i]) + (stat[2 * HC + i] + stat[3 * HC + i]);
       const float m = stat[4 * HC + i] * p.scale_log2 * 0.69314718055994531f;
       __syncwarp();

@@ -695,6 +695,28 @@ def test_attention_over_a_long_table_of_the_same_pages(mods, dtype, times):
     assert ((lse[0].double().cpu() - want).abs() <= gamma + 2.0 ** -18 + terms * 2.0 ** -23 + 2.0 ** -23 * want.abs()).all()
 
 
+def test_attention_over_pieces_that_take_seconds(mods):
+    """A token a pair, each over 3 * 2^26 rows, 1024 rows over and over: 786432 steps, of 4357 cycles at least (the MMAs'),
+    are 3.4e9 cycles, more than one wait may take. Nothing gives up, and the sums are those of all rows."""
+    m = mods["bf16"]
+    T, times = torch.cuda.get_device_properties(0).multi_processor_count // 2, 3 * 2 ** 16
+    c = Case("bf16", 64, [1024], [1], seed=70, spare=0, pad=T - 1)
+    n = 1024 * times
+    b = mla.PagedBatch(c.cache, c.d_table[:, :16].repeat(1, times), torch.tensor([0, T], device="cuda"),
+                       torch.tensor([n], device="cuda"), T)
+    o, lse = m.attn_paged(b, c.q_abs, c.q_rope)
+    ok(m)
+    assert torch.isfinite(o).all()
+    for t in (0, 1, T - 2, T - 1):
+        _, rl, _, gamma = c.attend(t, c.rows[0])
+        # the T - 1 - t rows that t does not see are part of one of the `times` rounds. A thread adds 786432 sums of 64
+        # weights, to partial sums that grow evenly to the whole; 2^-18 for the exponentials
+        rel = (n / 256 / 2 + 64) * 2.0 ** -23 + 2.0 ** -18 + 2.0 / times
+        want = rl + torch.tensor(float(times), dtype=torch.float64).log()
+        err = (lse[t].double().cpu() - want).abs()
+        assert (err <= gamma + rel + 2.0 ** -23 * want.abs()).all(), (t, float(err.max()))
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_calls_and_graphs_side_by_side_on_two_streams(mods, dtype):
     """The same calls of one handle on two streams at once, eager and as two graphs: as when they run alone."""
