@@ -394,7 +394,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Rows rows;
     rows.init(p, w, lane);
     int base = 0, bph = 1, turn = me;         // slot and parity of the block of entries at hand, this warp's first of it
-    int n = 0, last = -1;                     // ring index of the block, this warp's last entry
+    uint32_t n = 0, end = 0;                  // ring index of the block, behind this warp's last entry (2^32: 250 million steps)
     int gpc = 0;
     // waits for the slot of entry e of the block; false when it gave up
     auto ready = [&](int e, int* slot) -> bool {
@@ -424,7 +424,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int s = 0; s < 128 / GRAN; ++s) pair_load(dst + s * GRAN * 128, &p.kmap, 64 * e, y[s], b);
         }
         __syncwarp();
-        last = n + e;
+        end = n + e + 1;
       }
       leave(kEntriesK);
     };
@@ -460,7 +460,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (to_l2 >= 0 && elect_one())
           prefetch_l2(reinterpret_cast<const __nv_bfloat16*>(p.v.cache) + (int64_t)to_l2 * (DC + DR), 16 * (DC + DR) * 2);
         __syncwarp();
-        last = n + e;
+        end = n + e + 1;
       }
       leave(kEntriesV);
     };
@@ -482,7 +482,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // copies still in flight, those of the peer too (seen at the leader's barriers; a tail entry's bytes land
       // within the same waits)
       if (r == 0) {
-        for (int i = max(0, last - RING + 1); i <= last; ++i) wait_own(bar(B_FULL + i % RING), (i / RING) & 1);
+        for (uint32_t i = end > RING ? end - RING : 0; i < end; ++i) wait_own(bar(B_FULL + i % RING), (i / RING) & 1);
         if (me == 1 && gpc > 0) wait_own(bar(B_QFULL), (gpc - 1) & 1);
       }
     }
@@ -582,7 +582,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const float c2 = p.scale_log2, thr = kRescaleLog2 / c2;
     const uint32_t sfree = lead(B_SFREE), prdy = lead(B_PRDY), trdy = lead(B_TRDY);
     auto wait_u = [&](uint32_t b, uint32_t par) { return __all_sync(0xffffffffu, wait_own(b, par)) != 0; };
-    int js = 0, gpc = 0, tails = 0, nbase = 0;
+    int js = 0, gpc = 0, tails = 0, nbase = 0;               // nbase: slot of the token's first entry
     for (; ok && w.valid(); w.next(), ++gpc) {
       const int ns = w.steps();
       float m = -INFINITY, l = 0.f;
@@ -696,7 +696,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      nbase += (kEntriesK + kEntriesV) * ns;
+      nbase = (nbase + (kEntriesK + kEntriesV) * ns) % RING;
       if (!wait_u(bar(B_LFREE), (gpc & 1) ^ 1)) { ok = false; break; }
       stat[kq * HC + i] = l;
       if (kq == 0) stat[4 * HC + i] = m;
