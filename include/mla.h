@@ -428,6 +428,11 @@ mla_status_t mla_kernel_time_ms(int which, float *ms);
  * and later calls run normally. Not thread-safe: arm it only while no other thread launches. */
 void mla_test_arm_stall(void);
 
+/* The same for the paged calls on BF16 handles: arms the next launch of the paged attention core (mla_attn_paged,
+ * mla_attn_paged_sparse) or of the block scores (mla_paged_select), whichever comes first. The first pair of CTAs waits
+ * for queries, or the first CTA for codes, that are never loaded; the waits keep their limit of about 1 s. */
+void mla_test_arm_paged_stall(void);
+
 const char *mla_status_string(mla_status_t s);
 
 /* Frees the handle's own device memory (its error word). Borrowed tensors are untouched. */

@@ -3,10 +3,17 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "handle.cuh"
 #include "mla.h"
 #include "paged.cuh"
 #include "tc_paged.cuh"
+
+namespace mla {
+static std::atomic<bool> g_paged_stall{false};
+bool take_paged_stall() { return g_paged_stall.exchange(false, std::memory_order_relaxed); }
+}  // namespace mla
 
 namespace {
 
@@ -149,5 +156,7 @@ mla_status_t mla_paged_select(mla_handle_t* h, const mla_paged_t* batch, const v
   return cuda_status(mla::paged_select(v, tc_dims(h), q_abs, q_rope, summaries, top_k, n_first, n_last, blocks, ws,
                                        h->num_sms, h->d_err, (cudaStream_t)stream));
 }
+
+void mla_test_arm_paged_stall(void) { mla::g_paged_stall.store(true, std::memory_order_relaxed); }
 
 }  // extern "C"

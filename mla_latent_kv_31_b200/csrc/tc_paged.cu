@@ -121,6 +121,7 @@ struct CoreParams {
   float2* part_ml;            // [2 * pairs][H]: maximum (natural units), sum
   float scale_log2;
   uint32_t* err;
+  int32_t stall;              // test hook: the first pair's leader leaves out its first token's queries
 };
 
 // ---- pairs of CTAs ------------------------------------------------------------------------------------------
@@ -385,8 +386,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (ok && elect_one()) {
         if (r == 0) mbar_expect_tx(bar(B_QFULL), 2 * Q_BYTES);
         const int32_t y = w.id * H + HC * (int)r;
-        for (int c = 0; c < 8; ++c) pair_load(sbase + OFF_Q + c * BOX, &p.qmap, 64 * c, y, lead(B_QFULL));
-        pair_load(sbase + OFF_Q + 8 * BOX, &p.qrmap, 0, y, lead(B_QFULL));
+        if (!(p.stall && pair == 0 && r == 0 && g == 0)) {
+          for (int c = 0; c < 8; ++c) pair_load(sbase + OFF_Q + c * BOX, &p.qmap, 64 * c, y, lead(B_QFULL));
+          pair_load(sbase + OFF_Q + 8 * BOX, &p.qrmap, 0, y, lead(B_QFULL));
+        }
       }
       __syncwarp();
     };
@@ -1186,6 +1189,7 @@ cudaError_t tc_paged_attention(const PagedView& v, const void* q_abs, const void
   p.part_ml = s.part_ml;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.err = err;
+  p.stall = take_paged_stall();
   PlanParams pp;
   pp.v = v;
   pp.blocks = blocks;

@@ -14,6 +14,9 @@ cudaError_t tc_paged_attention(const PagedView& v, const void* q_abs, const void
                                int32_t top_k, float scale, void* o_lat, float* lse, void* ws, int num_sms, uint32_t* err,
                                cudaStream_t st);
 
+// Whether mla_test_arm_paged_stall armed this launch; the next one is not.
+bool take_paged_stall();
+
 // Scores [T, max_pages] fp32 (at the start of ws) of the blocks that each new token sees, for the tokens with more than
 // top_k of them; ws: tc_select_bytes().
 size_t tc_select_bytes(int64_t total_q, int64_t max_pages);

@@ -194,6 +194,7 @@ struct ScoreParams {
   int32_t top_k, group;       // tokens per CTA
   float* scores;              // [T, max_pages]
   uint32_t* err;
+  int32_t stall;              // test hook: the first CTA leaves out its first box of codes
 };
 
 __global__ void __launch_bounds__(kThreads, 1) select_score_kernel(const __grid_constant__ ScoreParams p) {
@@ -278,7 +279,8 @@ __global__ void __launch_bounds__(kThreads, 1) select_score_kernel(const __grid_
           if (!ok) break;
           if (elect_one()) {
             mbar_expect_tx(bar(B_FULL + slot), KBOX);
-            tma_load_2d(sbase + OFF_RING + slot * KBOX, &p.qmap, 128 * e, (int32_t)((from + k) * H), bar(B_FULL + slot));
+            if (!(p.stall && n == 0 && blockIdx.x == 0 && blockIdx.y == 0))
+              tma_load_2d(sbase + OFF_RING + slot * KBOX, &p.qmap, 128 * e, (int32_t)((from + k) * H), bar(B_FULL + slot));
           }
           __syncwarp();
         }
@@ -400,6 +402,7 @@ cudaError_t tc_select_scores(const PagedView& v, const void* q_abs, const void* 
   p.pitch = (int64_t)summary_pitch(DC, DR);
   p.top_k = top_k;
   p.err = err;
+  p.stall = take_paged_stall();
   // one CTA an SM and about two rounds of them: more tokens a CTA gather a tile's summaries less often (512 tokens x 512
   // blocks: 3 rounds 89 us, 2 rounds 80, 1 round 79), fewer balance tiles behind a sequence's end and single tokens of
   // many sequences (64 x 1 over 512 blocks: 2 rounds 37, 1 round 41)

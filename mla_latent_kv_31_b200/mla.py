@@ -100,6 +100,7 @@ def lib() -> ctypes.CDLL:
             "mla_kernel_time_ms": (c_int, [c_int, POINTER(ctypes.c_float)]),
             "mla_status_string": (c_char_p, [c_int]),
             "mla_test_arm_stall": (None, []),
+            "mla_test_arm_paged_stall": (None, []),
             "mla_destroy": (None, [H]),
         }
         for name, (res, args) in sigs.items():
@@ -351,6 +352,11 @@ def mla_kernel_time_ms(which: int) -> float:
 def mla_test_arm_stall():
     """Arms the next decode latent-core launch to give up on a wait nothing signals (20 ms limit)."""
     lib().mla_test_arm_stall()
+
+
+def mla_test_arm_paged_stall():
+    """Arms the next launch of the paged attention core or of the block scores to give up on a wait (about 1 s)."""
+    lib().mla_test_arm_paged_stall()
 
 
 def mla_kernel_launches() -> int:

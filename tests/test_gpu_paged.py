@@ -229,6 +229,26 @@ def test_calls_take_every_name_of_their_device(mods):
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_runs(mods):
+    """Queries of the attention core, then codes of the block scores, that are never loaded: every role gives up, the
+    status says so, and the same call gives its usual results afterwards."""
+    m = mods["bf16"]
+    c = Case("bf16", 16, [3000, 700, 40], [2, 1, 3], seed=71)
+    b, qa, qr, sums = c.batch(), c.q_abs, c.q_rope, c.summaries(c.normal(c.num_pages, c.W)).cuda()
+    blocks = m.paged_select(b, qa, qr, sums, 8, 1, 1)
+    calls = [lambda: m.attn_paged(b, qa, qr), lambda: m.attn_paged_sparse(b, qa, qr, blocks),
+             lambda: (m.paged_select(b, qa, qr, sums, 8, 1, 1),)]
+    for call in calls:
+        want = [x.clone() for x in call()]
+        ok(m)
+        mla.mla_test_arm_paged_stall()
+        call()
+        assert m.sync_status() == 6 and mla.mla_device_error_bits(m.handle) == 1 << 6
+        got = call()
+        ok(m)
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_flagged_batches_give_empty_rows(mods, dtype):
     m = mods[dtype]
