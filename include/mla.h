@@ -354,7 +354,8 @@ mla_status_t mla_paged_summary_bytes(const mla_handle_t *h, size_t *bytes);
  *   q_out      [total_q, n_h, d_r]   handle dtype, R_pos q; may be q_rope itself; NULL with q_rope
  *   summaries  [num_pages] rows of mla_paged_summary_bytes(); NULL: none. For every page that the
  *              new tokens complete (its last row is one of them), its summary: the mean of its rows
- *              (sums in fp64, one rounding to fp32), x / scale rounded to the nearest whole number (ties
+ *              (sums in fp64, in an order that the page size fixes,
+ *              one rounding to fp32), x / scale rounded to the nearest whole number (ties
  *              to even) in -127 .. 127, scale = max|x| / 127 (a row of scale 0, inf or NaN: all zero). */
 mla_status_t mla_paged_append(mla_handle_t *h, const mla_paged_t *batch, const void *kv, int64_t kv_stride,
                               const void *q_rope, void *q_out, void *summaries, mla_stream_t stream);

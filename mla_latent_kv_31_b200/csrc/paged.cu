@@ -168,7 +168,9 @@ __device__ __forceinline__ int code_of(float x, float s) {
 // Summaries of the pages that the new tokens complete. Block i looks at `group` <= 32 tokens, a lane each; a token that is
 // its page's last row stands for the page. The lookups come before the wait for the append's rows. Four groups of
 // threads take a quarter of the rows each (page sizes are multiples of 16), 16 of them in flight; their sums meet in
-// shared memory. The sums are in double: of bf16 values they are exact, so the summary does not depend on the order.
+// shared memory. The sums are in double and in a fixed order: a quarter's rows one after the other, then the quarters. Of
+// bf16 values they are exact, and so free of the order, where a column's values span fewer than 45 - log2(page size)
+// binades (53 bits of a double, 8 of a value), which rows of a latent cache do.
 constexpr int SUM_GROUPS = 4;
 template <typename T>
 __global__ void __launch_bounds__(512) summarise_kernel(PagedView v, int group, uint8_t* summaries, int64_t pitch) {

@@ -1,5 +1,7 @@
 """The paged latent cache on the GPU against its float64 form: ragged batches, pages that end inside a tile, NaN in
 every row that must not matter, padded batches, lists of blocks, captured and replayed steps."""
+import math
+
 import pytest
 import torch
 
@@ -424,6 +426,34 @@ def test_append_flags_bad_pages_and_writes_nothing_for_them(mods, dtype):
     i = torch.int16 if dtype == "bf16" else torch.int32
     changed = (c.cache.view(i) != before.view(i)).flatten(1).any(1).nonzero().flatten().tolist()
     assert changed == sorted([page2, int(c.table[1, 1])])
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("page", [16, 48, 64, 256])
+def test_summaries_of_values_far_apart(mods, dtype, page):
+    """Rows whose values span 120 binades, half of them cancelled by their negatives: sums that a double rounds."""
+    m = mods[dtype]
+    c = Case(dtype, page, [page], [1], seed=24)
+    d = c.dims
+    x = c.normal(page, c.W) * 2.0 ** (torch.randint(-60, 61, (page, c.W), generator=c.g).double())
+    x[page // 2:page - page // 4] = -x[:page // 4]
+    x = x.to(DT[dtype])
+    p = int(c.table[0, 0])
+    c.cache[p] = x.cuda()
+    sums = m.new_summaries(c.num_pages)
+    m.paged_append(c.batch(), c.on(x[-1:].double()), summaries=sums)
+    ok(m)
+    rows = c.cache[p].double().cpu()                       # (the last row's rotary part has been turned)
+    mean = torch.tensor([math.fsum(col) / page for col in rows.T.tolist()], dtype=torch.float64)
+    # page additions in 53 bits, the division and the rounding to fp32 (half a step each)
+    off = page * 2.0 ** -53 * rows.abs().sum(0) / page + (2.0 ** -53 + 2.0 ** -24) * mean.abs()
+    out = sums[p].cpu()
+    codes, scale = out[:c.W].view(torch.int8).double(), float(out[c.W:c.W + 4].view(torch.float32))
+    big = float(mean.abs().max())
+    assert abs(scale - big / 127) <= (float(off.max()) + 2.0 ** -24 * big) / 127 * (1 + 2.0 ** -20)
+    # the nearest whole number of scales, the division off by half a step of a quotient of up to 127
+    assert ((codes * scale - mean).abs() <= scale / 2 + off + 128 * 2.0 ** -24 * scale).all()
+    assert codes.abs().max() == 127
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
