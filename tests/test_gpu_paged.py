@@ -429,6 +429,22 @@ def test_append_flags_bad_pages_and_writes_nothing_for_them(mods, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("lens,tq,pad", [([33, 20], [2, 1], 1), ([64, 5, 300], [64, 0, 7], 40), ([1], [1], 299)])
+def test_append_leaves_query_rows_behind_the_last_sequence(mods, dtype, in_place, lens, tq, pad):
+    m = mods[dtype]
+    c = Case(dtype, 16, lens, tq, seed=25, pad=pad)
+    qd = c.q_rope
+    out = qd if in_place else torch.full_like(qd, 7.0)
+    before = out.clone()
+    m.paged_append(c.batch(), c.on(c.normal(c.T + pad, c.W)), q_rope=qd, q_out=out, summaries=m.new_summaries(c.num_pages))
+    ok(m)
+    assert torch.equal(out[c.T:], before[c.T:])
+    last = c.tokens()[-1][0]
+    assert c.tokens()[-1][2] == 0 or not torch.equal(out[last], before[last])       # (position 0 is not turned)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("page", [16, 48, 64, 256])
 def test_summaries_of_values_far_apart(mods, dtype, page):
     """Rows whose values span 120 binades, half of them cancelled by their negatives: sums that a double rounds."""
