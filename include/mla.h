@@ -322,7 +322,8 @@ mla_status_t mla_attn_prefill(mla_handle_t *h, const void *q_c, const void *q_ro
  * an offending sequence is not appended, and its outputs are zero, with lse = -inf and no blocks; a
  * page outside the pool is read as zero rows.
  * The handle's cache format must be MLA_CACHE_BF16 (MLA_ERR_UNSUPPORTED otherwise); page_size is a
- * multiple of 16, num_pages * page_size < 2^31 and max_pages * page_size <= 2^30. A handle without
+ * multiple of 16, num_pages * page_size < 2^31 and max_pages * page_size <= 2^30, 1 <= B <= 2^20 and
+ * 1 <= total_q < 2^31 / n_h (a step without new tokens passes a row that cu_q[B] = 0 leaves alone). A handle without
  * weights serves these calls; its first call allocates the error word, so it must not be part of a
  * stream capture. A workspace belongs to one call at a time: calls, and captured graphs, that may run
  * at the same time need one each. */

@@ -28,15 +28,17 @@ using mla::tc_dims;
 constexpr int64_t kMaxRows = INT32_MAX;
 constexpr int64_t kMaxLen = 1 << 30;         // rows of a sequence: 32-bit key numbers with room for a step
 constexpr int64_t kMaxSelectTokens = 65535;  // a grid's second dimension
+constexpr int64_t kMaxSeqs = 1 << 20;
+constexpr int32_t kMinPage = 16;
 
 // The host checks that every paged call shares; on MLA_OK *v describes the batch.
 mla_status_t view_of(const mla_handle_t* h, const mla_paged_t* b, PagedView* v) {
   if (!h || !b) return MLA_ERR_INVALID_ARG;
   if (h->opts.cache_fp8) return MLA_ERR_UNSUPPORTED;
   if (!b->cache || !b->block_table || !b->cu_q || !b->kv_lens || b->B <= 0 || b->total_q <= 0 || b->num_pages <= 0 ||
-      b->max_pages <= 0 || b->table_stride < b->max_pages || b->page_size <= 0 || b->page_size % 16 != 0)
+      b->max_pages <= 0 || b->table_stride < b->max_pages || b->page_size <= 0 || b->page_size % kMinPage != 0)
     return MLA_ERR_INVALID_ARG;
-  if (b->num_pages > kMaxRows / b->page_size || b->max_pages > kMaxLen / b->page_size || b->B > (1 << 20) ||
+  if (b->num_pages > kMaxRows / b->page_size || b->max_pages > kMaxLen / b->page_size || b->B > kMaxSeqs ||
       b->total_q > kMaxRows / h->dims.n_h)
     return MLA_ERR_INVALID_ARG;
   if (!aligned16(b->cache) || !aligned16(b->block_table) || !aligned16(b->cu_q) || !aligned16(b->kv_lens))
@@ -111,7 +113,7 @@ mla_status_t mla_paged_append(mla_handle_t* h, const mla_paged_t* batch, const v
 }
 
 mla_status_t mla_attn_paged_workspace(const mla_handle_t* h, int64_t B, int64_t total_q, size_t* bytes) {
-  if (!h || !bytes || B <= 0 || total_q <= 0) return MLA_ERR_INVALID_ARG;
+  if (!h || !bytes || B <= 0 || B > kMaxSeqs || total_q <= 0 || total_q > kMaxRows / h->dims.n_h) return MLA_ERR_INVALID_ARG;
   *bytes = tc_dims(h) ? mla::tc_paged_attention_bytes(total_q) : 0;
   return MLA_OK;
 }
@@ -130,7 +132,8 @@ mla_status_t mla_attn_paged_sparse(mla_handle_t* h, const mla_paged_t* batch, co
 }
 
 mla_status_t mla_paged_select_workspace(const mla_handle_t* h, int64_t total_q, int64_t max_pages, size_t* bytes) {
-  if (!h || !bytes || total_q <= 0 || max_pages <= 0) return MLA_ERR_INVALID_ARG;
+  if (!h || !bytes || total_q <= 0 || total_q > kMaxSelectTokens || max_pages <= 0 || max_pages > kMaxLen / kMinPage)
+    return MLA_ERR_INVALID_ARG;
   *bytes = mla::paged_select_bytes(tc_dims(h), h->dims.n_h, h->dims.d_c, h->dims.d_r, total_q, max_pages);
   return MLA_OK;
 }

@@ -120,6 +120,15 @@ def test_workspaces_and_summary_rows():
             for x, y in ((0, 1), (1, 0), (-1, 1)):
                 with pytest.raises(mla.MLAError):
                     f(h, x, y)
+        n, r = synth.V3.n_h, 2 ** 31 - 1
+        assert mla.mla_attn_paged_workspace(h, 1 << 20, r // n) > r // n * 16
+        assert mla.mla_paged_select_workspace(h, 65535, 1 << 26) > 65535 << 28
+        for f, x, y in ((mla.mla_attn_paged_workspace, 1, r // n + 1), (mla.mla_attn_paged_workspace, (1 << 20) + 1, 1),
+                        (mla.mla_attn_paged_workspace, 1, 1 << 60), (mla.mla_paged_select_workspace, 65536, 1),
+                        (mla.mla_paged_select_workspace, 1, (1 << 26) + 1), (mla.mla_paged_select_workspace, 1 << 62, 1 << 62)):
+            with pytest.raises(mla.MLAError) as e:      # sizes that no call takes: their bytes would wrap around
+                f(h, x, y)
+            assert e.value.status == INVALID
         small, large = (mla.mla_paged_select_workspace(h, 4, n) for n in (10, 2000))
         assert 4 * 2000 * 4 <= large and small < large
     finally:
