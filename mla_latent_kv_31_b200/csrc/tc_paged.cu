@@ -12,12 +12,15 @@
 // 36 and 32 MMAs of N = 256. (An M = 128 pair MMA of K = 16 takes 64 cycles at N = 256, 32 at N = 128, measured: 4357 a
 // step. The loads take about 4200 of 66 bytes a cycle and SM. With both under way a step takes 7000 to 8000.)
 //
-// What it reaches. 512 tokens of one sequence behind 32768 rows: 1540 TFLOP/s; 8 x 64 behind 16384 rows 1270 to 1400 (1.65
-// to 1.8 ms), 64 x 4 behind 8192 rows 1230, 64 x 2 behind 16896 1190 (0.51 ms), the rows read once from HBM; 4 single
-// tokens over 131072 rows 4.0 TB/s (150 us), 16 over 4096 rows 39 us: there the chain plan - first rows - last partial -
-// merge takes half of the time. Where rows come from L2 a step takes 4600 cycles, MMAs and loads both near their rates;
-// where they come from HBM 6500 to 8000 and no unit is at its limit: the ring of 112 KB, which cannot grow, holds what is
-// on its way for 2 us or so.
+// What it reaches, in bursts of ten calls at 1965 MHz (a graph; under the power cap of a long row 8 to 20 % less). 512
+// tokens of one sequence behind 32768 rows: 1520 TFLOP/s; 8 x 64 behind 16384 rows 1470 (1.59 ms), 64 x 4 behind 8192 rows
+// 1200, 64 x 2 behind 16896 1155 (0.52 ms), the rows read once from HBM; 4 single tokens over 131072 rows 4.1 TB/s
+// (148 us), 16 over 4096 rows 38 us: there the chain plan - first rows - last partial - merge takes half of the time.
+// Where rows come from L2 a step takes 4600 cycles, MMAs and loads both near their rates. Where they come from HBM it
+// takes 6500 to 8000. Single tokens share no rows, so there the bytes bound a step: 74 pairs x 256 rows x 1152 B at the
+// 6.46 TB/s of a copy are 3.4 us, 6500 cycles at 1.92 GHz. Rows that several pairs share need fewer bytes a step and no
+// unit is at its limit; how much of either is time in which a pair has too few rows on their way (its ring of 112 KB, and
+// the fetches to L2, which go out beside the values only) has not been measured step by step.
 // Measured and not kept: a ring and an issuing warp each for K and V (1184 -> 1041 TFLOP/s), waits for several entries at
 // once (0 to 8 % slower), P handed over 64 keys at a time (5 % slower: each wait and commit of the MMA warp counts),
 // 64 score columns a thread in registers (the same time, 128 registers instead of 94).
