@@ -655,10 +655,8 @@ mla_status_t mla_sync_status(mla_handle_t* h, mla_stream_t stream) {
   if (!h->d_err) return MLA_OK;
   DeviceGuard g(h->device);
   if (!g.ok) return MLA_ERR_CUDA;
-  MLA_TRY(cudaStreamSynchronize((cudaStream_t)stream));
   uint32_t bits = 0;
-  MLA_TRY(cudaMemcpy(&bits, h->d_err, sizeof(bits), cudaMemcpyDeviceToHost));
-  MLA_TRY(cudaMemset(h->d_err, 0, sizeof(uint32_t)));
+  MLA_TRY(mla::take_error_bits(h, (cudaStream_t)stream, &bits));
   h->last_err_bits = bits;
   if (bits & mla::DEVERR_TIMEOUT) return MLA_ERR_TIMEOUT;
   if (bits) return MLA_ERR_DEVICE_CHECK;

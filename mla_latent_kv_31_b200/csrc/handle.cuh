@@ -89,4 +89,14 @@ inline mla_status_t ensure_device(mla_handle* h) {
   return MLA_OK;
 }
 
+// Waits for the stream, then reads and clears the error word. The clearing is waited for too (cudaMemset is asynchronous):
+// a launch on any stream after it finds the word at zero, and what it flags stays.
+inline cudaError_t take_error_bits(mla_handle* h, cudaStream_t stream, uint32_t* bits) {
+  cudaError_t e = cudaStreamSynchronize(stream);
+  if (e == cudaSuccess) e = cudaMemcpy(bits, h->d_err, sizeof(uint32_t), cudaMemcpyDeviceToHost);
+  if (e == cudaSuccess) e = cudaMemset(h->d_err, 0, sizeof(uint32_t));
+  if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);
+  return e;
+}
+
 }  // namespace mla

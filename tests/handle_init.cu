@@ -1,6 +1,6 @@
 // The first call of a handle (ensure_device, csrc/handle.cuh) over a stand-in for the CUDA runtime: no GPU and no
 // cudart, host code only. Threads that make it at once all find the handle ready, a failure of any runtime call leaves
-// nothing behind, and the next call tries again. "ok" and exit status 0 on success. Built and run by
+// nothing behind, and the next call tries again; reading the error word clears it for good. "ok" and exit status 0 on success. Built and run by
 // tests/test_paged_host.py.
 #include <stdio.h>
 #include <stdlib.h>
@@ -70,6 +70,11 @@ CALL cudaDeviceGetAttribute(int* v, cudaDeviceAttr, int) {
   *v = 148;
   return cudaSuccess;
 }
+CALL cudaMemcpy(void* to, const void* from, size_t n, cudaMemcpyKind) {
+  if (!works()) return cudaErrorUnknown;
+  memcpy(to, from, n);
+  return cudaSuccess;
+}
 CALL cudaGetDevice(int* d) { *d = 0; return cudaSuccess; }
 CALL cudaSetDevice(int) { return cudaSuccess; }
 // What the compiler's start-up code calls for a program with device code; this one launches none.
@@ -105,6 +110,17 @@ int main() {
     for (auto& t : threads) t.join();
     CHECK(1, wrong == 0);
     CHECK(2, g_mallocs == 1);
+    cudaFree(h.d_err);
+  }
+  // reading the error word leaves it at zero, with no clearing on its way behind the call
+  {
+    mla_handle h;
+    memset(&h, 0, sizeof(h));
+    CHECK(8, mla::ensure_device(&h) == MLA_OK);
+    *h.d_err = 5;
+    uint32_t bits = 0;
+    CHECK(9, mla::take_error_bits(&h, nullptr, &bits) == cudaSuccess && bits == 5);
+    CHECK(10, *h.d_err == 0 && !g_pending);
     cudaFree(h.d_err);
   }
   // each runtime call fails once
