@@ -1,6 +1,8 @@
 """The paged latent cache on the GPU against its float64 form: ragged batches, pages that end inside a tile, NaN in
 every row that must not matter, padded batches, lists of blocks, captured and replayed steps."""
+import concurrent.futures
 import math
+import threading
 
 import pytest
 import torch
@@ -229,6 +231,95 @@ def test_calls_take_every_name_of_their_device(mods):
             mla.mla_attn_paged(m.handle, b, qa, qr, o2, lse2, ws, n, device=device)
         assert mla.mla_sync_status(m.handle, s, device=device) == 0
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def in_fresh_thread(f):
+    """f() in a thread that has made no CUDA call before."""
+    with concurrent.futures.ThreadPoolExecutor(1) as pool:
+        return pool.submit(f).result()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_calls_from_a_thread_without_cuda_calls_before(mods, dtype):
+    """A handle that is ready, and a thread in which the call is the first to need the device's context."""
+    m = mods[dtype]
+    c = Case(dtype, 16, [700, 64], [2, 1], seed=72)
+    d, b, qa, qr, kv = c.dims, c.batch(), c.q_abs, c.q_rope, c.on(c.normal(c.T, c.W))
+    sums = c.summaries(c.normal(c.num_pages, c.W)).cuda()
+    o, lse, out, blocks = torch.empty_like(qa), torch.empty(c.T, d.n_h, device="cuda"), torch.empty_like(qr), \
+        torch.empty(c.T, 6, dtype=torch.int32, device="cuda")
+    n = max(mla.mla_attn_paged_workspace(m.handle, 2, 3), mla.mla_paged_select_workspace(m.handle, 3, b.max_pages))
+    ws, stream = torch.empty(n, dtype=torch.uint8, device="cuda"), torch.cuda.current_stream().cuda_stream
+    calls = [lambda: mla.mla_paged_append(m.handle, b, kv, c.W, qr, out, sums, stream),
+             lambda: mla.mla_paged_select(m.handle, b, qa, qr, sums, 6, 1, 1, blocks, ws, n, stream),
+             lambda: mla.mla_attn_paged_sparse(m.handle, b, qa, qr, blocks, 6, o, lse, ws, n, stream),
+             lambda: mla.mla_attn_paged(m.handle, b, qa, qr, o, lse, ws, n, stream)]
+    for call in calls:
+        call()
+        ok(m)
+        outs = {0: [out], 1: [blocks], 2: [o, lse], 3: [o, lse]}[calls.index(call)]
+        want = [x.clone() for x in outs]
+        for x in outs:
+            x.zero_()
+        in_fresh_thread(call)
+        ok(m)
+        assert all(torch.equal(x, y) for x, y in zip(outs, want))
+
+
+def test_layer_calls_from_a_thread_without_cuda_calls_before():
+    """The same for the layer's append and decode, whose first step is a projection."""
+    d, g = synth.V3, torch.Generator(device="cuda").manual_seed(73)
+
+    def normal(*shape):
+        return (torch.randn(*shape, generator=g, device="cuda") * shape[-1] ** -0.5).bfloat16()
+
+    w = {"w_dq": normal(d.d_cq, d.d), "w_uq": normal(d.n_h * d.d_h, d.d_cq), "w_qr": normal(d.n_h * d.d_r, d.d_cq),
+         "w_dkv": normal(d.d_c, d.d), "w_kr": normal(d.d_r, d.d), "w_uk": normal(d.n_h * d.d_h, d.d_c),
+         "w_uv": normal(d.n_h * d.d_h, d.d_c), "w_o": normal(d.d, d.n_h * d.d_h)}
+    m = mla.MLA(d, w)
+    stream = torch.cuda.current_stream().cuda_stream
+    h, cache, u = normal(2, d.d) * d.d ** 0.5, torch.zeros(2, d.d_c + d.d_r, dtype=torch.bfloat16, device="cuda"), normal(2, d.d)
+    at = torch.zeros(2, dtype=torch.int64, device="cuda"), torch.arange(2, device="cuda")
+    cu = torch.tensor([0, 1, 2], device="cuda")
+    na, nd = mla.mla_workspace_size(m.handle, mla.OP_CACHE_APPEND, 0, 1, 2), mla.mla_workspace_size(m.handle, mla.OP_DECODE, 2, 1)
+    ws = torch.empty(max(na, nd), dtype=torch.uint8, device="cuda")
+    calls = [(lambda: mla.mla_cache_append(m.handle, h, *at, 2, cache, 2, ws, na, stream), cache),
+             (lambda: mla.mla_decode(m.handle, h, 2, 1, cu, cache, 2, u, ws, nd, stream), u)]
+    for call, out in calls:
+        call()
+        ok(m)
+        want = out.clone()
+        out.zero_()
+        in_fresh_thread(call)
+        ok(m)
+        assert torch.equal(out, want)
+    m.close()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_first_calls_of_a_handle_from_several_threads(dtype):
+    """Threads that make a handle's first calls at once, each on a stream of its own: as when they come one by one."""
+    cases = [Case(dtype, 16, [300 + 90 * k, 20], [2, 1], seed=80 + k) for k in range(6)]
+    jobs = [(c.batch(), c.q_abs, c.q_rope, c.summaries(c.normal(c.num_pages, c.W)).cuda(), torch.cuda.Stream()) for c in cases]
+
+    def run(m, b, qa, qr, sums, s):
+        with torch.cuda.stream(s):
+            blocks = m.paged_select(b, qa, qr, sums, 6, 1, 1)
+            return blocks, *m.attn_paged_sparse(b, qa, qr, blocks), *m.attn_paged(b, qa, qr)
+
+    torch.cuda.synchronize()
+    one, all_at_once = handle(dtype), handle(dtype)
+    want = [run(one, *job) for job in jobs]
+    ok(one)
+    gate = threading.Barrier(len(jobs))
+    with concurrent.futures.ThreadPoolExecutor(len(jobs)) as pool:
+        got = list(pool.map(lambda job: (gate.wait(), run(all_at_once, *job))[1], jobs))
+    torch.cuda.synchronize()
+    ok(all_at_once)
+    for x, y in zip(got, want):
+        assert all(torch.equal(a, b) for a, b in zip(x, y))
+    one.close()
+    all_at_once.close()
 
 
 def test_a_wait_that_runs_out_is_reported_and_the_next_call_runs(mods):
